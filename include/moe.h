@@ -157,7 +157,7 @@ int32_t moe_capacity(int32_t T, int32_t k, int32_t E, int32_t phi_num, int32_t p
 int64_t moe_max_rows(const moe_config* cfg);
 
 /* Bytes of workspace that moe_forward needs (it keeps every intermediate there); the
- * staged calls need only the leading scratch part, which this also covers.
+ * staged calls and moe_forward_few are covered too.
  * Returns 0 for an invalid config.                                                      */
 size_t moe_workspace_bytes(const moe_config* cfg);
 
@@ -250,6 +250,32 @@ moe_status moe_forward(const moe_config* cfg, const void* x, const void* w_route
                        const void* shared_down, void* y, int32_t* ids_out, float* gates_out,
                        int32_t* demand_out, int32_t* offsets_out, void* ws,
                        moe_stream_t stream);
+
+/* moe_forward for a few tokens (decode): the whole layer in ONE kernel, for T <= 32.  The
+ * same inputs, outputs and routing as moe_forward, and outputs within the same tolerance (the
+ * gate is folded into H before H is rounded to dtype, and the sum over a token's experts
+ * stays in fp32).  Demand and offsets are those of the RAGGED layout.
+ *   n_tokens    device int32 or NULL.  Rows 0 .. *n_tokens - 1 of x hold tokens (the value is
+ *               clamped to 0..T; NULL: all T): a batch padded to a captured T.  Rows behind
+ *               them take no part in the routing and are left as they were in y, ids_out
+ *               and gates_out.
+ *   capacity    as in moe_dispatch: a route past its expert's first C tokens is dropped.
+ *   Masks       a logit_bias of -inf keeps an expert from being chosen while k others are
+ *               left; a route chosen at a logit of -inf (or NaN, which ranks as -inf) has
+ *               gate 0, and a token with no other logit has only zero gates, so its routed
+ *               part is zero.
+ *   y           may be x itself.
+ * cfg->tiles is ignored.  MOE_ERR_UNSUPPORTED: T > 32, stats, the padded layout, the reroute
+ * policy, fused steps.  MOE_ERR_INVALID also for x or weights that are not 16-byte aligned.
+ * The kernel occupies every SM (a cooperative launch) and can be captured into a graph.  If
+ * it ever reports MOE_ERR_TIMEOUT, call moe_workspace_init before the workspace's next use.
+ * Source: "271,104 Routes...", section 5 (with small batches the cost is moving weights). */
+moe_status moe_forward_few(const moe_config* cfg, const void* x, const void* w_router,
+                           const float* logit_bias, const void* w_gate, const void* w_up,
+                           const void* w_down, const void* shared_gate, const void* shared_up,
+                           const void* shared_down, void* y, int32_t* ids_out, float* gates_out,
+                           int32_t* demand_out, int32_t* offsets_out, const int32_t* n_tokens,
+                           void* ws, moe_stream_t stream);
 
 /* moe_forward that also records caller-created CUDA events (cudaEvent_t handles, e.g.
  * created with timing enabled) on `stream` around its kernels, for live per-kernel timing:

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "internal.h"
@@ -124,6 +125,13 @@ moe_status check_ws(const void* ws) {
 template <typename P>
 uint8_t* at(P* base, size_t off) {
   return reinterpret_cast<uint8_t*>(const_cast<void*>(static_cast<const void*>(base))) + off;
+}
+
+// Rows read by 16-byte loads and bulk copies.
+bool aligned16(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return false;
+  return true;
 }
 
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -253,7 +261,8 @@ int64_t moe_max_rows(const moe_config* cfg) {
 
 size_t moe_workspace_bytes(const moe_config* cfg) {
   if (validate(cfg) != MOE_OK) return 0;
-  return layout_of(*cfg).total;
+  const size_t total = layout_of(*cfg).total;
+  return few_layer_supported(*cfg) ? std::max(total, few_layer_layout(*cfg).total) : total;
 }
 
 moe_status moe_workspace_init(void* ws, moe_stream_t stream) {
@@ -333,6 +342,24 @@ moe_status moe_forward(const moe_config* cfg, const void* x, const void* w_route
   return forward_impl(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, shared_gate, shared_up,
                       shared_down, y, ids_out, gates_out, demand_out, offsets_out, nullptr, 0,
                       ws, stream);
+}
+
+moe_status moe_forward_few(const moe_config* cfg, const void* x, const void* w_router,
+                           const float* logit_bias, const void* w_gate, const void* w_up,
+                           const void* w_down, const void* shared_gate, const void* shared_up,
+                           const void* shared_down, void* y, int32_t* ids_out, float* gates_out,
+                           int32_t* demand_out, int32_t* offsets_out, const int32_t* n_tokens,
+                           void* ws, moe_stream_t stream) {
+  MOE_TRY(validate(cfg));
+  MOE_TRY(check_ws(ws));
+  if (!few_layer_supported(*cfg)) return MOE_ERR_UNSUPPORTED;
+  if (!x || !w_router || !w_gate || !w_up || !w_down || !y) return MOE_ERR_INVALID;
+  if (cfg->has_shared && (!shared_gate || !shared_up || !shared_down)) return MOE_ERR_INVALID;
+  if (!aligned16({x, w_router, w_gate, w_up, w_down, shared_gate, shared_up, shared_down}))
+    return MOE_ERR_INVALID;
+  const FewArgs a{x, w_router, logit_bias, w_gate, w_up, w_down, shared_gate, shared_up,
+                  shared_down, y, ids_out, gates_out, demand_out, offsets_out, n_tokens};
+  return cuda_status(launch_few_layer(*cfg, a, ws, stream));
 }
 
 moe_status moe_forward_profiled(const moe_config* cfg, const void* x, const void* w_router,

@@ -22,6 +22,8 @@ constexpr size_t kWsStatsCounterOffset = 64;
 // Byte offset, in the header, of the ticket counter of the dispatch prep (the CTA that
 // writes the last tile of the expert histogram turns it into prefixes and offsets).
 constexpr size_t kWsPrepCounterOffset = 128;
+// Byte offset, in the header, of the two words of the few-token kernels' grid barrier.
+constexpr size_t kWsGridSyncOffset = 192;
 
 // A route (t, j) is valid if its expert id is in range and not repeated earlier in the
 // token's row of ids.
@@ -181,6 +183,24 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// A cooperative launch: all CTAs are resident at the same time, so they may wait for each
+// other.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                      size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -1,0 +1,510 @@
+// The whole MoE layer for at most 32 tokens in one kernel (moe_forward_few).
+//
+//   z = x W_r^T + bias; ids, g = top-k; H'[t,e] = g (SiLU(x_t Wg_e^T) * (x_t Wu_e^T));
+//   y[t] = sum_e H'[t,e] Wd_e^T (+ shared expert) (+ x_t)
+// Sources: "271,104 Routes: What I Missed About Mixture-of-Experts", sections 1-3 (the layer),
+// section 5 (with small batches the cost is moving the weights); "MoE Inference Visualized",
+// Expert Execution.
+//
+// With few tokens the layer is bound by reading each touched expert's 3 d F weights once.
+// The five launches of moe_forward each pay a ramp and a tail there, and the padding of
+// their tiles; here one cooperative kernel runs three phases over the streaming engine of
+// few_stream.cuh, with two grid barriers between them:
+//   router   one warp per (expert, up to 4 tokens) dot product, spread over all CTAs.
+//   -- barrier --  every CTA selects the top-k for all tokens itself (T * k <= 1024 routes)
+//                  and builds the same tables: per expert a 32-bit mask of its tokens.
+//   gate/up  (touched experts x F) rows, cut evenly over the CTAs; a tile is up to 16 gate
+//            rows with their 16 up rows, against the expert's own tokens only.
+//   -- barrier --  meanwhile the producer already streams W_down into the ring; only the
+//                  H rows of those slots wait for the barrier.
+//   down     d output rows, cut evenly over the CTAs; each CTA runs all touched experts'
+//            columns for its rows, so the k-way combine is the contraction itself: the gate
+//            is folded into H before it is rounded to the storage type (one rounding, as for
+//            H without the gate), the sum over experts stays in fp32 and there is no
+//            combine pass and no atomics.
+#include <cmath>
+
+#include "few_stream.cuh"
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace {
+
+using namespace few;
+
+constexpr int kMaxExperts = 256;
+
+struct FewParams {
+  const void* x;
+  const void* w_router;
+  const float* bias;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const void* s_gate;  // null without a shared expert
+  const void* s_up;
+  const void* s_down;
+  void* y;
+  int32_t* ids_out;
+  float* gates_out;
+  int32_t* demand_out;
+  int32_t* offsets_out;
+  const int32_t* n_tokens;  // null: all T
+  float* logits;            // [T, E] scratch
+  void* h;                  // [T k (+ T), F] scratch
+  int32_t* status;
+  GridSync sync;
+  int T, d, E, k, F, gate_mode, capacity, has_shared, residual;
+  uint32_t smem_bytes;
+};
+
+// What every CTA knows after the top-k: touched experts in ascending order, the shared
+// expert last (index E).  H row of (expert, its s-th token): hrow + s.
+struct Tables {
+  uint32_t mask[kMaxExperts + 1];  // kept tokens of each expert
+  uint32_t seg_mask[kMaxExperts + 1];
+  int16_t seg_e[kMaxExperts + 2];
+  int16_t seg_hrow[kMaxExperts + 2];
+  int32_t ids[kMaxTokens * 32];    // [T, k]
+  float gates[kMaxTokens * 32];    // [T, k]
+  float gate_of_row[kMaxTokens * 33];
+  int32_t nseg, live, routes;
+};
+constexpr uint32_t kTableBytes = (sizeof(Tables) + 15) & ~15u;
+static_assert(kCtlBytes + 2 * kRedFloats<4> * 4 + kTableBytes + kMaxSlotBytes <= kSmemBytes,
+              "the ring holds the largest slot");
+
+__device__ __forceinline__ float rank_key(float z) { return isnan(z) ? -INFINITY : z; }
+// Larger logit, larger key; -0 ranks as +0.
+__device__ __forceinline__ uint32_t order_key(float z) {
+  const uint32_t b = __float_as_uint(z + 0.f);
+  return b ^ ((b & 0x80000000u) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  return v;
+}
+
+// Router logits: item (expert, group of tokens) per warp, spread over the grid.
+template <typename Tin>
+__device__ __forceinline__ void router_logits(const FewParams& p, int live) {
+  constexpr int VEC = Vec<Tin>::N;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warps = gridDim.x * kConsumerWarps;
+  const int per = (live * p.E <= warps) ? 1 : (live * p.E <= 2 * warps) ? 2 : 4;
+  const int groups = (live + per - 1) / per;
+  const int nv = p.d / VEC;
+  // neighbouring items on different SMs
+  for (int item = warp * gridDim.x + blockIdx.x; item < p.E * groups; item += warps) {
+    const int e = item % p.E, t0 = (item / p.E) * per;
+    const int nt = min(per, live - t0);
+    const Tin* w = static_cast<const Tin*>(p.w_router) + static_cast<size_t>(e) * p.d;
+    const Tin* x = static_cast<const Tin*>(p.x) + static_cast<size_t>(t0) * p.d;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int v = lane; v < nv; v += 32) {
+      float wf[VEC];
+      Vec<Tin>::to_f32(ld_vec(w + v * VEC), wf);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < nt) {
+          float xf[VEC];
+          Vec<Tin>::to_f32(ld_vec(x + static_cast<size_t>(i) * p.d + v * VEC), xf);
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) acc[i] = fmaf(xf[q], wf[q], acc[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < nt) {
+        const float z = warp_sum(acc[i]);
+        if (lane == 0)
+          p.logits[(t0 + i) * p.E + e] = z + (p.bias != nullptr ? __ldg(p.bias + e) : 0.f);
+      }
+    }
+  }
+}
+
+// Top-k and gates of token t by one warp: k rounds of (largest key, then lowest index).
+template <int NP>
+__device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, int t) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int e = 32 * i + lane;
+    key[i] = 0;  // below every logit's key (-inf is 0x007fffff)
+    if (e < p.E) key[i] = order_key(rank_key(__ldcg(p.logits + t * p.E + e)));
+  }
+  uint32_t taken = 0;
+  float sel_z = -INFINITY;
+  int sel_e = 0;
+  for (int j = 0; j < p.k; ++j) {
+    uint32_t best = 0;
+    int be = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (!(taken & (1u << i)) && key[i] > best) { best = key[i]; be = 32 * i + lane; }
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int e = __reduce_min_sync(0xffffffffu, best == top ? be : 0x7fffffff);
+    if (e % 32 == lane) taken |= 1u << (e / 32);
+    if (lane == j) { sel_z = key_value(top); sel_e = e; }
+  }
+  const float m = __shfl_sync(0xffffffffu, sel_z, 0);
+  float g = 0.f;
+  if (m > -INFINITY) {  // else every expert is masked: the token takes nothing from any
+    const float ej = (lane < p.k) ? expf(sel_z - m) : 0.f;
+    float denom = warp_sum(ej);
+    if (p.gate_mode == MOE_GATE_SOFTMAX_TOPK) {
+      float local = 0.f;
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if (32 * i + lane < p.E) local += expf(key_value(key[i]) - m);
+      denom = warp_sum(local);
+    }
+    // renormalising the full softmax over the selected experts cancels its denominator
+    g = ej / denom;
+  }
+  if (lane < p.k) {
+    tb.ids[t * p.k + lane] = sel_e;
+    tb.gates[t * p.k + lane] = g;
+    atomicOr(&tb.mask[sel_e], 1u << t);
+  }
+}
+
+// The tables, by the consumer threads.
+__device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int live) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int e = tid; e <= p.E; e += kConsumers) tb.mask[e] = 0;
+  consumer_sync();
+  for (int t = warp; t < live; t += kConsumerWarps) {
+    if (p.E <= 32) select_token<1>(p, tb, t);
+    else if (p.E <= 64) select_token<2>(p, tb, t);
+    else select_token<8>(p, tb, t);
+  }
+  consumer_sync();
+  if (warp == 0) {
+    int nseg = 0, rows = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      uint32_t m = e < p.E ? tb.mask[e] : 0;
+      if (blockIdx.x == 0 && e < p.E && p.demand_out != nullptr) p.demand_out[e] = __popc(m);
+      if (p.capacity >= 0)  // arrival order is token order: the lowest C tokens stay
+        while (__popc(m) > p.capacity) m &= ~(0x80000000u >> __clz(m));
+      const int n = __popc(m);
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
+      const int row = rows + incl - n;
+      if (e < p.E) {
+        tb.mask[e] = m;
+        if (blockIdx.x == 0 && p.offsets_out != nullptr) p.offsets_out[e] = row;
+      }
+      if (n > 0) {
+        const int i = nseg + __popc(has & ((1u << lane) - 1u));
+        tb.seg_e[i] = static_cast<int16_t>(e);
+        tb.seg_mask[i] = m;
+        tb.seg_hrow[i] = static_cast<int16_t>(row);
+      }
+      nseg += __popc(has);
+      rows += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int total = rows + (p.has_shared ? live : 0);
+    if (lane == 0) {
+      if (p.has_shared && live > 0) {
+        tb.seg_e[nseg] = static_cast<int16_t>(p.E);
+        tb.seg_mask[nseg] = live == 32 ? 0xffffffffu : (1u << live) - 1u;
+        tb.seg_hrow[nseg] = static_cast<int16_t>(rows);
+        ++nseg;
+      }
+      tb.nseg = nseg;
+      tb.routes = rows;
+      if (blockIdx.x == 0 && p.offsets_out != nullptr) {
+        p.offsets_out[p.E] = rows;
+        p.offsets_out[p.E + 1] = total;
+      }
+    }
+    for (int i = rows + lane; i < total; i += 32) tb.gate_of_row[i] = 1.f;  // shared expert
+  }
+  consumer_sync();
+  // gate of each kept route's H row
+  for (int s = warp; s < tb.nseg; s += kConsumerWarps) {
+    const int e = tb.seg_e[s];
+    const uint32_t m = tb.seg_mask[s];
+    if (e < p.E && ((m >> lane) & 1u)) {
+      float g = 0.f;
+      for (int j = 0; j < p.k; ++j)
+        if (tb.ids[lane * p.k + j] == e) g = tb.gates[lane * p.k + j];
+      tb.gate_of_row[tb.seg_hrow[s] + __popc(m & ((1u << lane) - 1u))] = g;
+    }
+  }
+  if (blockIdx.x == 0)
+    for (int i = tid; i < live * p.k; i += kConsumers) {
+      if (p.ids_out != nullptr) p.ids_out[i] = tb.ids[i];
+      if (p.gates_out != nullptr) p.gates_out[i] = tb.gates[i];
+    }
+}
+
+// This CTA's share of n rows.
+__device__ __forceinline__ void share(int64_t n, int64_t* lo, int64_t* hi) {
+  *lo = n * blockIdx.x / gridDim.x;
+  *hi = n * (blockIdx.x + 1) / gridDim.x;
+}
+
+// Position of the down phase: tiles of output rows, and per tile every (segment, chunk).
+struct DownPos {
+  int row, nrows, seg, kv;  // first row and rows of the tile, segment, first vector
+};
+
+template <typename Tin, int NT>
+__global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams p) {
+  constexpr bool F32 = sizeof(Tin) == 4;
+  constexpr int VEC = Vec<Tin>::N;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Shared s = carve<NT>(smem, kTableBytes, p.smem_bytes);
+  Tables& tb = *reinterpret_cast<Tables*>(smem + kCtlBytes + 2 * kRedFloats<NT> * 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Tin* X = static_cast<const Tin*>(p.x);
+  Tin* H = static_cast<Tin*>(p.h);
+
+  init_shared(s);
+  const int live = p.n_tokens != nullptr ? min(max(__ldg(p.n_tokens), 0), p.T) : p.T;
+  __syncthreads();
+
+  // ---- router, top-k, tables ----
+  bool ok = true;
+  if (warp < kConsumerWarps) {
+    router_logits<Tin>(p, live);
+    consumer_sync();
+    if (tid == 0) {
+      grid_arrive(p.sync);
+      grid_wait(p.sync, gridDim.x, s.abort_flag, p.status);
+    }
+    consumer_sync();
+    ok = *s.abort_flag == 0;  // written before the barrier: the same for all
+    if (ok) build_tables(p, tb, live);
+    else if (tid == 0) tb.nseg = 0;
+  }
+  __syncthreads();
+  const int nseg = tb.nseg;
+  int64_t g0, g1, c0, c1;
+  share(static_cast<int64_t>(nseg) * p.F, &g0, &g1);
+  share(p.d, &c0, &c1);
+  const int dv = p.d / VEC, fv = p.F / VEC;  // 16-byte vectors of a row
+
+  if (warp == kConsumerWarps) {
+    // ------------------------------------------------------------------ producer
+    Producer<F32> pr{s, p.status};
+    bool go = *s.abort_flag == 0;
+    for (int64_t at = g0; at < g1 && go;) {
+      const int seg = static_cast<int>(at / p.F), f0 = static_cast<int>(at % p.F);
+      const int np = static_cast<int>(min(min(static_cast<int64_t>(16), g1 - at),
+                                          static_cast<int64_t>(p.F - f0)));
+      const int e = tb.seg_e[seg];
+      const uint32_t mask = tb.seg_mask[seg];
+      const int nb = __popc(mask);
+      const bool sh = e == p.E;
+      const Tin* wg = static_cast<const Tin*>(sh ? p.s_gate : p.w_gate);
+      const Tin* wu = static_cast<const Tin*>(sh ? p.s_up : p.w_up);
+      const size_t base = (sh ? 0 : static_cast<size_t>(e) * p.F) + f0;
+      const Tin* wrow = (lane < np) ? wg + (base + lane) * p.d : wu + (base + lane - np) * p.d;
+      const Tin* xrow = X + static_cast<size_t>(lane) * p.d;
+      for (int kv = 0; kv < dv; kv += kChunkVecs) {
+        const int n = min(kChunkVecs, dv - kv);
+        uint32_t off;
+        if (pr.place((2 * np + nb) * kPitch<F32>, 0xffffffffu, &off) != 1) { go = false; break; }
+        const SlotDesc d{off, static_cast<int16_t>(np), static_cast<int16_t>(np),
+                         static_cast<int16_t>(n), kv == 0, kv + n == dv, mask, 0, seg, f0};
+        pr.open(d, (2 * np + nb) * n * 16);
+        uint64_t* bar = &s.full[pr.it % kSlots];
+        if (lane < 2 * np) bulk_load(pr.row_ptr(off, lane), wrow + kv * VEC, n * 16, bar);
+        if ((mask >> lane) & 1u)
+          bulk_load(pr.row_ptr(off, 2 * np + __popc(mask & ((1u << lane) - 1u))),
+                    xrow + kv * VEC, n * 16, bar);
+        ++pr.it;
+      }
+      at += np;
+    }
+    // Down: the weight rows of the slots that fit come before the barrier, their H rows
+    // after it.  `w` is the position of the next slot, `b` the one whose H rows are next.
+    const uint32_t first = pr.it;
+    DownPos w{static_cast<int>(c0), 0, 0, 0}, b;
+    w.nrows = static_cast<int>(min(static_cast<int64_t>(kTileRows), c1 - c0));
+    b = w;
+    auto next = [&](DownPos& q) {
+      q.kv += kChunkVecs;
+      if (q.kv < fv) return;
+      q.kv = 0;
+      if (++q.seg < nseg) return;
+      q.seg = 0;
+      q.row += q.nrows;
+      q.nrows = min(kTileRows, static_cast<int>(c1) - q.row);
+    };
+    auto load_h = [&](const DownPos& q, uint32_t it) {
+      const uint32_t mask = tb.seg_mask[q.seg];
+      if ((mask >> lane) & 1u) {
+        const int slot = __popc(mask & ((1u << lane) - 1u));
+        const int n = min(kChunkVecs, fv - q.kv);
+        bulk_load(pr.row_ptr(s.desc[it % kSlots].off, q.nrows + slot),
+                  H + static_cast<size_t>(tb.seg_hrow[q.seg] + slot) * p.F + q.kv * VEC, n * 16,
+                  &s.full[it % kSlots]);
+      }
+    };
+    bool passed = false;
+    uint32_t h_it = first;
+    while (go && nseg > 0 && w.nrows > 0) {
+      const int e = tb.seg_e[w.seg];
+      const uint32_t mask = tb.seg_mask[w.seg];
+      const int nb = __popc(mask);
+      const int n = min(kChunkVecs, fv - w.kv);
+      uint32_t off;
+      int r = pr.place((w.nrows + nb) * kPitch<F32>, passed ? 0xffffffffu : first, &off);
+      if (r == 0) {  // the ring is full of slots that wait for H
+        go = __all_sync(0xffffffffu,
+                        grid_wait(p.sync, 2 * gridDim.x, s.abort_flag, p.status));
+        if (!go) break;
+        passed = true;
+        fence_proxy_async_all();
+        for (; h_it < pr.it; ++h_it, next(b)) load_h(b, h_it);
+        continue;
+      }
+      if (r < 0) { go = false; break; }
+      const bool sh = e == p.E;
+      const Tin* wd = static_cast<const Tin*>(sh ? p.s_down : p.w_down) +
+                      ((sh ? 0 : static_cast<size_t>(e) * p.d) + w.row) * p.F;
+      const int r0 = min(16, w.nrows);
+      const SlotDesc d{off, static_cast<int16_t>(r0), static_cast<int16_t>(w.nrows - r0),
+                       static_cast<int16_t>(n), w.seg == 0 && w.kv == 0,
+                       w.seg == nseg - 1 && w.kv + n == fv, mask, 1, w.seg, w.row};
+      pr.open(d, (w.nrows + nb) * n * 16);
+      if (lane < w.nrows)
+        bulk_load(pr.row_ptr(off, lane), wd + static_cast<size_t>(lane) * p.F + w.kv * VEC,
+                  n * 16, &s.full[pr.it % kSlots]);
+      if (passed) load_h(w, pr.it);
+      ++pr.it;
+      next(w);
+    }
+    if (go && !passed && pr.it > first) {  // everything fitted: only H is missing
+      go = __all_sync(0xffffffffu, grid_wait(p.sync, 2 * gridDim.x, s.abort_flag, p.status));
+      if (go) {
+        fence_proxy_async_all();
+        for (; h_it < pr.it; ++h_it, next(b)) load_h(b, h_it);
+      }
+    }
+    if (!go) {  // every slot's copies are issued (H rows of any content), then land
+      for (; h_it < pr.it; ++h_it, next(b)) load_h(b, h_it);
+      pr.drain();
+    }
+  } else {
+    // ------------------------------------------------------------------ consumers
+    uint32_t it = 0, tile = 0;
+    int tiles = 0;
+    for (int64_t at = g0; at < g1; ++tiles)
+      at += min(min(static_cast<int64_t>(16), g1 - at), p.F - at % p.F);
+    ok = consume<F32, NT>(s, it, tile, ok ? tiles : 0, p.status, [&](const SlotDesc& d,
+                                                                     const float* red) {
+      const int nb = __popc(d.mask), hrow = tb.seg_hrow[d.seg];
+      for (int i = tid; i < 16 * nb; i += kConsumers) {
+        const int r = i & 15, n = i >> 4;
+        if (r >= d.r0) continue;
+        const float g = red_sum<NT>(red, 0, r, n), u = red_sum<NT>(red, 1, r, n);
+        const float v = g / (1.f + expf(-g)) * u * tb.gate_of_row[hrow + n];
+        Tin* o = H + static_cast<size_t>(hrow + n) * p.F + d.row + r;
+        if constexpr (F32) *o = v;
+        else *o = __float2bfloat16_rn(v);
+      }
+    }) && ok;
+    fence_proxy_async_all();  // H is read by bulk copies
+    ok = consumer_all(ok);    // one decision for the barriers below
+    if (tid == 0) grid_arrive(p.sync);
+    const int rows = static_cast<int>(c1 - c0);
+    auto put = [&](int t, int c, float v) {
+      const size_t o = static_cast<size_t>(t) * p.d + c;
+      Tin* yo = static_cast<Tin*>(p.y) + o;
+      if constexpr (F32) {
+        *yo = p.residual ? v + X[o] : v;
+      } else {
+        *yo = __float2bfloat16_rn(p.residual ? v + __bfloat162float(X[o]) : v);
+      }
+    };
+    if (nseg == 0) {  // capacity 0 and no shared expert: only the residual is left
+      if (ok)
+        for (int i = tid; i < rows * live; i += kConsumers)
+          put(i / rows, static_cast<int>(c0) + i % rows, 0.f);
+    } else {
+      consume<F32, NT>(s, it, tile, ok ? (rows + kTileRows - 1) / kTileRows : 0, p.status,
+                       [&](const SlotDesc& d, const float* red) {
+        const int nr = d.r0 + d.r1;
+        for (int i = tid; i < kTileRows * live; i += kConsumers) {
+          const int r = i & 31, t = i >> 5;
+          if (r < nr) put(t, d.row + r, red_sum<NT>(red, 0, r, t));
+        }
+      });
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *s.abort_flag == 0) grid_leave(p.sync);
+}
+
+template <typename Tin, int NT>
+cudaError_t launch_nt(FewParams p, cudaStream_t s) {
+  static DeviceOnce once;
+  cudaError_t e = once.run([] {
+    cudaError_t r = cudaFuncSetAttribute(few_layer_kernel<Tin, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return r != cudaSuccess ? r : prefer_max_shared(few_layer_kernel<Tin, NT>);
+  });
+  if (e != cudaSuccess) return e;
+  p.smem_bytes = kSmemBytes;
+  return launch_cooperative(few_layer_kernel<Tin, NT>, dim3(sm_count()), dim3(kThreads), kSmemBytes,
+                            s, p);
+}
+
+template <typename Tin>
+cudaError_t launch_typed(const FewParams& p, cudaStream_t s) {
+  if (p.T <= 8) return launch_nt<Tin, 1>(p, s);
+  if (p.T <= 16) return launch_nt<Tin, 2>(p, s);
+  return launch_nt<Tin, 4>(p, s);
+}
+
+}  // namespace
+
+FewLayout few_layer_layout(const moe_config& c) {
+  auto align = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+  const size_t esz = c.dtype == MOE_BF16 ? 2 : 4;
+  FewLayout L{};
+  L.logits = kWsHeaderBytes;
+  L.h = L.logits + align(static_cast<size_t>(c.T) * c.E * 4);
+  L.total = L.h + align(static_cast<size_t>(c.T) * (c.k + c.has_shared) * c.d_ff * esz);
+  return L;
+}
+
+bool few_layer_supported(const moe_config& c) {
+  return c.T <= kMaxTokens && !c.stats && c.layout == MOE_LAYOUT_RAGGED &&
+         c.overflow == MOE_OVERFLOW_DROP && c.fuse == MOE_FUSE_NONE;
+}
+
+cudaError_t launch_few_layer(const moe_config& c, const FewArgs& a, void* ws, cudaStream_t s) {
+  const FewLayout L = few_layer_layout(c);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  unsigned int* sync = reinterpret_cast<unsigned int*>(w + kWsGridSyncOffset);
+  FewParams p{a.x, a.w_router, a.bias, a.w_gate, a.w_up, a.w_down, a.s_gate, a.s_up, a.s_down,
+              a.y, a.ids, a.gates, a.demand, a.offsets, a.n_tokens,
+              reinterpret_cast<float*>(w + L.logits), w + L.h,
+              reinterpret_cast<int32_t*>(w), GridSync{sync, sync + 1},
+              c.T, c.d, c.E, c.k, c.d_ff, c.gate_mode, c.capacity, c.has_shared,
+              c.add_residual, 0};
+  return c.dtype == MOE_BF16 ? launch_typed<__nv_bfloat16>(p, s) : launch_typed<float>(p, s);
+}
+
+}  // namespace moe

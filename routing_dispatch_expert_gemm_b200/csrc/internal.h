@@ -168,6 +168,31 @@ bool ffn_shared_on_pairs(const moe_config& c);
 // Kernel launches of the expert FFN for the config: 2, or 4 with ffn_shared_on_pairs.
 int ffn_launches(const moe_config& c);
 
+// The whole layer for at most 32 tokens in one cooperative kernel (few_layer.cu).
+struct FewArgs {
+  const void* x;
+  const void* w_router;
+  const float* bias;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const void* s_gate;  // null without a shared expert
+  const void* s_up;
+  const void* s_down;
+  void* y;
+  int32_t* ids;        // optional outputs, null: not written
+  float* gates;
+  int32_t* demand;
+  int32_t* offsets;
+  const int32_t* n_tokens;  // device count of tokens, null: all T
+};
+struct FewLayout {
+  size_t logits, h, total;  // byte offsets in the workspace, bytes in all
+};
+FewLayout few_layer_layout(const moe_config& c);
+bool few_layer_supported(const moe_config& c);
+cudaError_t launch_few_layer(const moe_config& c, const FewArgs& a, void* ws, cudaStream_t s);
+
 cudaError_t launch_debug_wait(int32_t* status, int64_t limit_ns, cudaStream_t s);
 
 // Default bound on every in-kernel wait (nanoseconds).

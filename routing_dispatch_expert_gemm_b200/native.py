@@ -7,6 +7,7 @@ raises ``ImportError`` (build it with ``routing_dispatch_expert_gemm_b200.build.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -28,7 +29,7 @@ FUSE = {"none": 0, "gather": 1, "combine": 2, "gather+combine": 3}
 EXPORTS = ("moe_capacity", "moe_max_rows", "moe_workspace_bytes", "moe_workspace_init",
            "moe_ffn_tile_shape", "moe_ffn_launches",
            "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine", "moe_forward",
-           "moe_forward_profiled", "moe_get_device_status", "moe_debug_bounded_wait",
+           "moe_forward_few", "moe_forward_profiled", "moe_get_device_status", "moe_debug_bounded_wait",
            "moe_dispatch_noalloc", "moe_routing_stats", "moe_status_string",
            "moe_abi_version")
 
@@ -105,6 +106,7 @@ def lib() -> ctypes.CDLL:
             "moe_expert_ffn": (_I32, [_CFG] + [_P] * 12 + [_P]),
             "moe_combine": (_I32, [_CFG, _P, _P, _P, _P, _P, _P, _P]),
             "moe_forward": (_I32, [_CFG] + [_P] * 15 + [_P]),
+            "moe_forward_few": (_I32, [_CFG] + [_P] * 16 + [_P]),
             "moe_forward_profiled": (_I32, [_CFG] + [_P] * 14 + [ctypes.POINTER(_P), _I32, _P, _P]),
             "moe_get_device_status": (_I32, [_P, _P, _I32, ctypes.POINTER(_I32)]),
             "moe_debug_bounded_wait": (_I32, [_P, ctypes.c_int64, _P]),
@@ -140,6 +142,14 @@ def _stream(s):
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _on_device(t):
+    """Make a tensor's device the current one for the call (its stream is the default)."""
+    if hasattr(t, "is_cuda") and t.is_cuda:
+        import torch
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
 
 
 def _check(code: int, where: str):
@@ -222,6 +232,20 @@ def moe_forward(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, shared_gate,
                              _ptr(shared_up), _ptr(shared_down), _ptr(y), _ptr(ids_out),
                              _ptr(gates_out), _ptr(demand_out), _ptr(offsets_out), _ptr(ws),
                              _stream(stream)), "moe_forward")
+
+
+def moe_forward_few(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, shared_gate, shared_up,
+                    shared_down, y, ids_out, gates_out, demand_out, offsets_out, n_tokens, ws,
+                    stream=None):
+    """moe_forward for at most 32 tokens in one kernel.  ``n_tokens``: a device int32 tensor
+    with the number of leading rows of ``x`` that hold tokens, or None for all of them."""
+    with _on_device(x):
+        _check(lib().moe_forward_few(ctypes.byref(cfg), _ptr(x), _ptr(w_router),
+                                     _ptr(logit_bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                     _ptr(shared_gate), _ptr(shared_up), _ptr(shared_down),
+                                     _ptr(y), _ptr(ids_out), _ptr(gates_out), _ptr(demand_out),
+                                     _ptr(offsets_out), _ptr(n_tokens), _ptr(ws),
+                                     _stream(stream)), "moe_forward_few")
 
 
 def moe_forward_profiled(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, shared_gate,
