@@ -13,7 +13,7 @@
 //   router   one warp per (expert, up to 4 tokens) dot product, spread over all CTAs.
 //   -- barrier --  every CTA selects the top-k for all tokens itself (T * k <= 1024 routes)
 //                  and builds the same tables: per expert a 32-bit mask of its tokens.
-//   gate/up  (touched experts x F) rows, cut evenly over the CTAs; a tile is up to 16 gate
+//   gate/up  (touched experts x F) row pairs, cut over the CTAs at equal cost; a tile is up to 16 gate
 //            rows with their 16 up rows, against the expert's own tokens only.
 //   -- barrier --  meanwhile the producer already streams W_down into the ring; only the
 //                  H rows of those slots wait for the barrier.
@@ -68,8 +68,14 @@ struct Tables {
   int32_t ids[kMaxTokens * 32];    // [T, k]
   float gates[kMaxTokens * 32];    // [T, k]
   float gate_of_row[kMaxTokens * 33];
-  int32_t nseg, live, routes;
+  int32_t cost[kMaxExperts + 2];   // per hidden row, summed over the segments before
+  int64_t lo, hi;                  // this CTA's (segment, hidden row) pairs of gate/up
+  int32_t nseg;
 };
+// Cost of a gate/up row pair with nb tokens: two weight rows and, per 16 pairs, nb token
+// rows through the same copies and shared memory.
+__device__ __forceinline__ int pair_cost(int nb) { return 32 + nb; }
+
 constexpr uint32_t kTableBytes = (sizeof(Tables) + 15) & ~15u;
 static_assert(kCtlBytes + 2 * kRedFloats<4> * 4 + kTableBytes + kMaxSlotBytes <= kSmemBytes,
               "the ring holds the largest slot");
@@ -178,6 +184,12 @@ __device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, int
   }
 }
 
+// This CTA's share of n rows.
+__device__ __forceinline__ void share(int64_t n, int64_t* lo, int64_t* hi) {
+  *lo = n * blockIdx.x / gridDim.x;
+  *hi = n * (blockIdx.x + 1) / gridDim.x;
+}
+
 // The tables, by the consumer threads.
 __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int live) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -190,19 +202,20 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
   }
   consumer_sync();
   if (warp == 0) {
-    int nseg = 0, rows = 0;
+    int nseg = 0, rows = 0, cost = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       uint32_t m = e < p.E ? tb.mask[e] : 0;
       if (blockIdx.x == 0 && e < p.E && p.demand_out != nullptr) p.demand_out[e] = __popc(m);
       if (p.capacity >= 0)  // arrival order is token order: the lowest C tokens stay
         while (__popc(m) > p.capacity) m &= ~(0x80000000u >> __clz(m));
-      const int n = __popc(m);
-      int incl = n;
+      const int n = __popc(m), w = n > 0 ? pair_cost(n) : 0;
+      int incl = n, cincl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int q = __shfl_up_sync(0xffffffffu, cincl, o);
+        if (lane >= o) { incl += v; cincl += q; }
       }
       const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
       const int row = rows + incl - n;
@@ -215,9 +228,11 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
         tb.seg_e[i] = static_cast<int16_t>(e);
         tb.seg_mask[i] = m;
         tb.seg_hrow[i] = static_cast<int16_t>(row);
+        tb.cost[i] = cost + cincl - w;
       }
       nseg += __popc(has);
       rows += __shfl_sync(0xffffffffu, incl, 31);
+      cost += __shfl_sync(0xffffffffu, cincl, 31);
     }
     const int total = rows + (p.has_shared ? live : 0);
     if (lane == 0) {
@@ -225,10 +240,13 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
         tb.seg_e[nseg] = static_cast<int16_t>(p.E);
         tb.seg_mask[nseg] = live == 32 ? 0xffffffffu : (1u << live) - 1u;
         tb.seg_hrow[nseg] = static_cast<int16_t>(rows);
+        tb.cost[nseg] = cost;
+        cost += pair_cost(live);
         ++nseg;
       }
       tb.nseg = nseg;
-      tb.routes = rows;
+      tb.cost[nseg] = cost;
+      tb.lo = tb.hi = static_cast<int64_t>(nseg) * p.F;  // the end, unless a segment has it
       if (blockIdx.x == 0 && p.offsets_out != nullptr) {
         p.offsets_out[p.E] = rows;
         p.offsets_out[p.E + 1] = total;
@@ -237,6 +255,17 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
     for (int i = rows + lane; i < total; i += 32) tb.gate_of_row[i] = 1.f;  // shared expert
   }
   consumer_sync();
+  // equal cost for every CTA: where this one's share of the pairs begins and ends
+  const int64_t sum = static_cast<int64_t>(tb.cost[tb.nseg]) * p.F;
+  int64_t from, to;
+  share(sum, &from, &to);
+  for (int s = tid; s < tb.nseg; s += kConsumers) {
+    const int64_t a = static_cast<int64_t>(tb.cost[s]) * p.F;
+    const int64_t b = static_cast<int64_t>(tb.cost[s + 1]) * p.F;
+    const int w = tb.cost[s + 1] - tb.cost[s];
+    if (from >= a && from < b) tb.lo = static_cast<int64_t>(s) * p.F + (from - a) / w;
+    if (to >= a && to < b) tb.hi = static_cast<int64_t>(s) * p.F + (to - a) / w;
+  }
   // gate of each kept route's H row
   for (int s = warp; s < tb.nseg; s += kConsumerWarps) {
     const int e = tb.seg_e[s];
@@ -255,15 +284,12 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
     }
 }
 
-// This CTA's share of n rows.
-__device__ __forceinline__ void share(int64_t n, int64_t* lo, int64_t* hi) {
-  *lo = n * blockIdx.x / gridDim.x;
-  *hi = n * (blockIdx.x + 1) / gridDim.x;
-}
-
-// Position of the down phase: tiles of output rows, and per tile every (segment, chunk).
+// Position of the down phase: tiles of output rows, and per tile every (segment, chunk),
+// starting at a different one in each CTA.  In one common order all CTAs would ask for the
+// same few H rows at the same moment, and the L2 slices that hold them become the limit.
 struct DownPos {
   int row, nrows, seg, kv;  // first row and rows of the tile, segment, first vector
+  int left;                 // (segment, chunk) pairs of the tile still to come, this one too
 };
 
 template <typename Tin, int NT>
@@ -273,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
   extern __shared__ __align__(128) uint8_t smem[];
   const Shared s = carve<NT>(smem, kTableBytes, p.smem_bytes);
   Tables& tb = *reinterpret_cast<Tables*>(smem + kCtlBytes + 2 * kRedFloats<NT> * 4);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const Tin* X = static_cast<const Tin*>(p.x);
   Tin* H = static_cast<Tin*>(p.h);
 
@@ -297,14 +323,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
   }
   __syncthreads();
   const int nseg = tb.nseg;
-  int64_t g0, g1, c0, c1;
-  share(static_cast<int64_t>(nseg) * p.F, &g0, &g1);
+  const int64_t g0 = nseg > 0 ? tb.lo : 0, g1 = nseg > 0 ? tb.hi : 0;
+  int64_t c0, c1;
   share(p.d, &c0, &c1);
   const int dv = p.d / VEC, fv = p.F / VEC;  // 16-byte vectors of a row
 
-  if (warp == kConsumerWarps) {
-    // ------------------------------------------------------------------ producer
-    Producer<F32> pr{s, p.status};
+  if (warp >= kConsumerWarps) {
+    // ------------------------------------------------------------------ producers
+    constexpr uint32_t P = kPitch<F32>;
+    const size_t xs = static_cast<size_t>(p.d) * sizeof(Tin);  // bytes of a row of d
+    const size_t hs = static_cast<size_t>(p.F) * sizeof(Tin);  // bytes of a row of F
+    Producer<F32> pr(s, p.status);
     bool go = *s.abort_flag == 0;
     for (int64_t at = g0; at < g1 && go;) {
       const int seg = static_cast<int>(at / p.F), f0 = static_cast<int>(at % p.F);
@@ -312,97 +341,100 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
                                           static_cast<int64_t>(p.F - f0)));
       const int e = tb.seg_e[seg];
       const uint32_t mask = tb.seg_mask[seg];
-      const int nb = __popc(mask);
+      const uint32_t rows = 2 * np + __popc(mask);
       const bool sh = e == p.E;
-      const Tin* wg = static_cast<const Tin*>(sh ? p.s_gate : p.w_gate);
-      const Tin* wu = static_cast<const Tin*>(sh ? p.s_up : p.w_up);
-      const size_t base = (sh ? 0 : static_cast<size_t>(e) * p.F) + f0;
-      const Tin* wrow = (lane < np) ? wg + (base + lane) * p.d : wu + (base + lane - np) * p.d;
-      const Tin* xrow = X + static_cast<size_t>(lane) * p.d;
-      for (int kv = 0; kv < dv; kv += kChunkVecs) {
-        const int n = min(kChunkVecs, dv - kv);
-        uint32_t off;
-        if (pr.place((2 * np + nb) * kPitch<F32>, 0xffffffffu, &off) != 1) { go = false; break; }
-        const SlotDesc d{off, static_cast<int16_t>(np), static_cast<int16_t>(np),
-                         static_cast<int16_t>(n), kv == 0, kv + n == dv, mask, 0, seg, f0};
-        pr.open(d, (2 * np + nb) * n * 16);
-        uint64_t* bar = &s.full[pr.it % kSlots];
-        if (lane < 2 * np) bulk_load(pr.row_ptr(off, lane), wrow + kv * VEC, n * 16, bar);
-        if ((mask >> lane) & 1u)
-          bulk_load(pr.row_ptr(off, 2 * np + __popc(mask & ((1u << lane) - 1u))),
-                    xrow + kv * VEC, n * 16, bar);
-        ++pr.it;
+      const size_t base = ((sh ? 0 : static_cast<size_t>(e) * p.F) + f0) * xs;
+      const uint8_t* wg = static_cast<const uint8_t*>(sh ? p.s_gate : p.w_gate) + base;
+      const uint8_t* wu = static_cast<const uint8_t*>(sh ? p.s_up : p.w_up) + base;
+      const uint8_t* xb = static_cast<const uint8_t*>(p.x);
+      const int chunks = (dv + kChunkVecs - 1) / kChunkVecs;
+      int c = blockIdx.x % chunks;  // see DownPos: not all CTAs read the same token chunk
+      for (int i = 0; i < chunks; ++i, c = c + 1 == chunks ? 0 : c + 1) {
+        const int kv = c * kChunkVecs;
+        pr.reserve(rows * P);
+        if (pr.mine()) {
+          if (pr.ready(rows * P, 0xffffffffu) != 1) { go = false; break; }
+          const int n = min(kChunkVecs, dv - kv);
+          const uint32_t bytes = n * 16, o = kv * 16;
+          pr.open(SlotDesc{0, static_cast<int16_t>(np), static_cast<int16_t>(np),
+                           static_cast<int16_t>(n), i + 1 == chunks, mask, 0, seg, f0},
+                  rows * bytes);
+          pr.copy_rows(pr.it, pr.head, 0, wg + o, xs, np, bytes);
+          pr.copy_rows(pr.it, pr.head, np, wu + o, xs, np, bytes);
+          pr.copy_tokens(pr.it, pr.head, 2 * np, xb + o, xs, mask, bytes);
+        }
+        pr.pass(rows * P);
       }
       at += np;
     }
     // Down: the weight rows of the slots that fit come before the barrier, their H rows
-    // after it.  `w` is the position of the next slot, `b` the one whose H rows are next.
+    // after it.  `w` is the position of the next slot, `b` that of slot h_it, the first
+    // whose H rows are still to come.
     const uint32_t first = pr.it;
-    DownPos w{static_cast<int>(c0), 0, 0, 0}, b;
-    w.nrows = static_cast<int>(min(static_cast<int64_t>(kTileRows), c1 - c0));
-    b = w;
+    uint32_t h_it = first;
+    const int fch = (fv + kChunkVecs - 1) / kChunkVecs, pairs = fch * nseg;
+    const int turn = static_cast<int>(static_cast<int64_t>(pairs) * blockIdx.x / gridDim.x);
+    DownPos w{static_cast<int>(c0), static_cast<int>(min(static_cast<int64_t>(kTileRows),
+                                                         c1 - c0)),
+              turn / fch, turn % fch * kChunkVecs, pairs};
+    DownPos b = w;
     auto next = [&](DownPos& q) {
       q.kv += kChunkVecs;
-      if (q.kv < fv) return;
-      q.kv = 0;
-      if (++q.seg < nseg) return;
-      q.seg = 0;
+      if (q.kv >= fv) {
+        q.kv = 0;
+        if (++q.seg == nseg) q.seg = 0;
+      }
+      if (--q.left > 0) return;
+      q.left = pairs;  // back at the turn: the next tile
       q.row += q.nrows;
       q.nrows = min(kTileRows, static_cast<int>(c1) - q.row);
     };
     auto load_h = [&](const DownPos& q, uint32_t it) {
-      const uint32_t mask = tb.seg_mask[q.seg];
-      if ((mask >> lane) & 1u) {
-        const int slot = __popc(mask & ((1u << lane) - 1u));
-        const int n = min(kChunkVecs, fv - q.kv);
-        bulk_load(pr.row_ptr(s.desc[it % kSlots].off, q.nrows + slot),
-                  H + static_cast<size_t>(tb.seg_hrow[q.seg] + slot) * p.F + q.kv * VEC, n * 16,
-                  &s.full[it % kSlots]);
-      }
+      const int nb = __popc(tb.seg_mask[q.seg]);
+      pr.copy_rows(it, s.desc[it % kSlots].off, q.nrows,
+                   reinterpret_cast<const uint8_t*>(H) + tb.seg_hrow[q.seg] * hs + q.kv * 16,
+                   hs, nb, min(kChunkVecs, fv - q.kv) * 16);
+    };
+    auto load_late_h = [&] {
+      for (; h_it < pr.it; ++h_it, next(b))
+        if (h_it % kProducerWarps == pr.me) load_h(b, h_it);
     };
     bool passed = false;
-    uint32_t h_it = first;
+    auto pass_barrier = [&] {  // H is complete; bulk copies may read it
+      go = grid_wait_warp(p.sync, 2 * gridDim.x, s.abort_flag, p.status);
+      passed = true;
+      fence_proxy_async_all();
+      load_late_h();
+    };
     while (go && nseg > 0 && w.nrows > 0) {
       const int e = tb.seg_e[w.seg];
       const uint32_t mask = tb.seg_mask[w.seg];
-      const int nb = __popc(mask);
-      const int n = min(kChunkVecs, fv - w.kv);
-      uint32_t off;
-      int r = pr.place((w.nrows + nb) * kPitch<F32>, passed ? 0xffffffffu : first, &off);
-      if (r == 0) {  // the ring is full of slots that wait for H
-        go = __all_sync(0xffffffffu,
-                        grid_wait(p.sync, 2 * gridDim.x, s.abort_flag, p.status));
-        if (!go) break;
-        passed = true;
-        fence_proxy_async_all();
-        for (; h_it < pr.it; ++h_it, next(b)) load_h(b, h_it);
-        continue;
+      const uint32_t rows = w.nrows + __popc(mask);
+      pr.reserve(rows * P);
+      if (pr.mine()) {
+        int r = pr.ready(rows * P, passed ? 0xffffffffu : first);
+        if (r == 0) {  // the ring is full of slots that wait for H
+          pass_barrier();
+          r = go ? pr.ready(rows * P, 0xffffffffu) : -1;
+        }
+        if (r < 0) { go = false; break; }
+        const int n = min(kChunkVecs, fv - w.kv);
+        const bool sh = e == p.E;
+        const uint8_t* wd = static_cast<const uint8_t*>(sh ? p.s_down : p.w_down) +
+                            ((sh ? 0 : static_cast<size_t>(e) * p.d) + w.row) * hs + w.kv * 16;
+        const int r0 = min(16, w.nrows);
+        pr.open(SlotDesc{0, static_cast<int16_t>(r0), static_cast<int16_t>(w.nrows - r0),
+                         static_cast<int16_t>(n), w.left == 1, mask, 1, w.seg, w.row},
+                rows * n * 16);
+        pr.copy_rows(pr.it, pr.head, 0, wd, hs, w.nrows, n * 16);
+        if (passed) load_h(w, pr.it);
       }
-      if (r < 0) { go = false; break; }
-      const bool sh = e == p.E;
-      const Tin* wd = static_cast<const Tin*>(sh ? p.s_down : p.w_down) +
-                      ((sh ? 0 : static_cast<size_t>(e) * p.d) + w.row) * p.F;
-      const int r0 = min(16, w.nrows);
-      const SlotDesc d{off, static_cast<int16_t>(r0), static_cast<int16_t>(w.nrows - r0),
-                       static_cast<int16_t>(n), w.seg == 0 && w.kv == 0,
-                       w.seg == nseg - 1 && w.kv + n == fv, mask, 1, w.seg, w.row};
-      pr.open(d, (w.nrows + nb) * n * 16);
-      if (lane < w.nrows)
-        bulk_load(pr.row_ptr(off, lane), wd + static_cast<size_t>(lane) * p.F + w.kv * VEC,
-                  n * 16, &s.full[pr.it % kSlots]);
-      if (passed) load_h(w, pr.it);
-      ++pr.it;
+      pr.pass(rows * P);
       next(w);
     }
-    if (go && !passed && pr.it > first) {  // everything fitted: only H is missing
-      go = __all_sync(0xffffffffu, grid_wait(p.sync, 2 * gridDim.x, s.abort_flag, p.status));
-      if (go) {
-        fence_proxy_async_all();
-        for (; h_it < pr.it; ++h_it, next(b)) load_h(b, h_it);
-      }
-    }
+    if (go && !passed && pr.it > first) pass_barrier();  // everything fitted
     if (!go) {  // every slot's copies are issued (H rows of any content), then land
-      for (; h_it < pr.it; ++h_it, next(b)) load_h(b, h_it);
+      if (!passed) load_late_h();
       pr.drain();
     }
   } else {
@@ -411,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     int tiles = 0;
     for (int64_t at = g0; at < g1; ++tiles)
       at += min(min(static_cast<int64_t>(16), g1 - at), p.F - at % p.F);
-    ok = consume<F32, NT>(s, it, tile, ok ? tiles : 0, p.status, [&](const SlotDesc& d,
+    ok = consume<F32, NT>(s, it, tile, ok ? tiles : 0, (dv + kChunkVecs - 1) / kChunkVecs,
+                          p.status, [&](const SlotDesc& d,
                                                                      const float* red) {
       const int nb = __popc(d.mask), hrow = tb.seg_hrow[d.seg];
       for (int i = tid; i < 16 * nb; i += kConsumers) {
@@ -442,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
         for (int i = tid; i < rows * live; i += kConsumers)
           put(i / rows, static_cast<int>(c0) + i % rows, 0.f);
     } else {
-      consume<F32, NT>(s, it, tile, ok ? (rows + kTileRows - 1) / kTileRows : 0, p.status,
+      consume<F32, NT>(s, it, tile, ok ? (rows + kTileRows - 1) / kTileRows : 0,
+                       (fv + kChunkVecs - 1) / kChunkVecs * nseg, p.status,
                        [&](const SlotDesc& d, const float* red) {
         const int nr = d.r0 + d.r1;
         for (int i = tid; i < kTileRows * live; i += kConsumers) {

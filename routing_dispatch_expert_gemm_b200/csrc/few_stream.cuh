@@ -4,12 +4,18 @@
 //
 //   * One CTA per SM, all resident (cooperative launch).  Every phase cuts its output rows
 //     (weight rows) evenly over the CTAs, at single-row granularity, whatever the expert.
-//   * Warp 8 is the producer: it cuts the CTA's rows into tiles of up to 32 weight rows and
-//     the contraction into chunks of 1 KB per row, and copies each chunk's weight rows and
-//     token rows to shared memory with one bulk copy per row.  Slots of a byte ring are
-//     sized by the rows they hold, so thin tiles (a phase that leaves a CTA 7 rows) still
-//     keep the whole ring in flight; the stream does not stop between tiles or phases.
-//   * Warps 0-7 consume: each takes 1/8 of the chunk's contraction for all rows and tokens.
+//   * Warps 8.. produce: the CTA's rows are cut into tiles of up to 32 weight rows and the
+//     contraction into chunks of 1 KB per row; a slot of the ring holds one chunk of a
+//     tile's weight rows and of its token rows, copied with one bulk copy per row.  Slots
+//     are sized by the rows they hold, so thin tiles (a phase that leaves a CTA 7 rows)
+//     still keep the whole ring in flight; the stream does not stop between tiles or phases.
+//     One warp issues a bulk copy about every 45 ns, which would cap the stream at half of
+//     HBM's rate (Mixtral-shaped T=16: 890 us with one producer), so slot i belongs to
+//     producer warp i mod kProducerWarps, one lane per row; every producer follows the same
+//     sequence of slots and places them by the same arithmetic.
+//   * Warps 0-7 consume, two warps to a slot (kGroups slots at a time): a slot costs a warp
+//     a fixed latency (its barrier, descriptor, first loads) that eight warps sharing every
+//     slot all paid (Granite-shaped T=16: 0.7 us per 11-row slot), now paid in parallel.
 //     bf16: mma.sync m16n8k16 with the weight rows on M and the tokens on N, fed by 16-byte
 //     shared loads: thread q of a quad takes 8 consecutive k of its row, for weights and
 //     tokens alike, which only permutes the k index inside a 32-wide block.  At 8 tokens
@@ -17,8 +23,9 @@
 //     below even the warp-level MMA rate, and there is no tensor-memory round trip at the
 //     end of a 7-row tile; that is why this is not tcgen05, whose M is at least 64 rows.
 //     fp32: FMA, one weight row per lane.
-//   * The 8 partial sums per output meet in shared memory in warp order (fixed order: the
-//     same bits every run) and the caller's epilogue consumes the total.
+//   * The 8 partial sums per output meet in shared memory in warp order (which slots a warp
+//     takes depends on the shape alone, so runs give the same bits); the caller's epilogue
+//     consumes a tile's total while the next tile's slots are already being consumed.
 //
 // The MMA reads whole 16-row and 8-token fragments; rows past a tile's last one are clamped
 // to it.  A garbage row or token column only reaches its own outputs, which are not stored.
@@ -33,8 +40,11 @@ namespace few {
 constexpr int kMaxTokens = 32;       // one token-mask word
 constexpr int kConsumerWarps = 8;
 constexpr int kConsumers = 32 * kConsumerWarps;
-constexpr int kThreads = kConsumers + 32;
-constexpr int kSlots = 16;           // slots in flight at most
+constexpr int kGroupWarps = 2;       // warps that share a slot
+constexpr int kGroups = kConsumerWarps / kGroupWarps;
+constexpr int kProducerWarps = 4;
+constexpr int kThreads = kConsumers + 32 * kProducerWarps;
+constexpr int kSlots = 64;           // slot descriptors and barriers
 constexpr int kChunkBytes = 1024;    // contraction bytes per row and chunk
 constexpr int kChunkVecs = kChunkBytes / 16;
 constexpr uint32_t kSmemBytes = 227 * 1024;
@@ -52,7 +62,7 @@ struct alignas(16) SlotDesc {
   int16_t r0, r1;  // weight rows of the first and second row block (the second follows the
                    // first in the slot; in a pair tile they are the gate and the up rows)
   int16_t kvec;    // valid 16-byte vectors along the contraction
-  int8_t first, last;  // first / last chunk of the tile
+  int8_t last;     // last chunk of the tile
   uint32_t mask;   // tokens whose rows the slot holds, ascending
   int32_t scatter; // 1: the token of mask bit t is column t; 0: columns are 0..popc(mask)-1
   int32_t seg;     // caller's: what the tile belongs to
@@ -63,14 +73,19 @@ struct Shared {
   uint64_t* full;
   uint64_t* empty;
   SlotDesc* desc;
+  uint32_t* start;  // [kProducerWarps][kSlots]: each producer's record of slot positions
+  uint64_t* sums;   // [2] a tile's partial sums are complete
+  SlotDesc* tile;   // [2] its last slot's descriptor
   volatile int* abort_flag;
   uint8_t* ring;
-  float* red;      // [2][8 warps][8 NT][kRedStride]
+  float* red;       // [2][8 warps][8 NT][kRedStride]
+  uint8_t* zeros;   // a chunk of zeros: the row of a token that a slot does not hold
   uint32_t ring_bytes;
 };
 
-constexpr int kCtlBytes = 2 * kSlots * 8 + kSlots * 32 + 64;
+constexpr int kCtlBytes = 2 * kSlots * 8 + kSlots * 32 + kProducerWarps * kSlots * 4 + 2 * 32 + 64 + kChunkBytes;
 static_assert(sizeof(SlotDesc) == 32, "descriptor size");
+static_assert(kSlots % kGroups == 0, "a slot's barriers belong to one group");
 template <int NT> constexpr int kRedFloats = kConsumerWarps * 8 * NT * kRedStride;
 // The largest slot: a full tile and 32 token rows.
 constexpr uint32_t kMaxSlotBytes = (kTileRows + kMaxTokens) * (kChunkBytes + 64);
@@ -82,8 +97,12 @@ __device__ __forceinline__ Shared carve(uint8_t* smem, uint32_t table_bytes, uin
   s.full = reinterpret_cast<uint64_t*>(smem);
   s.empty = s.full + kSlots;
   s.desc = reinterpret_cast<SlotDesc*>(s.empty + kSlots);
-  s.abort_flag = reinterpret_cast<volatile int*>(s.desc + kSlots);
+  s.start = reinterpret_cast<uint32_t*>(s.desc + kSlots);
+  s.tile = reinterpret_cast<SlotDesc*>(s.start + kProducerWarps * kSlots);
+  s.sums = reinterpret_cast<uint64_t*>(s.tile + 2);
+  s.abort_flag = reinterpret_cast<volatile int*>(s.sums + 2);
   s.red = reinterpret_cast<float*>(smem + kCtlBytes);
+  s.zeros = smem + kCtlBytes - kChunkBytes;
   const uint32_t at = kCtlBytes + 2 * kRedFloats<NT> * 4 + table_bytes;
   s.ring = smem + at;
   s.ring_bytes = (total - at) & ~15u;
@@ -91,11 +110,15 @@ __device__ __forceinline__ Shared carve(uint8_t* smem, uint32_t table_bytes, uin
 }
 
 __device__ __forceinline__ void init_shared(const Shared& s) {
+  for (int i = threadIdx.x; i < kChunkVecs; i += kThreads)
+    reinterpret_cast<uint4*>(s.zeros)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], kConsumerWarps);
+      mbar_init(&s.empty[i], kGroupWarps);
     }
+    mbar_init(&s.sums[0], kConsumerWarps);
+    mbar_init(&s.sums[1], kConsumerWarps);
     *s.abort_flag = 0;
     fence_mbar_init();
   }
@@ -131,7 +154,7 @@ __device__ __forceinline__ void grid_arrive(const GridSync& g) {  // one thread,
   __threadfence();
   atomicAdd(g.count, 1u);
 }
-// Bounded: returns false (and records MOE_ERR_TIMEOUT) when the arrivals do not come.
+// One thread.  Bounded: returns false (and records MOE_ERR_TIMEOUT) when the arrivals do not come.
 __device__ __forceinline__ bool grid_wait(const GridSync& g, unsigned int target,
                                           volatile int* abort_flag, int32_t* status) {
   const uint64_t t0 = global_timer_ns();
@@ -149,6 +172,13 @@ __device__ __forceinline__ bool grid_wait(const GridSync& g, unsigned int target
     }
   }
 }
+// The same by a whole warp: one lane polls.
+__device__ __forceinline__ bool grid_wait_warp(const GridSync& g, unsigned int target,
+                                               volatile int* abort_flag, int32_t* status) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = grid_wait(g, target, abort_flag, status);
+  return __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+}
 __device__ __forceinline__ void grid_leave(const GridSync& g) {  // one thread, waits all passed
   __threadfence();
   if (atomicAdd(g.left, 1u) == gridDim.x - 1) {
@@ -163,76 +193,116 @@ __device__ __forceinline__ void fence_proxy_async_all() {
 }
 
 // ---------------------------------------------------------------------------------
-// Producer: a FIFO byte ring (warp-uniform state; every lane runs it)
+// Producer: a FIFO byte ring, run by whole producer warps.  Slot i starts at byte
+// `at` of an endless line that skips the ring's end where the slot would not fit; its place
+// is `at` modulo the ring.  The line depends on the slots' sizes only, so every producer
+// computes the same places, and a slot may be written once the oldest slot still in use
+// starts less than a ring's length before its end.  A producer waits for the slots' releases
+// in order and keeps fewer than kInFlight of them unreleased when it fills one.
+//   It must not fall behind by two uses of a slot, whose barrier parity would be ambiguous:
+// while it waits, with its own slot j not filled, for the release of `tail`, no slot from
+// tail + kSlots on may be released.  The others pass slot j only by being ahead, and fill
+// slots below j + kInFlight at most; its own slots are kProducerWarps apart, so
+// j - tail < kInFlight + kProducerWarps.  Hence 2 kInFlight + kProducerWarps <= kSlots + 1.
 // ---------------------------------------------------------------------------------
+constexpr uint32_t kInFlight = (kSlots + 1 - kProducerWarps) / 2;
 template <bool F32>
 struct Producer {
   Shared s;
   int32_t* status;
-  uint32_t head = 0;   // next free byte
-  uint32_t it = 0;     // slots issued
+  uint32_t* start;     // line positions of the last kSlots slots
+  uint32_t me;         // this producer's index
+  uint32_t line = 0;   // line position of the next slot
+  uint32_t head = 0;   // the same modulo the ring
+  uint32_t it = 0;     // slots passed
   uint32_t tail = 0;   // slots known to be released
 
-  __device__ __forceinline__ bool wait_tail() {  // the oldest live slot is released
-    const uint32_t slot = tail % kSlots;
-    if (!mbar_wait_bounded(&s.empty[slot], (tail / kSlots) & 1u, s.abort_flag, kWaitLimitNs,
-                           status))
-      return false;
-    ++tail;
-    return true;
+  __device__ __forceinline__ Producer(const Shared& sh, int32_t* st)
+      : s(sh), status(st), me((threadIdx.x >> 5) - kConsumerWarps) {
+    start = s.start + me * kSlots;
   }
+  __device__ __forceinline__ bool mine() const { return it % kProducerWarps == me; }
 
-  // Place `bytes` in the ring without waiting for any slot >= `barrier_it`; *off is the
-  // offset.  Returns 1 when placed, 0 when it would have to wait for such a slot, -1 on abort.
-  __device__ __forceinline__ int place(uint32_t bytes, uint32_t barrier_it, uint32_t* off) {
-    for (;;) {
-      const uint32_t live = it - tail;
-      if (live == 0) {
-        head = bytes;
-        *off = 0;
-        return 1;
-      }
-      if (live < kSlots) {
-        const uint32_t toff = s.desc[tail % kSlots].off;
-        if (head > toff) {
-          if (s.ring_bytes - head >= bytes) { *off = head; head += bytes; return 1; }
-          if (toff > bytes) { *off = 0; head = bytes; return 1; }
-        } else if (toff - head > bytes) {
-          *off = head;
-          head += bytes;
-          return 1;
-        }
-      }
-      if (tail >= barrier_it) return 0;
-      if (!wait_tail()) return -1;
+  // Take the place of the next slot; `pass` moves on to the one after it.
+  __device__ __forceinline__ void reserve(uint32_t bytes) {
+    if (s.ring_bytes - head < bytes) {
+      line += s.ring_bytes - head;
+      head = 0;
     }
+    if ((threadIdx.x & 31) == 0) start[it % kSlots] = line;
+    __syncwarp();
   }
-
-  // Open the slot: descriptor, then the barrier's expected bytes.
-  __device__ __forceinline__ void open(const SlotDesc& d, uint32_t bytes) {
-    const uint32_t slot = it % kSlots;
+  __device__ __forceinline__ void pass(uint32_t bytes) {
+    line += bytes;
+    head += bytes;
+    ++it;
+  }
+  // Wait until the reserved slot may be written: 1, or 0 if that takes the release of slot
+  // `stop` or a later one, or -1 on abort.
+  __device__ __forceinline__ int ready(uint32_t bytes, uint32_t stop) {
+    while (tail != it &&  // warp-uniform: every lane sees the same state
+           (it - tail >= kInFlight || line + bytes - start[tail % kSlots] > s.ring_bytes)) {
+      if (tail >= stop) return 0;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s.empty[tail % kSlots],
+                                                     (tail / kSlots) & 1u, s.abort_flag,
+                                                     kWaitLimitNs, status)))
+        return -1;
+      ++tail;
+    }
+    return 1;
+  }
+  // Publish the slot's descriptor and arm its barrier; then come its copies.
+  __device__ __forceinline__ void open(SlotDesc d, uint32_t bytes) {
+    d.off = head;
     if ((threadIdx.x & 31) == 0) {
-      s.desc[slot] = d;
-      mbar_arrive_expect_tx(&s.full[slot], bytes);
+      s.desc[it % kSlots] = d;
+      mbar_arrive_expect_tx(&s.full[it % kSlots], bytes);
     }
     __syncwarp();
   }
-  __device__ __forceinline__ uint8_t* row_ptr(uint32_t off, int row) const {
-    return s.ring + off + static_cast<uint32_t>(row) * kPitch<F32>;
+  // Copy `rows` (at most 32) rows of `bytes` bytes, `stride` bytes apart, to rows row.. of the
+  // slot at `off`.
+  __device__ __forceinline__ void copy_rows(uint32_t slot, uint32_t off, int row,
+                                            const uint8_t* src, size_t stride, int rows,
+                                            uint32_t bytes) {
+    const int r = threadIdx.x & 31;
+    if (r < rows)
+      bulk_load(s.ring + off + static_cast<uint32_t>(row + r) * kPitch<F32>, src + r * stride,
+                bytes, &s.full[slot % kSlots]);
+    __syncwarp();
   }
-  // Before leaving early: every copy in flight has landed.
+  // The same for the rows of a token mask.
+  __device__ __forceinline__ void copy_tokens(uint32_t slot, uint32_t off, int row,
+                                              const uint8_t* src, size_t stride, uint32_t mask,
+                                              uint32_t bytes) {
+    const int t = threadIdx.x & 31;
+    if ((mask >> t) & 1u)
+      bulk_load(s.ring + off +
+                    static_cast<uint32_t>(row + __popc(mask & ((1u << t) - 1u))) * kPitch<F32>,
+                src + t * stride, bytes, &s.full[slot % kSlots]);
+    __syncwarp();
+  }
+  // Before leaving early: every copy of this producer has landed, or has had the wait's
+  // limit to.
   __device__ __forceinline__ void drain() {
-    const uint32_t n = min(it, static_cast<uint32_t>(kSlots));
-    for (uint32_t i = it - n; i < it; ++i)
-      mbar_wait_bounded(&s.full[i % kSlots], (i / kSlots) & 1u, nullptr, kWaitLimitNs, status);
+    for (uint32_t i = it - min(it, static_cast<uint32_t>(kSlots)); i < it; ++i)
+      if (i % kProducerWarps == me &&
+          !mbar_wait_bounded(&s.full[i % kSlots], (i / kSlots) & 1u, nullptr, kWaitLimitNs,
+                             status))
+        break;
   }
 };
 
 // ---------------------------------------------------------------------------------
 // Consumers
 // ---------------------------------------------------------------------------------
-__device__ __forceinline__ uint4 lds_vec(const uint8_t* p) {
-  return *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ uint4 lds_vec(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -256,48 +326,87 @@ template <int NT> struct Acc<false, NT> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[m][n][i] = 0.f;
   }
-  __device__ __forceinline__ void chunk(const SlotDesc& d, const uint8_t* base, int warp,
-                                        int lane) {
+  // One 32-wide block: two k-steps.  The k-step is the outer loop so that consecutive MMAs
+  // have different accumulators (an MMA's result is 21 cycles away, its issue slot 8).
+  template <bool TWO, int NB>
+  __device__ __forceinline__ void block(const uint4 (&w)[4], const uint4 (&x)[NB]) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mma_bf16(c[0][n], w[0].x, w[1].x, w[0].y, w[1].y, x[n].x, x[n].y);
+      if (TWO) mma_bf16(c[1][n], w[2].x, w[3].x, w[2].y, w[3].y, x[n].x, x[n].y);
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mma_bf16(c[0][n], w[0].z, w[1].z, w[0].w, w[1].w, x[n].z, x[n].w);
+      if (TWO) mma_bf16(c[1][n], w[2].z, w[3].z, w[2].w, w[3].w, x[n].z, x[n].w);
+    }
+  }
+  // The chunk for NB token blocks, with a second row block or without.  Compile-time: a
+  // branch around each MMA costs more than the MMA (T=16 slots: 3000 cycles instead of 1000).
+  template <bool TWO, int NB>
+  __device__ __forceinline__ void chunk_of(const SlotDesc& d, const Shared& s, int part,
+                                           int lane) {
     constexpr int P = kPitch<false>;
+    const uint32_t base = smem_u32(s.ring) + d.off;
     const int g = lane >> 2, q = lane & 3;
-    const int nb = __popc(d.mask);
+    const uint32_t at = (part * 4 + q) * 16;
     // 16-row blocks: rows past a block's last one are clamped to it
-    const uint8_t* a00 = base + min(g, d.r0 - 1) * P;
-    const uint8_t* a01 = base + min(g + 8, d.r0 - 1) * P;
-    const uint8_t* a10 = base + (d.r0 + min(g, max(d.r1 - 1, 0))) * P;
-    const uint8_t* a11 = base + (d.r0 + min(g + 8, max(d.r1 - 1, 0))) * P;
-    const uint8_t* b = base + (d.r0 + d.r1) * P;
-    const uint4 z = make_uint4(0, 0, 0, 0);
+    const uint32_t a[4] = {base + min(g, d.r0 - 1) * P + at, base + min(g + 8, d.r0 - 1) * P + at,
+                           base + (d.r0 + min(g, d.r1 - 1)) * P + at,
+                           base + (d.r0 + min(g + 8, d.r1 - 1)) * P + at};
+    const int nb = __popc(d.mask);
+    uint32_t b[NB];
 #pragma unroll
-    for (int h = 0; h < kChunkVecs / 4 / kConsumerWarps; ++h) {
-      const int kb = warp + h * kConsumerWarps;  // 32-wide block of the contraction
-      if (kb * 4 >= d.kvec) break;
-      const int v = kb * 4 + q;
-      const bool in = v < d.kvec;  // a ragged contraction ends inside a block: zeros
-      const int o = v * 16;
-      const uint4 w00 = in ? lds_vec(a00 + o) : z, w01 = in ? lds_vec(a01 + o) : z;
-      uint4 w10 = z, w11 = z;
-      if (d.r1 > 0 && in) { w10 = lds_vec(a10 + o); w11 = lds_vec(a11 + o); }
+    for (int n = 0; n < NB; ++n) {
+      const int t = 8 * n + g;
+      int row = t < nb ? t : -1;  // the token row of this lane's column, or none
+      if (d.scatter) row = ((d.mask >> t) & 1u) ? __popc(d.mask & ((1u << t) - 1u)) : -1;
+      b[n] = row >= 0 ? base + (d.r0 + d.r1 + row) * P + at : smem_u32(s.zeros) + at;
+    }
+    constexpr int kStep = kGroupWarps * 64;                // bytes between a warp's blocks
+    constexpr int kBlocks = kChunkBytes / kStep;
+    constexpr int HB = NB == 4 ? 2 : 4;  // blocks loaded together, so that latencies overlap
+    if (d.kvec == kChunkVecs) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        uint4 x = z;
-        if (d.scatter) {  // column = token: zeros for the tokens the slot does not hold
-          if (((d.mask >> (8 * n)) & 0xffu) == 0) continue;
-          const int t = 8 * n + g;
-          const int slot = __popc(d.mask & ((1u << t) - 1u));
-          if (in && ((d.mask >> t) & 1u)) x = lds_vec(b + slot * P + o);
-        } else {
-          if (8 * n >= nb) continue;
-          if (in) x = lds_vec(b + min(8 * n + g, nb - 1) * P + o);
+      for (int i = 0; i < kBlocks; i += HB) {
+        uint4 w[HB][4], x[HB][NB];
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          const int o = (i + h) * kStep;
+#pragma unroll
+          for (int j = 0; j < (TWO ? 4 : 2); ++j) w[h][j] = lds_vec(a[j] + o);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) x[h][n] = lds_vec(b[n] + o);
         }
-        mma_bf16(c[0][n], w00.x, w01.x, w00.y, w01.y, x.x, x.y);
-        mma_bf16(c[0][n], w00.z, w01.z, w00.w, w01.w, x.z, x.w);
-        if (d.r1 > 0) {
-          mma_bf16(c[1][n], w10.x, w11.x, w10.y, w11.y, x.x, x.y);
-          mma_bf16(c[1][n], w10.z, w11.z, w10.w, w11.w, x.z, x.w);
-        }
+#pragma unroll
+        for (int h = 0; h < HB; ++h) block<TWO, NB>(w[h], x[h]);
+      }
+    } else {
+#pragma unroll 1
+      for (int o = 0; (part * 4 + o / 16) < d.kvec; o += kStep) {
+        const bool in = part * 4 + q + o / 16 < d.kvec;  // the end inside a block: zeros
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        uint4 w[4], x[NB];
+#pragma unroll
+        for (int j = 0; j < (TWO ? 4 : 2); ++j) w[j] = in ? lds_vec(a[j] + o) : z;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) x[n] = in ? lds_vec(b[n] + o) : z;
+        block<TWO, NB>(w, x);
       }
     }
+  }
+  template <int NB>
+  __device__ __forceinline__ void chunk_n(const SlotDesc& d, const Shared& s, int part,
+                                          int lane) {
+    if (d.r1 > 0) chunk_of<true, NB>(d, s, part, lane);
+    else chunk_of<false, NB>(d, s, part, lane);
+  }
+  __device__ __forceinline__ void chunk(const SlotDesc& d, const Shared& s, int part, int lane) {
+    // columns in use: up to the last token, or one per token
+    const int cols = d.scatter ? 32 - __clz(d.mask) : __popc(d.mask);
+    if (NT == 1 || cols <= 8) chunk_n<1>(d, s, part, lane);
+    else if (NT == 2 || cols <= 16) chunk_n<(NT < 2 ? 1 : 2)>(d, s, part, lane);
+    else chunk_n<NT>(d, s, part, lane);
   }
   __device__ __forceinline__ void store(float* red, int warp, int lane) const {
     const int g = lane >> 2, q = lane & 3;
@@ -321,21 +430,23 @@ template <int NT> struct Acc<true, NT> {
 #pragma unroll
     for (int n = 0; n < 8 * NT; ++n) c[n] = 0.f;
   }
-  __device__ __forceinline__ void chunk(const SlotDesc& d, const uint8_t* base, int warp,
-                                        int lane) {
+  __device__ __forceinline__ void chunk(const SlotDesc& d, const Shared& s, int part, int lane) {
     constexpr int P = kPitch<true>;
+    const uint32_t base = smem_u32(s.ring) + d.off;
     const int nb = __popc(d.mask);
-    const int row = lane < 16 ? min(lane, d.r0 - 1) : d.r0 + min(lane - 16, max(d.r1 - 1, 0));
-    const uint8_t* a = base + (lane >= 16 && d.r1 == 0 ? 0 : row) * P;
-    const uint8_t* b = base + (d.r0 + d.r1) * P;
-    constexpr int V = kChunkVecs / kConsumerWarps;
-#pragma unroll 2
-    for (int i = 0; i < V; ++i) {
-      const int v = warp * V + i;
-      if (v >= d.kvec) break;
-      const uint4 wv = lds_vec(a + v * 16);
-      float w[4];
-      Vec<float>::to_f32(wv, w);
+    const int row = lane < 16 || d.r1 == 0 ? min(lane, d.r0 - 1)
+                                           : d.r0 + min(lane - 16, d.r1 - 1);
+    const uint32_t a = base + row * P;
+    const uint32_t b = base + (d.r0 + d.r1) * P;
+    constexpr int V = 8;  // vectors of the row held together
+#pragma unroll 1
+    for (int v0 = part * V; v0 < d.kvec; v0 += V * kGroupWarps) {
+      float w[V][4];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        Vec<float>::to_f32(v0 + i < d.kvec ? lds_vec(a + (v0 + i) * 16) : make_uint4(0, 0, 0, 0),
+                           w[i]);
+      const int left = d.kvec - v0;
 #pragma unroll
       for (int n = 0; n < 8 * NT; ++n) {
         int slot = n;
@@ -345,10 +456,18 @@ template <int NT> struct Acc<true, NT> {
         } else if (n >= nb) {
           continue;
         }
-        float x[4];
-        Vec<float>::to_f32(lds_vec(b + slot * P + v * 16), x);
+        const uint32_t xb = b + slot * P + v0 * 16;
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[n] = fmaf(w[j], x[j], c[n]);
+        for (int i = 0; i < V; ++i) {
+          if (i < left) {
+            float x[4];
+            Vec<float>::to_f32(lds_vec(xb + i * 16), x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s4[j] = fmaf(w[i][j], x[j], s4[j]);
+          }
+        }
+        c[n] += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       }
     }
   }
@@ -369,39 +488,50 @@ __device__ __forceinline__ float red_sum(const float* red, int m, int i, int n) 
   return v;
 }
 
-// Consume slots until `tiles` tiles are done.  epilogue(desc, red) runs on all consumer
-// threads once per tile with the 8 warps' partial sums.  Returns false on abort; a warp that
-// gives up still passes the remaining barriers, so none of the others waits for it forever.
+// Consume `tiles` tiles of `chunks` slots each; `it` and `tile` count the CTA's slots and
+// tiles across phases.  epilogue(desc, red) runs on all consumer threads once per tile, with
+// the descriptor of its last slot and the 8 warps' partial sums, after the next tile's slots
+// are consumed.  A buffer of partial sums is written again only after its tile's epilogue:
+// each warp arrives for a tile after its own epilogue of the tile before, and waits for all
+// arrivals of that one first.  Returns false on abort (every wait is bounded).
 template <bool F32, int NT, typename Epi>
 __device__ __forceinline__ bool consume(const Shared& s, uint32_t& it, uint32_t& tile,
-                                        int tiles, int32_t* status, Epi&& epilogue) {
+                                        int tiles, int chunks, int32_t* status, Epi&& epilogue) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t group = warp / kGroupWarps;
+  const int part = warp % kGroupWarps;
   Acc<F32, NT> acc;
-  for (int done = 0; done < tiles;) {
-    const uint32_t slot = it % kSlots;
-    const bool ok = mbar_wait_bounded(&s.full[slot], (it / kSlots) & 1u, s.abort_flag,
+  auto finish = [&](uint32_t t) {
+    const bool ok = mbar_wait_bounded(&s.sums[t & 1u], (t >> 1) & 1u, s.abort_flag,
                                       kWaitLimitNs, status);
-    if (!__all_sync(0xffffffffu, ok)) {
-      for (; done < tiles; ++done) consumer_sync();
-      return false;
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    epilogue(s.tile[t & 1u], s.red + (t & 1u) * kRedFloats<NT>);
+    return true;
+  };
+  for (int i = 0; i < tiles; ++i, ++tile) {
+    acc.zero();
+    const uint32_t end = it + chunks;
+    bool last = false;
+    SlotDesc d;
+    for (it += (group - it) % kGroups; it < end; it += kGroups) {
+      const uint32_t slot = it % kSlots;
+      const bool ok = mbar_wait_bounded(&s.full[slot], (it / kSlots) & 1u, s.abort_flag,
+                                        kWaitLimitNs, status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      d = s.desc[slot];
+      acc.chunk(d, s, part, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.empty[slot]);
+      last = d.last != 0;
     }
-    const SlotDesc d = s.desc[slot];
-    if (d.first) acc.zero();
-    acc.chunk(d, s.ring + d.off, warp, lane);
+    it = end;
+    if (i > 0 && !finish(tile - 1)) return false;
+    acc.store(s.red + (tile & 1u) * kRedFloats<NT>, warp, lane);
+    if (last && part == 0 && lane == 0) s.tile[tile & 1u] = d;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&s.empty[slot]);
-    ++it;
-    if (d.last) {
-      // double-buffered: a buffer's readers passed the other buffer's barrier
-      float* red = s.red + (tile & 1u) * kRedFloats<NT>;
-      acc.store(red, warp, lane);
-      consumer_sync();
-      epilogue(d, red);
-      ++tile;
-      ++done;
-    }
+    if (lane == 0) mbar_arrive(&s.sums[tile & 1u]);
   }
-  return true;
+  return tiles == 0 || finish(tile - 1);
 }
 
 }  // namespace few
