@@ -53,7 +53,8 @@ typedef enum {
   MOE_ERR_WORKSPACE = 3,      /* workspace null or misaligned                             */
   MOE_ERR_CUDA = 4,           /* a CUDA runtime/driver call or a launch failed            */
   MOE_ERR_BAD_EXPERT_ID = 5,  /* device: an id outside [0, E) or repeated within a token  */
-  MOE_ERR_TIMEOUT = 6         /* device: a bounded wait ran out; the kernel returned early */
+  MOE_ERR_TIMEOUT = 6,        /* device: a bounded wait ran out; the kernel returned early */
+  MOE_ERR_BAD_ADAPTER_ID = 7  /* device: an adapter id outside [-1, n_adapters)           */
 } moe_status;
 
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
@@ -276,6 +277,48 @@ moe_status moe_forward_few(const moe_config* cfg, const void* x, const void* w_r
                            const void* shared_down, void* y, int32_t* ids_out, float* gates_out,
                            int32_t* demand_out, int32_t* offsets_out, const int32_t* n_tokens,
                            void* ws, moe_stream_t stream);
+
+/* A projection that all tokens share (a shared expert's, or the router of a dense block) with
+ * each token's own low-rank adapter beside it, for the tokens of many requests at once.     */
+typedef struct {
+  int32_t T;           /* tokens in this call (>= 1)                                     */
+  int32_t d_in, d_out; /* the projection W is [d_out, d_in]                               */
+  int32_t n_adapters;  /* adapters held (>= 1)                                            */
+  int32_t rank;        /* rank of every adapter, at most 128 (pad smaller ones with zeros) */
+  int32_t dtype;       /* moe_dtype                                                       */
+} moe_adapter_config;
+/* Supported shapes (else MOE_ERR_UNSUPPORTED): d_in, d_out and rank are multiples of 8 (bf16)
+ * or 4 (fp32); rank <= 128; T <= 2^24; T * d_in, T * d_out and d_in * d_out below 2^40.     */
+
+/* Bytes of workspace of the two calls below; 0 for an invalid config.                     */
+size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg);
+
+/* y[t] = W x[t] + scale[a] B_a (A_a x[t]) (+ addend[t]),  a = adapter_ids[t].
+ *   x           [T, d_in]                    w       [d_out, d_in]
+ *   a           [n_adapters, rank, d_in]     b       [n_adapters, d_out, rank]
+ *   scale       [n_adapters] fp32 or NULL (1)
+ *   adapter_ids [T] int32; -1: the projection alone.  Any other id outside [0, n_adapters)
+ *               counts as -1 and records MOE_ERR_BAD_ADAPTER_ID in the status word.
+ *   addend      [T, d_out] or NULL; may be y itself (the layer's output, added to in place)
+ *   y           [T, d_out] (out); must not overlap x
+ *   n_tokens    device int32 or NULL: rows 0 .. *n_tokens - 1 hold tokens (clamped to 0..T;
+ *               NULL: all T); y's rows behind them are left as they were.
+ * A_a x is summed and kept in fp32 or better than 16 bits of it, sums are fp32, y is rounded
+ * once.  x, w, a and b must be 16-byte aligned (else MOE_ERR_INVALID).                     */
+moe_status moe_adapter_linear(const moe_adapter_config* cfg, const void* x, const void* w,
+                              const void* a, const void* b, const float* scale,
+                              const int32_t* adapter_ids, const void* addend, void* y,
+                              const int32_t* n_tokens, void* ws, moe_stream_t stream);
+
+/* The first half of a SwiGLU expert with an adapter beside each projection:
+ *   h[t] = SiLU(p_gate[t]) * p_up[t],  p_*[t] = W_* x[t] + scale[a] B_*_a (A_*_a x[t])
+ * with the arguments of moe_adapter_linear for both projections ("MoE Inference Visualized",
+ * Expert Execution: down(SiLU(gate(x)) * up(x)); moe_adapter_linear is the down part).     */
+moe_status moe_adapter_gate_up(const moe_adapter_config* cfg, const void* x, const void* w_gate,
+                               const void* w_up, const void* a_gate, const void* b_gate,
+                               const void* a_up, const void* b_up, const float* scale,
+                               const int32_t* adapter_ids, void* h, const int32_t* n_tokens,
+                               void* ws, moe_stream_t stream);
 
 /* moe_forward that also records caller-created CUDA events (cudaEvent_t handles, e.g.
  * created with timing enabled) on `stream` around its kernels, for live per-kernel timing:

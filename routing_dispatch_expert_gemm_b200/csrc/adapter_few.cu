@@ -1,0 +1,301 @@
+// A projection shared by all tokens plus each token's own low-rank adapter, for at most 32
+// tokens (moe_adapter_linear, moe_adapter_gate_up):
+//   p[t] = W x_t + s_a B_a (A_a x_t),  a = adapter of token t (-1: none)
+//   linear   y[t] = p[t] (+ addend[t])         gate_up  h[t] = SiLU(p_gate[t]) * p_up[t]
+// Source: "Mixture-of-Experts: routing and capacity", Top-k and mixture (the shared expert,
+// a dense projection every token passes); "MoE Inference Visualized", Expert Execution.
+//
+// Bound by reading W once, and the used adapters' A and B.  One cooperative kernel over the
+// streaming engine of few_stream.cuh, two phases:
+//   shrink   u[t] = s_a A_a x_t: the rows of the A matrices in use, cut evenly over the CTAs,
+//            each against the tokens of its adapter only; fp32, written to the workspace.
+//   W        the rows of W, cut evenly over the CTAs, against all tokens.  Its weights follow
+//            the A rows through the ring without a pause; only the epilogue needs u, so the
+//            grid barrier between the phases is hidden behind the stream of W.  The epilogue
+//            adds B_a u in fp32 (rank FMAs per output; T * rank is far too small to bound).
+#include <algorithm>
+
+#include "few_stream.cuh"
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace {
+
+using namespace few;
+
+struct AdapterFewParams {
+  const void* x;
+  const void* w[2];
+  const void* a[2];
+  const void* b[2];
+  const float* scale;       // null: 1
+  const int32_t* ids;       // [T]
+  const void* addend;       // null: none
+  void* y;
+  const int32_t* n_tokens;  // null: all T
+  float* u;                 // [2, T, rank] scratch
+  int32_t* status;
+  GridSync sync;
+  int t0, T, d_in, d_out, n, rank;  // tokens t0 .. t0 + T - 1 of the call's (T <= 32)
+  uint32_t smem_bytes;
+};
+
+// The adapters in use, in the order of their first token.
+struct AdapterTables {
+  int32_t id[kMaxTokens];          // of each token; -1 none
+  uint32_t seg_mask[kMaxTokens];   // tokens of each adapter in use
+  int32_t seg_id[kMaxTokens];
+  int32_t seg_tok[kMaxTokens];     // where its tokens begin in tok
+  int32_t tok[kMaxTokens];         // tokens by adapter
+  int32_t nseg;
+};
+constexpr uint32_t kAdapterTableBytes = (sizeof(AdapterTables) + 15) & ~15u;
+static_assert(kCtlBytes + 2 * kRedFloats<4> * 4 + kAdapterTableBytes + kMaxSlotBytes <= kSmemBytes,
+              "the ring holds the largest slot");
+
+__device__ __forceinline__ void build_adapter_tables(const AdapterFewParams& p,
+                                                     AdapterTables& tb, int live) {
+  const int lane = threadIdx.x & 31;
+  int id = lane < live ? __ldg(p.ids + lane) : -1;
+  if (id < -1 || id >= p.n) {
+    if (blockIdx.x == 0) record_status(p.status, MOE_ERR_BAD_ADAPTER_ID);
+    id = -1;
+  }
+  const uint32_t same = __match_any_sync(0xffffffffu, id);
+  const bool leads = id >= 0 && __ffs(same) - 1 == lane;
+  const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+  const int mine = leads ? __popc(same) : 0;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int begin = __shfl_sync(0xffffffffu, incl - mine, __ffs(same) - 1);  // of my adapter
+  tb.id[lane] = id;
+  if (id >= 0) tb.tok[begin + __popc(same & ((1u << lane) - 1u))] = lane;
+  if (leads) {
+    const int s = __popc(leaders & ((1u << lane) - 1u));
+    tb.seg_mask[s] = same;
+    tb.seg_id[s] = id;
+    tb.seg_tok[s] = begin;
+  }
+  if (lane == 0) tb.nseg = __popc(leaders);
+}
+
+// sum_j u[j] B[row, j] in fp32, fixed order.
+template <typename Tin>
+__device__ __forceinline__ float expand(const Tin* b, const float* u, int rank) {
+  constexpr int VEC = Vec<Tin>::N;
+  float v = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < rank; j += VEC) {
+    float bf[VEC];
+    Vec<Tin>::to_f32(ld_vec(b + j), bf);
+#pragma unroll
+    for (int q = 0; q < VEC; q += 4) {
+      const float4 w = __ldcg(reinterpret_cast<const float4*>(u + j + q));
+      v = fmaf(bf[q], w.x, v);
+      v = fmaf(bf[q + 1], w.y, v);
+      v = fmaf(bf[q + 2], w.z, v);
+      v = fmaf(bf[q + 3], w.w, v);
+    }
+  }
+  return v;
+}
+
+template <typename Tin, int NT, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterFewParams p) {
+  constexpr bool F32 = sizeof(Tin) == 4;
+  constexpr int VEC = Vec<Tin>::N;
+  constexpr int M = PAIR ? 2 : 1;           // projections
+  constexpr int TILE = kTileRows / M;       // output rows of a tile
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Shared s = carve<NT>(smem, kAdapterTableBytes, p.smem_bytes);
+  AdapterTables& tb = *reinterpret_cast<AdapterTables*>(smem + kCtlBytes + 2 * kRedFloats<NT> * 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  init_shared(s);
+  const int live = p.n_tokens != nullptr ? min(max(max(__ldg(p.n_tokens), 0) - p.t0, 0), p.T)
+                                      : p.T;
+  if (warp == 0) build_adapter_tables(p, tb, live);
+  __syncthreads();
+  const int nseg = tb.nseg;
+  const uint32_t all = live == 32 ? 0xffffffffu : (1u << live) - 1u;
+  // this CTA's rows: of the A matrices in use ((projection, adapter, rank) order), and of W
+  int64_t a0, a1, c0, c1;
+  share(static_cast<int64_t>(M) * nseg * p.rank, &a0, &a1);
+  share(live > 0 ? p.d_out : 0, &c0, &c1);
+  const int dv = p.d_in / VEC;
+  const int chunks = (dv + kChunkVecs - 1) / kChunkVecs;
+  auto shrink_rows = [&](int64_t at) {  // rows of the shrink tile at `at`: within one matrix
+    return static_cast<int>(min(min(static_cast<int64_t>(kTileRows), a1 - at),
+                                p.rank - at % p.rank));
+  };
+
+  if (warp >= kConsumerWarps) {
+    // ------------------------------------------------------------------ producers
+    constexpr uint32_t P = kPitch<F32>;
+    const size_t xs = static_cast<size_t>(p.d_in) * sizeof(Tin);
+    const uint8_t* xb = static_cast<const uint8_t*>(p.x);
+    Producer<F32> pr(s, p.status);
+    bool go = true;
+    // a tile: n0 rows from w0, then n1 rows from w1, against the tokens of `mask`
+    auto tile = [&](const uint8_t* w0, int n0, const uint8_t* w1, int n1, uint32_t mask, int seg,
+                    int row) {
+      const uint32_t rows = n0 + n1 + __popc(mask);
+      int c = blockIdx.x % chunks;  // not all CTAs read the same token chunk at once
+      for (int i = 0; i < chunks; ++i, c = c + 1 == chunks ? 0 : c + 1) {
+        const int kv = c * kChunkVecs;
+        pr.reserve(rows * P);
+        if (pr.mine()) {
+          if (pr.ready(rows * P, 0xffffffffu) != 1) { go = false; return; }
+          const int n = min(kChunkVecs, dv - kv);
+          const uint32_t bytes = n * 16, o = kv * 16;
+          pr.open(SlotDesc{0, static_cast<int16_t>(n0), static_cast<int16_t>(n1),
+                           static_cast<int16_t>(n), i + 1 == chunks, mask, 0, seg, row},
+                  rows * bytes);
+          pr.copy_rows(pr.it, pr.head, 0, w0 + o, xs, n0, bytes);
+          pr.copy_rows(pr.it, pr.head, n0, w1 + o, xs, n1, bytes);
+          pr.copy_tokens(pr.it, pr.head, n0 + n1, xb + o, xs, mask, bytes);
+        }
+        pr.pass(rows * P);
+      }
+    };
+    for (int64_t at = a0; at < a1 && go;) {
+      const int n = shrink_rows(at), r0 = min(16, n);
+      const int seg = static_cast<int>(at / p.rank), j = static_cast<int>(at % p.rank);
+      const int m = PAIR && seg >= nseg ? 1 : 0;
+      const uint8_t* w = static_cast<const uint8_t*>(p.a[m]) +
+                         (static_cast<size_t>(tb.seg_id[seg - m * nseg]) * p.rank + j) * xs;
+      tile(w, r0, w + 16 * xs, n - r0, tb.seg_mask[seg - m * nseg], seg, j);
+      at += n;
+    }
+    for (int64_t at = c0; at < c1 && go; at += TILE) {
+      const int n = static_cast<int>(min(static_cast<int64_t>(TILE), c1 - at));
+      const uint8_t* w = static_cast<const uint8_t*>(p.w[0]) + static_cast<size_t>(at) * xs;
+      if (PAIR)
+        tile(w, n, static_cast<const uint8_t*>(p.w[1]) + static_cast<size_t>(at) * xs, n, all, 0,
+             static_cast<int>(at));
+      else
+        tile(w, min(16, n), w + 16 * xs, n - min(16, n), all, 0, static_cast<int>(at));
+    }
+    if (!go) pr.drain();
+  } else {
+    // ------------------------------------------------------------------ consumers
+    // bring this CTA's rows of the B matrices into L2 while A and W stream
+    {
+      const uint32_t bytes = static_cast<uint32_t>(c1 - c0) * p.rank * sizeof(Tin);
+      const int lines = (bytes + 127) / 128;
+      for (int i = tid; i < M * nseg * lines; i += kConsumers) {
+        const int seg = i / lines, m = PAIR && seg >= nseg ? 1 : 0;
+        const uint8_t* b =
+            static_cast<const uint8_t*>(p.b[m]) +
+            (static_cast<size_t>(tb.seg_id[seg - m * nseg]) * p.d_out + c0) * p.rank * sizeof(Tin);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(b + min((i % lines) * 128u, bytes - 1)));
+      }
+    }
+    uint32_t it = 0, tile = 0;
+    int tiles = 0;
+    for (int64_t at = a0; at < a1; ++tiles) at += shrink_rows(at);
+    bool ok = consume<F32, NT>(s, it, tile, tiles, chunks, p.status,
+                               [&](const SlotDesc& d, const float* red) {
+      const int m = PAIR && d.seg >= nseg ? 1 : 0, seg = d.seg - m * nseg;
+      const int nr = d.r0 + d.r1, nb = __popc(d.mask);
+      const float sc = p.scale != nullptr ? __ldg(p.scale + tb.seg_id[seg]) : 1.f;
+      for (int i = tid; i < kTileRows * nb; i += kConsumers) {
+        const int r = i & 31, n = i >> 5;
+        // rows 0..15 and 16..31 are the two row blocks
+        if (r < nr)
+          p.u[(static_cast<size_t>(m) * p.T + tb.tok[tb.seg_tok[seg] + n]) * p.rank + d.row + r] =
+              sc * red_sum<NT>(red, 0, r, n);
+      }
+    });
+    ok = consumer_all(ok);
+    if (tid == 0) grid_arrive(p.sync);
+    bool waited = nseg == 0;
+    const int wt = ok ? static_cast<int>((c1 - c0 + TILE - 1) / TILE) : 0;
+    ok = consume<F32, NT>(s, it, tile, wt, chunks, p.status,
+                          [&](const SlotDesc& d, const float* red) {
+      if (!waited) {  // u is complete
+        if (!grid_wait_warp(p.sync, gridDim.x, s.abort_flag, p.status)) return;
+        waited = true;
+      }
+      const int nr = PAIR ? d.r0 : d.r0 + d.r1;
+      for (int i = tid; i < TILE * live; i += kConsumers) {
+        const int r = i % TILE, t = i / TILE;
+        if (r >= nr) continue;
+        const int c = d.row + r, id = tb.id[t];
+        float v[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          v[m] = red_sum<NT>(red, m, r, t);
+          if (id >= 0)
+            v[m] += expand(static_cast<const Tin*>(p.b[m]) +
+                               (static_cast<size_t>(id) * p.d_out + c) * p.rank,
+                           p.u + (static_cast<size_t>(m) * p.T + t) * p.rank, p.rank);
+        }
+        const size_t o = static_cast<size_t>(t) * p.d_out + c;
+        float out = v[0];
+        if constexpr (PAIR) out = v[0] / (1.f + expf(-v[0])) * v[M - 1];
+        if constexpr (F32) {
+          if (!PAIR && p.addend != nullptr) out += static_cast<const float*>(p.addend)[o];
+          static_cast<float*>(p.y)[o] = out;
+        } else {
+          if (!PAIR && p.addend != nullptr)
+            out += __bfloat162float(static_cast<const __nv_bfloat16*>(p.addend)[o]);
+          static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(out);
+        }
+      }
+    });
+  }
+  __syncthreads();
+  if (tid == 0 && *s.abort_flag == 0) grid_leave(p.sync);
+}
+
+template <typename Tin, int NT, bool PAIR>
+cudaError_t launch_pair(AdapterFewParams p, cudaStream_t s) {
+  static DeviceOnce once;
+  cudaError_t e = once.run([] {
+    cudaError_t r = cudaFuncSetAttribute(adapter_few_kernel<Tin, NT, PAIR>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return r != cudaSuccess ? r : prefer_max_shared(adapter_few_kernel<Tin, NT, PAIR>);
+  });
+  if (e != cudaSuccess) return e;
+  p.smem_bytes = kSmemBytes;
+  return launch_cooperative(adapter_few_kernel<Tin, NT, PAIR>, dim3(sm_count()), dim3(kThreads),
+                            kSmemBytes, s, p);
+}
+
+template <typename Tin>
+cudaError_t launch_typed(const AdapterFewParams& p, bool pair, cudaStream_t s) {
+  if (p.T <= 8) return pair ? launch_pair<Tin, 1, true>(p, s) : launch_pair<Tin, 1, false>(p, s);
+  if (p.T <= 16) return pair ? launch_pair<Tin, 2, true>(p, s) : launch_pair<Tin, 2, false>(p, s);
+  return pair ? launch_pair<Tin, 4, true>(p, s) : launch_pair<Tin, 4, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_adapter_few(const moe_adapter_config& c, const AdapterArgs& a,
+                               const AdapterLayout& L, void* ws, cudaStream_t s) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  unsigned int* sync = reinterpret_cast<unsigned int*>(w + kWsGridSyncOffset);
+  const size_t esz = c.dtype == MOE_BF16 ? 2 : 4;
+  for (int t0 = 0; t0 < c.T; t0 += kMaxTokens) {
+    const size_t xo = static_cast<size_t>(t0) * c.d_in * esz;
+    const size_t yo = static_cast<size_t>(t0) * c.d_out * esz;
+    const AdapterFewParams p{
+        static_cast<const uint8_t*>(a.x) + xo, {a.w[0], a.w[1]}, {a.a[0], a.a[1]},
+        {a.b[0], a.b[1]}, a.scale, a.ids + t0,
+        a.addend != nullptr ? static_cast<const uint8_t*>(a.addend) + yo : nullptr,
+        static_cast<uint8_t*>(a.y) + yo, a.n_tokens, reinterpret_cast<float*>(w + L.u),
+        reinterpret_cast<int32_t*>(w), GridSync{sync, sync + 1}, t0,
+        std::min(kMaxTokens, c.T - t0), c.d_in, c.d_out, c.n_adapters, c.rank, 0};
+    const cudaError_t e = c.dtype == MOE_BF16 ? launch_typed<__nv_bfloat16>(p, a.pair, s)
+                                              : launch_typed<float>(p, a.pair, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace moe

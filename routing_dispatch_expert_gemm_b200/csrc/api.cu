@@ -147,6 +147,39 @@ moe_status ffn(const moe_config& c, const FfnArgs& f, cudaStream_t s, cudaEvent_
                                          : launch_ffn_simt(c, f, s, mid));
 }
 
+moe_status validate_adapter(const moe_adapter_config* c) {
+  if (c == nullptr) return MOE_ERR_INVALID;
+  if (c->T < 1 || c->d_in < 1 || c->d_out < 1 || c->n_adapters < 1 || c->rank < 1)
+    return MOE_ERR_INVALID;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID;
+  const int unit = c->dtype == MOE_BF16 ? 8 : 4;
+  if (c->d_in % unit != 0 || c->d_out % unit != 0 || c->rank % unit != 0 || c->rank > 128)
+    return MOE_ERR_UNSUPPORTED;
+  const int64_t limit = int64_t{1} << 40;
+  if (c->T > (1 << 24) || static_cast<int64_t>(c->T) * c->d_in >= limit ||
+      static_cast<int64_t>(c->T) * c->d_out >= limit ||
+      static_cast<int64_t>(c->d_in) * c->d_out >= limit)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+AdapterLayout adapter_layout(const moe_adapter_config& c) {
+  AdapterLayout L{};
+  L.u = kWsHeaderBytes;
+  L.total = align256(L.u + 2 * static_cast<size_t>(c.T) * c.rank * 4);
+  return L;
+}
+
+moe_status adapter_impl(const moe_adapter_config* cfg, const AdapterArgs& a, void* ws,
+                        cudaStream_t stream) {
+  MOE_TRY(validate_adapter(cfg));
+  MOE_TRY(check_ws(ws));
+  if (!a.x || !a.w[0] || !a.a[0] || !a.b[0] || !a.ids || !a.y) return MOE_ERR_INVALID;
+  if (a.pair && (!a.w[1] || !a.a[1] || !a.b[1])) return MOE_ERR_INVALID;
+  if (!aligned16({a.x, a.w[0], a.w[1], a.a[0], a.a[1], a.b[0], a.b[1]})) return MOE_ERR_INVALID;
+  return cuda_status(launch_adapter_few(*cfg, a, adapter_layout(*cfg), ws, stream));
+}
+
 moe_status record(void* const* events, int i, cudaStream_t s) {
   if (events == nullptr) return MOE_OK;
   return cuda_status(record_event(static_cast<cudaEvent_t>(events[i]), s));
@@ -232,6 +265,7 @@ const char* moe_status_string(moe_status s) {
     case MOE_ERR_CUDA: return "CUDA error";
     case MOE_ERR_BAD_EXPERT_ID: return "expert id out of range or repeated within a token";
     case MOE_ERR_TIMEOUT: return "a bounded device wait ran out";
+    case MOE_ERR_BAD_ADAPTER_ID: return "adapter id out of range";
   }
   return "unknown status";
 }
@@ -360,6 +394,32 @@ moe_status moe_forward_few(const moe_config* cfg, const void* x, const void* w_r
   const FewArgs a{x, w_router, logit_bias, w_gate, w_up, w_down, shared_gate, shared_up,
                   shared_down, y, ids_out, gates_out, demand_out, offsets_out, n_tokens};
   return cuda_status(launch_few_layer(*cfg, a, ws, stream));
+}
+
+size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg) {
+  if (validate_adapter(cfg) != MOE_OK) return 0;
+  return adapter_layout(*cfg).total;
+}
+
+moe_status moe_adapter_linear(const moe_adapter_config* cfg, const void* x, const void* w,
+                              const void* a, const void* b, const float* scale,
+                              const int32_t* adapter_ids, const void* addend, void* y,
+                              const int32_t* n_tokens, void* ws, moe_stream_t stream) {
+  return adapter_impl(cfg,
+                      AdapterArgs{x, {w, nullptr}, {a, nullptr}, {b, nullptr}, scale,
+                                  adapter_ids, addend, y, n_tokens, false},
+                      ws, stream);
+}
+
+moe_status moe_adapter_gate_up(const moe_adapter_config* cfg, const void* x, const void* w_gate,
+                               const void* w_up, const void* a_gate, const void* b_gate,
+                               const void* a_up, const void* b_up, const float* scale,
+                               const int32_t* adapter_ids, void* h, const int32_t* n_tokens,
+                               void* ws, moe_stream_t stream) {
+  return adapter_impl(cfg,
+                      AdapterArgs{x, {w_gate, w_up}, {a_gate, a_up}, {b_gate, b_up}, scale,
+                                  adapter_ids, nullptr, h, n_tokens, true},
+                      ws, stream);
 }
 
 moe_status moe_forward_profiled(const moe_config* cfg, const void* x, const void* w_router,

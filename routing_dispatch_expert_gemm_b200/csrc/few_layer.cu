@@ -184,12 +184,6 @@ __device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, int
   }
 }
 
-// This CTA's share of n rows.
-__device__ __forceinline__ void share(int64_t n, int64_t* lo, int64_t* hi) {
-  *lo = n * blockIdx.x / gridDim.x;
-  *hi = n * (blockIdx.x + 1) / gridDim.x;
-}
-
 // The tables, by the consumer threads.
 __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int live) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -141,6 +141,12 @@ __device__ __forceinline__ bool consumer_all(bool v) {
   return r != 0;
 }
 
+// This CTA's share of n rows.
+__device__ __forceinline__ void share(int64_t n, int64_t* lo, int64_t* hi) {
+  *lo = n * blockIdx.x / gridDim.x;
+  *hi = n * (blockIdx.x + 1) / gridDim.x;
+}
+
 // ---------------------------------------------------------------------------------
 // Grid barrier: counts arrivals in the workspace header (all CTAs are resident).  Both
 // words are zero between launches: the last CTA to leave clears them.

@@ -193,6 +193,25 @@ FewLayout few_layer_layout(const moe_config& c);
 bool few_layer_supported(const moe_config& c);
 cudaError_t launch_few_layer(const moe_config& c, const FewArgs& a, void* ws, cudaStream_t s);
 
+// Shared projection(s) plus low-rank adapters (adapter_few.cu, adapter_sm100.cu).
+struct AdapterArgs {
+  const void* x;       // [T, d_in]
+  const void* w[2];    // [d_out, d_in]; the second of a pair, or null
+  const void* a[2];    // [n, rank, d_in]
+  const void* b[2];    // [n, d_out, rank]
+  const float* scale;  // [n] or null
+  const int32_t* ids;  // [T]
+  const void* addend;  // [T, d_out] or null
+  void* y;             // [T, d_out]
+  const int32_t* n_tokens;
+  bool pair;           // SwiGLU of the two projections
+};
+struct AdapterLayout {
+  size_t u, total;  // byte offset of u [2, T, rank] fp32, bytes in all
+};
+cudaError_t launch_adapter_few(const moe_adapter_config& c, const AdapterArgs& a,
+                               const AdapterLayout& L, void* ws, cudaStream_t s);
+
 cudaError_t launch_debug_wait(int32_t* status, int64_t limit_ns, cudaStream_t s);
 
 // Default bound on every in-kernel wait (nanoseconds).

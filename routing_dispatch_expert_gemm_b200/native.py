@@ -17,7 +17,7 @@ MOE_OK = 0
 ABI_VERSION = 5  # moe_abi_version() of the library this binding mirrors
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID", 2: "MOE_ERR_UNSUPPORTED",
                 3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_BAD_EXPERT_ID",
-                6: "MOE_ERR_TIMEOUT"}
+                6: "MOE_ERR_TIMEOUT", 7: "MOE_ERR_BAD_ADAPTER_ID"}
 DTYPES = {"f32": 0, "bf16": 1}
 GATE_MODES = {"softmax_topk": 0, "softmax_topk_renorm": 1, "topk_softmax": 2}
 LAYOUTS = {"ragged": 0, "padded": 1}
@@ -29,7 +29,8 @@ FUSE = {"none": 0, "gather": 1, "combine": 2, "gather+combine": 3}
 EXPORTS = ("moe_capacity", "moe_max_rows", "moe_workspace_bytes", "moe_workspace_init",
            "moe_ffn_tile_shape", "moe_ffn_launches",
            "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine", "moe_forward",
-           "moe_forward_few", "moe_forward_profiled", "moe_get_device_status", "moe_debug_bounded_wait",
+           "moe_forward_few", "moe_adapter_workspace_bytes", "moe_adapter_linear",
+           "moe_adapter_gate_up", "moe_forward_profiled", "moe_get_device_status", "moe_debug_bounded_wait",
            "moe_dispatch_noalloc", "moe_routing_stats", "moe_status_string",
            "moe_abi_version")
 
@@ -65,6 +66,20 @@ def offsets_len(cfg: MoeConfig) -> int:
     return cfg.E + 2 + (cfg.E if cfg.layout == LAYOUTS["padded"] else 0)
 
 
+class MoeAdapterConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "d_in", "d_out", "n_adapters", "rank", "dtype")]
+
+    def __repr__(self):
+        return ("MoeAdapterConfig("
+                + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")")
+
+
+def make_adapter_config(T, d_in, d_out, n_adapters, rank, dtype="bf16") -> MoeAdapterConfig:
+    return MoeAdapterConfig(int(T), int(d_in), int(d_out), int(n_adapters), int(rank),
+                            DTYPES[dtype])
+
+
 class MoeRoutingSummary(ctypes.Structure):
     """moe_routing_summary; moe_routing_stats writes one into device memory."""
     _fields_ = [("aux_loss", ctypes.c_float), ("imbalance", ctypes.c_float),
@@ -84,6 +99,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _CFG = ctypes.POINTER(MoeConfig)
+_ACFG = ctypes.POINTER(MoeAdapterConfig)
 
 
 def lib() -> ctypes.CDLL:
@@ -107,6 +123,9 @@ def lib() -> ctypes.CDLL:
             "moe_combine": (_I32, [_CFG, _P, _P, _P, _P, _P, _P, _P]),
             "moe_forward": (_I32, [_CFG] + [_P] * 15 + [_P]),
             "moe_forward_few": (_I32, [_CFG] + [_P] * 16 + [_P]),
+            "moe_adapter_workspace_bytes": (ctypes.c_size_t, [_ACFG]),
+            "moe_adapter_linear": (_I32, [_ACFG] + [_P] * 10 + [_P]),
+            "moe_adapter_gate_up": (_I32, [_ACFG] + [_P] * 12 + [_P]),
             "moe_forward_profiled": (_I32, [_CFG] + [_P] * 14 + [ctypes.POINTER(_P), _I32, _P, _P]),
             "moe_get_device_status": (_I32, [_P, _P, _I32, ctypes.POINTER(_I32)]),
             "moe_debug_bounded_wait": (_I32, [_P, ctypes.c_int64, _P]),
@@ -248,6 +267,31 @@ def moe_forward_few(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, shared_g
                                      _stream(stream)), "moe_forward_few")
 
 
+def moe_adapter_workspace_bytes(cfg: MoeAdapterConfig) -> int:
+    return lib().moe_adapter_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_adapter_linear(cfg, x, w, a, b, scale, adapter_ids, addend, y, n_tokens, ws, stream=None):
+    """y[t] = w x[t] + scale * b (a x[t]) (+ addend[t]) with each token's own adapter (a, b);
+    see moe_adapter_linear in include/moe.h.  ``scale``, ``addend``, ``n_tokens`` may be None."""
+    with _on_device(x):
+        _check(lib().moe_adapter_linear(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(a), _ptr(b),
+                                        _ptr(scale), _ptr(adapter_ids), _ptr(addend), _ptr(y),
+                                        _ptr(n_tokens), _ptr(ws), _stream(stream)),
+               "moe_adapter_linear")
+
+
+def moe_adapter_gate_up(cfg, x, w_gate, w_up, a_gate, b_gate, a_up, b_up, scale, adapter_ids, h,
+                        n_tokens, ws, stream=None):
+    """h[t] = SiLU(gate[t]) * up[t], both projections with each token's own adapter."""
+    with _on_device(x):
+        _check(lib().moe_adapter_gate_up(ctypes.byref(cfg), _ptr(x), _ptr(w_gate), _ptr(w_up),
+                                         _ptr(a_gate), _ptr(b_gate), _ptr(a_up), _ptr(b_up),
+                                         _ptr(scale), _ptr(adapter_ids), _ptr(h),
+                                         _ptr(n_tokens), _ptr(ws), _stream(stream)),
+               "moe_adapter_gate_up")
+
+
 def moe_forward_profiled(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, shared_gate,
                          shared_up, shared_down, y, ids_out, gates_out, demand_out, offsets_out,
                          events, ws, stream=None):
@@ -302,4 +346,16 @@ def workspace(cfg: MoeConfig, device="cuda"):
         raise MoeError(1, "moe_workspace_bytes")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     moe_workspace_init(ws)
+    return ws
+
+
+def adapter_workspace(cfg: MoeAdapterConfig, device="cuda"):
+    """Allocate (with torch) and zero-initialise a workspace for an adapter config."""
+    import torch
+    n = moe_adapter_workspace_bytes(cfg)
+    if n == 0:
+        raise MoeError(1, "moe_adapter_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with _on_device(ws):
+        moe_workspace_init(ws)
     return ws

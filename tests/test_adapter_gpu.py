@@ -1,0 +1,253 @@
+"""Projections with per-token low-rank adapters (moe_adapter_linear, moe_adapter_gate_up)
+against a plain 64-bit implementation.
+
+Bounds.  u = 2^-24, r = eps/2 of the storage type, |.|-sums with absolute values throughout.
+An fp32 sum of n products in any order is off by at most (n + 2) u times its |.|-sum, so
+  v = A x            dv <= (d_in + 2) u |A||x|
+  s B v              dd <= |s| |B| dv + (rank + 6) u |s| |B||v| (+ 2^-16 |s| |B||v|: the
+                     tensor-core form may keep v in two bf16 halves, 16 bits in all)
+  p = W x + s B v    dp <= (d_in + 2) u |W||x| + dd + 4 u (|W||x| + |s||B||v|)
+  y = p + addend     dp + 2 u |y| + r |y|
+  h = SiLU(g) up     1.1 |up| dg + |SiLU(g)| dup + dg dup + 16 u |h| + r |h|
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def N():
+    from routing_dispatch_expert_gemm_b200 import build, native
+    build.build()
+    return native
+
+
+def make(T, d_in, d_out, n, rank, dtype="bf16", mix="tokens", seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rn(shape, std):
+        return (torch.randn(shape, generator=g, device="cuda") * std).to(DT[dtype])
+
+    p = {"x": rn((T, d_in), 1.0), "scale": torch.rand(n, generator=g, device="cuda") + 0.5,
+         "addend": rn((T, d_out), 1.0),
+         "w": [rn((d_out, d_in), 0.05) for _ in range(2)],
+         "a": [rn((n, rank, d_in), d_in ** -0.5) for _ in range(2)],
+         "b": [rn((n, d_out, rank), 0.3) for _ in range(2)]}
+    ids = torch.randint(-1, n, (T,), generator=g, device="cuda")
+    if mix == "requests":  # a few runs of tokens
+        ids = ids[(torch.arange(T, device="cuda") * 5 // T) * (T // 5 if T >= 5 else 1)]
+    elif mix == "one":
+        ids = torch.full((T,), n - 1, device="cuda")
+    elif mix == "none":
+        ids = torch.full((T,), -1, device="cuda")
+    p["ids"] = ids.to(torch.int32)
+    return p
+
+
+def projection(p, i, scale=True):
+    """p[t] and its bound, in 64 bits."""
+    x, w = p["x"].double(), p["w"][i].double()
+    d_in, rank = x.shape[1], p["a"][i].shape[1]
+    base, mag = x @ w.t(), x.abs() @ w.abs().t()
+    out, dp = base.clone(), (d_in + 6) * U * mag
+    for j in range(p["a"][i].shape[0]):
+        rows = torch.nonzero(p["ids"] == j).flatten()
+        if rows.numel() == 0:
+            continue
+        a, b = p["a"][i][j].double(), p["b"][i][j].double()
+        s = float(p["scale"][j]) if scale else 1.0
+        v = x[rows] @ a.t()
+        dv = (d_in + 2) * U * (x[rows].abs() @ a.abs().t())
+        out[rows] += s * (v @ b.t())
+        dp[rows] += s * (dv @ b.abs().t()) + ((rank + 10) * U + 2.0 ** -16) * s * (
+            (v.abs() + dv) @ b.abs().t())
+    return out, dp
+
+
+def reference(p, pair, addend=False, scale=True):
+    r = torch.finfo(p["x"].dtype).eps / 2
+    g, dg = projection(p, 0, scale)
+    if not pair:
+        y = g + (p["addend"].double() if addend else 0.0)
+        return y, (dg + (2 * U + r) * y.abs()) * 1.01 + 1e-30
+    up, du = projection(p, 1, scale)
+    s = g * torch.sigmoid(g)
+    h = s * up
+    return h, (1.1 * up.abs() * dg + s.abs() * du + 1.1 * dg * du
+               + (16 * U + r) * h.abs()) * 1.01 + 1e-30
+
+
+def call(N, p, pair, addend=False, n_tokens=None, ws=None, y=None, scale=True, status=0):
+    T, d_in = p["x"].shape
+    n, rank = p["a"][0].shape[:2]
+    d_out = p["w"][0].shape[0]
+    dtype = "bf16" if p["x"].dtype == torch.bfloat16 else "f32"
+    cfg = N.make_adapter_config(T, d_in, d_out, n, rank, dtype=dtype)
+    ws = N.adapter_workspace(cfg) if ws is None else ws
+    y = torch.full((T, d_out), 7.0, dtype=p["x"].dtype, device="cuda") if y is None else y
+    nt = None if n_tokens is None else torch.tensor([n_tokens], dtype=torch.int32, device="cuda")
+    sc = p["scale"] if scale else None
+    if pair:
+        N.moe_adapter_gate_up(cfg, p["x"], p["w"][0], p["w"][1], p["a"][0], p["b"][0], p["a"][1],
+                              p["b"][1], sc, p["ids"], y, nt, ws)
+    else:
+        N.moe_adapter_linear(cfg, p["x"], p["w"][0], p["a"][0], p["b"][0], sc, p["ids"],
+                             p["addend"] if addend else None, y, nt, ws)
+    assert N.moe_get_device_status(ws, clear=True) == status
+    return y
+
+
+def check(y, ref, live):
+    want, bound = ref
+    if live:
+        worst = ((y[:live].double() - want[:live]).abs() / bound[:live]).max()
+        assert worst <= 1.0, f"error is {float(worst):.2f} of its bound"
+    assert bool((y[live:] == 7.0).all())
+
+
+CASES = [
+    # T, d_in, d_out, adapters, rank, dtype, mix, live
+    (1, 8, 8, 1, 8, "bf16", "one", None),
+    (1, 4096, 1024, 8, 16, "bf16", "one", None),
+    (2, 520, 264, 3, 8, "bf16", "tokens", None),
+    (7, 1032, 136, 40, 24, "bf16", "tokens", 5),
+    (8, 256, 2048, 4, 128, "bf16", "requests", None),
+    (9, 512, 4744, 2, 64, "bf16", "none", None),
+    (16, 1000, 328, 16, 16, "bf16", "tokens", 16),
+    (24, 2056, 64, 1000, 16, "bf16", "tokens", None),
+    (31, 128, 5000, 5, 40, "bf16", "requests", 30),
+    (32, 72, 40, 32, 128, "bf16", "tokens", None),
+    (1, 4, 4, 1, 4, "f32", "one", None),
+    (5, 516, 132, 3, 12, "f32", "tokens", 4),
+    (13, 1028, 68, 6, 128, "f32", "tokens", None),
+    (32, 260, 500, 40, 20, "f32", "requests", None),
+    (33, 256, 128, 4, 16, "bf16", "tokens", None),
+    (64, 64, 128, 1, 8, "bf16", "one", None),
+    (65, 72, 8, 3, 8, "bf16", "tokens", 64),
+    (100, 1000, 264, 100, 40, "bf16", "tokens", 97),
+    (130, 520, 1032, 5, 128, "bf16", "requests", None),
+    (200, 4096, 512, 64, 16, "bf16", "tokens", None),
+    (257, 128, 4096, 7, 16, "bf16", "requests", 256),
+    (300, 648, 392, 3, 24, "bf16", "none", None),
+    (777, 512, 2048, 6, 32, "bf16", "requests", 700),
+    (1031, 264, 5000, 9, 16, "bf16", "tokens", None),
+    (33, 68, 36, 5, 4, "f32", "tokens", 33),
+    (77, 1000, 516, 5, 12, "f32", "tokens", 70),
+    (300, 132, 260, 3, 64, "f32", "requests", None),
+]
+
+
+@pytest.mark.parametrize("pair", [False, True], ids=["linear", "gate_up"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v) for v in c[:7]))
+def test_against_64_bits(N, case, pair):
+    T, d_in, d_out, n, rank, dtype, mix, live = case
+    p = make(T, d_in, d_out, n, rank, dtype, mix, seed=T + d_in)
+    for addend in ((False,) if pair else (False, True)):
+        y = call(N, p, pair, addend, live)
+        check(y, reference(p, pair, addend), T if live is None else live)
+
+
+@pytest.mark.parametrize("T", [6, 70])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_padding_ids_and_scale(N, T, dtype):
+    p = make(T, 256, 128, 3, 8, dtype)
+    for live, seen in ((0, 0), (-5, 0), (1, 1), (T + 9, T)):
+        for pair in (False, True):
+            check(call(N, p, pair, False, live), reference(p, pair), seen)
+    check(call(N, p, False, scale=False), reference(p, False, scale=False), T)
+    bad = dict(p, ids=p["ids"].clone())
+    bad["ids"][2], bad["ids"][4] = 3, -2  # out of range: no adapter, and flagged
+    ref = dict(p, ids=bad["ids"].clone())
+    ref["ids"][2] = ref["ids"][4] = -1
+    for pair in (False, True):
+        check(call(N, bad, pair, status=7), reference(ref, pair), T)
+    # behind the last token an id is not looked at
+    assert bool((call(N, bad, False, n_tokens=2)[2:] == 7.0).all())
+
+
+@pytest.mark.parametrize("T", [12, 150])
+def test_in_place_repeat_and_graph(N, T):
+    p = make(T, 1024, 512, 6, 16)
+    want = call(N, p, False, True)
+    y = p["addend"].clone()
+    q = dict(p, addend=y)
+    call(N, q, False, True, y=y)  # addend is y
+    assert torch.equal(y, want)
+    assert torch.equal(call(N, p, False, True), want)
+
+    cfg = N.make_adapter_config(T, 1024, 512, 6, 16)
+    back = N.make_adapter_config(T, 512, 1024, 6, 16)
+    ws = N.adapter_workspace(back)
+    down = make(T, 512, 1024, 6, 16, seed=3)
+    h, out = torch.empty((T, 512), dtype=torch.bfloat16, device="cuda"), torch.empty_like(p["x"])
+    count = torch.tensor([T], dtype=torch.int32, device="cuda")
+
+    def ffn():
+        N.moe_adapter_gate_up(cfg, p["x"], p["w"][0], p["w"][1], p["a"][0], p["b"][0], p["a"][1],
+                              p["b"][1], p["scale"], p["ids"], h, count, ws)
+        N.moe_adapter_linear(back, h, down["w"][0], down["a"][0], down["b"][0], down["scale"],
+                             p["ids"], p["x"], out, count, ws)
+
+    ffn()
+    first = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ffn()
+    for _ in range(3):
+        h.zero_()
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, first)
+    check(h, reference(p, True), T)
+    p["ids"].fill_(-1)  # the adapters of a replay are read when it runs
+    graph.replay()
+    check(h, reference(p, True), T)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.empty_like(want), N.adapter_workspace(cfg)) for _ in streams]
+    want = call(N, p, False, True)
+    for _ in range(4):
+        for s, (o, w) in zip(streams, outs):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                N.moe_adapter_linear(cfg, p["x"], p["w"][0], p["a"][0], p["b"][0], p["scale"],
+                                     p["ids"], p["addend"], o, None, w)
+    torch.cuda.synchronize()
+    for o, _ in outs:
+        assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("T", [9, 48])
+def test_layer_with_adapted_shared_expert(N, T):
+    """The layer's routed part, then the shared expert with each request's adapters, added in
+    place: what a decode step runs."""
+    d, F, E, k = 512, 256, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def rn(shape, std):
+        return (torch.randn(shape, generator=g, device="cuda") * std).bfloat16()
+
+    up, down = make(T, d, F, 4, 16, seed=1), make(T, F, d, 4, 16, seed=2)
+    x, ids = up["x"], up["ids"]
+    wr, wg, wu, wd = rn((E, d), d ** -0.5), rn((E, F, d), .05), rn((E, F, d), .05), rn((E, d, F), .05)
+    cfg = N.make_config(T, d, E, k, F, add_residual=True)
+    ws = N.workspace(cfg)
+    y = torch.empty_like(x)
+    fwd = N.moe_forward_few if T <= 32 else N.moe_forward
+    extra = (None, ws) if T <= 32 else (ws,)
+    fwd(cfg, x, wr, None, wg, wu, wd, None, None, None, y, None, None, None, None, *extra)
+    routed = y.clone()
+    c1, c2 = N.make_adapter_config(T, d, F, 4, 16), N.make_adapter_config(T, F, d, 4, 16)
+    h = torch.empty((T, F), dtype=torch.bfloat16, device="cuda")
+    aws = N.adapter_workspace(c2)
+    N.moe_adapter_gate_up(c1, x, up["w"][0], up["w"][1], up["a"][0], up["b"][0], up["a"][1],
+                          up["b"][1], up["scale"], ids, h, None, aws)
+    N.moe_adapter_linear(c2, h, down["w"][0], down["a"][0], down["b"][0], down["scale"], ids, y, y,
+                         None, aws)
+    check(h, reference(up, True), T)
+    check(y, reference(dict(down, x=h, ids=ids, addend=routed), False, True), T)
+    assert N.moe_get_device_status(ws) == 0 and N.moe_get_device_status(aws) == 0

@@ -1,0 +1,76 @@
+"""Host-side checks of the adapter projections' entry points: every call here is refused
+before anything is launched."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def native():
+    from routing_dispatch_expert_gemm_b200 import build, native
+    build.build()
+    native.lib()
+    return native
+
+
+FAKE = 1 << 20  # 16-byte aligned, never dereferenced
+WS = 1 << 12
+LINEAR = dict(x=FAKE, w=FAKE, a=FAKE, b=FAKE, scale=None, ids=FAKE, addend=None, y=FAKE,
+              n_tokens=None, ws=WS)
+PAIR = dict(x=FAKE, w_gate=FAKE, w_up=FAKE, a_gate=FAKE, b_gate=FAKE, a_up=FAKE, b_up=FAKE,
+            scale=None, ids=FAKE, h=FAKE, n_tokens=None, ws=WS)
+
+
+def linear(native, cfg, **kw):
+    args = dict(LINEAR, **kw)
+    return native.lib().moe_adapter_linear(ctypes.byref(cfg), *args.values(), None)
+
+
+def gate_up(native, cfg, **kw):
+    args = dict(PAIR, **kw)
+    return native.lib().moe_adapter_gate_up(ctypes.byref(cfg), *args.values(), None)
+
+
+SHAPE = dict(T=8, d_in=64, d_out=32, n_adapters=2, rank=8)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=0), 1), (dict(d_in=0), 1), (dict(d_out=-8), 1), (dict(n_adapters=0), 1),
+    (dict(rank=0), 1), (dict(d_in=60), 2), (dict(d_out=36), 2), (dict(rank=12), 2),
+    (dict(rank=136), 2), (dict(d_in=62, dtype="f32"), 2), (dict(rank=6, dtype="f32"), 2),
+    (dict(rank=132, dtype="f32"), 2), (dict(T=(1 << 24) + 1), 2),
+    (dict(d_in=1 << 20, d_out=1 << 20), 2), (dict(T=1 << 20, d_in=1 << 20), 2)])
+def test_shapes(native, kw, code):
+    cfg = native.make_adapter_config(**dict(SHAPE, **kw))
+    assert linear(native, cfg) == code and gate_up(native, cfg) == code
+    assert native.moe_adapter_workspace_bytes(cfg) == 0
+    with pytest.raises(native.MoeError):
+        native.adapter_workspace(cfg, device="cpu")
+
+
+def test_unknown_dtype(native):
+    cfg = native.make_adapter_config(**SHAPE)
+    cfg.dtype = 5
+    assert linear(native, cfg) == 1
+
+
+def test_pointers(native):
+    cfg = native.make_adapter_config(**SHAPE)
+    for name in ("x", "w", "a", "b", "ids", "y"):
+        assert linear(native, cfg, **{name: None}) == 1, name
+    for name in ("x", "w", "a", "b"):
+        assert linear(native, cfg, **{name: FAKE + 8}) == 1, name
+    for name in ("x", "w_gate", "w_up", "a_gate", "b_gate", "a_up", "b_up", "ids", "h"):
+        assert gate_up(native, cfg, **{name: None}) == 1, name
+    for name in ("x", "w_gate", "w_up", "a_gate", "b_gate", "a_up", "b_up"):
+        assert gate_up(native, cfg, **{name: FAKE + 4}) == 1, name
+    for call in (linear, gate_up):
+        assert call(native, cfg, ws=None) == 3 and call(native, cfg, ws=WS + 64) == 3
+    assert native.moe_status_string(7).startswith("adapter id")
+
+
+def test_workspace_holds_the_shrunk_tokens(native):
+    for T, rank in ((1, 8), (32, 128), (4099, 16)):
+        cfg = native.make_adapter_config(T, 64, 32, 2, rank)
+        assert native.moe_adapter_workspace_bytes(cfg) >= 256 + 2 * T * rank * 4
+        assert native.moe_adapter_workspace_bytes(cfg) % 256 == 0
