@@ -163,6 +163,9 @@ moe_status validate_adapter(const moe_adapter_config* c) {
   return MOE_OK;
 }
 
+// Tokens up to which the streaming kernel runs a bf16 projection.
+constexpr int kAdapterFewTokens = 32;
+
 AdapterLayout adapter_layout(const moe_adapter_config& c) {
   AdapterLayout L{};
   L.u = kWsHeaderBytes;
@@ -177,7 +180,10 @@ moe_status adapter_impl(const moe_adapter_config* cfg, const AdapterArgs& a, voi
   if (!a.x || !a.w[0] || !a.a[0] || !a.b[0] || !a.ids || !a.y) return MOE_ERR_INVALID;
   if (a.pair && (!a.w[1] || !a.a[1] || !a.b[1])) return MOE_ERR_INVALID;
   if (!aligned16({a.x, a.w[0], a.w[1], a.a[0], a.a[1], a.b[0], a.b[1]})) return MOE_ERR_INVALID;
-  return cuda_status(launch_adapter_few(*cfg, a, adapter_layout(*cfg), ws, stream));
+  const AdapterLayout L = adapter_layout(*cfg);
+  return cuda_status(cfg->dtype == MOE_BF16 && cfg->T > kAdapterFewTokens
+                         ? launch_adapter_sm100(*cfg, a, L, ws, stream)
+                         : launch_adapter_few(*cfg, a, L, ws, stream));
 }
 
 moe_status record(void* const* events, int i, cudaStream_t s) {

@@ -209,6 +209,10 @@ struct AdapterArgs {
 struct AdapterLayout {
   size_t u, total;  // byte offset of u [2, T, rank] fp32, bytes in all
 };
+// bf16, any T: shrink launch + tcgen05 GEMM.
+cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs& a,
+                                 const AdapterLayout& L, void* ws, cudaStream_t s);
+// 32 tokens per launch (one launch in the few-token range).
 cudaError_t launch_adapter_few(const moe_adapter_config& c, const AdapterArgs& a,
                                const AdapterLayout& L, void* ws, cudaStream_t s);
 
