@@ -253,6 +253,35 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
   }
 }
 
+// Totals of `cnt` tokens of one weight row over the cluster's S partial tiles, in rank order.
+// Four tokens' loads are in flight at a time.
+template <int S>
+__device__ __forceinline__ void gather_partials(const float* part, int cnt, float (&v)[kChunk]) {
+  uint32_t peer[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) peer[s] = cluster_map(part, s);
+#pragma unroll
+  for (int i0 = 0; i0 < kChunk; i0 += 4) {
+    if (i0 < cnt) {
+      float r[4][S];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+          r[i][s] = ld_cluster_f32(peer[s] + min(i0 + i, cnt - 1) * (BW * 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i0 + i] = r[i][0];
+#pragma unroll
+        for (int s = 1; s < S; ++s) v[i0 + i] += r[i][s];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i0 + i] = 0.f;
+    }
+  }
+}
+
 template <bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     adapter_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams p) {
@@ -437,24 +466,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int mid = (lo + hi + 1) / 2;  // the two warps of a row quarter share the tokens
       const int from = half == 0 ? lo : mid, to = half == 0 ? mid : hi;
       const float* part = reinterpret_cast<const float*>(ring) + quarter * 32 + lane;
-      uint32_t peer[8];
-#pragma unroll
-      for (int s = 0; s < 8; ++s) peer[s] = cluster_map(part, s < p.split ? s : 0);
 #pragma unroll 1
       for (int c0 = from; c0 < to; c0 += kChunk) {
         const int cnt = min(kChunk, to - c0);
         float v[M][kChunk];
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) {
-            v[m][i] = 0.f;
-            if (i < cnt) {
-#pragma unroll
-              for (int s = 0; s < 8; ++s)
-                if (s < p.split) v[m][i] += ld_cluster_f32(peer[s] + (m * NT + c0 + i) * BW * 4);
-            }
-          }
+        for (int m = 0; m < M; ++m) {
+          const float* at = part + (m * NT + c0) * BW;
+          if (p.split == 2) gather_partials<2>(at, cnt, v[m]);
+          else if (p.split == 4) gather_partials<4>(at, cnt, v[m]);
+          else gather_partials<8>(at, cnt, v[m]);
+        }
         finish_tokens<PAIR>(p, v, tb * NT + c0, cnt, rb * BW + quarter * 32 + lane,
                             su_all + warp * (kUBytes / 4));
       }
@@ -518,9 +540,11 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   const ShrinkParams sp{static_cast<const bf16*>(a.x),
                         {static_cast<const bf16*>(a.a[0]), static_cast<const bf16*>(a.a[1])},
                         a.scale, a.ids, a.n_tokens, u, status, c.T, c.d_in, c.n_adapters, c.rank};
-  adapter_shrink_kernel<<<dim3(tiles, deal, m), 32 * kShrinkWarps, 0, s>>>(sp);
-  cudaError_t e = cudaGetLastError();
+  static DeviceOnce once;
+  cudaError_t e = once.run([] { return prefer_max_shared(adapter_shrink_kernel); });
   if (e != cudaSuccess) return e;
+  adapter_shrink_kernel<<<dim3(tiles, deal, m), 32 * kShrinkWarps, 0, s>>>(sp);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
   GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u, a.ids,
                static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y), a.n_tokens, status,
