@@ -288,7 +288,7 @@ typedef struct {
   int32_t dtype;       /* moe_dtype                                                       */
 } moe_adapter_config;
 /* Supported shapes (else MOE_ERR_UNSUPPORTED): d_in, d_out and rank are multiples of 8 (bf16)
- * or 4 (fp32); rank <= 128; T <= 2^24; T * d_in, T * d_out and d_in * d_out below 2^40.     */
+ * or 4 (fp32); rank <= 128; T <= 2^24; d_out <= 2^20; T * d_in, T * d_out and d_in * d_out below 2^40.  */
 
 /* Bytes of workspace of the two calls below; 0 for an invalid config.                     */
 size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg);

@@ -13,8 +13,6 @@
 //            the A rows through the ring without a pause; only the epilogue needs u, so the
 //            grid barrier between the phases is hidden behind the stream of W.  The epilogue
 //            adds B_a u in fp32 (rank FMAs per output; T * rank is far too small to bound).
-#include <algorithm>
-
 #include "few_stream.cuh"
 #include "gemm_common.cuh"
 
@@ -36,7 +34,7 @@ struct AdapterFewParams {
   float* u;                 // [2, T, rank] scratch
   int32_t* status;
   GridSync sync;
-  int t0, T, d_in, d_out, n, rank;  // tokens t0 .. t0 + T - 1 of the call's (T <= 32)
+  int T, d_in, d_out, n, rank;
   uint32_t smem_bytes;
 };
 
@@ -116,8 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   init_shared(s);
-  const int live = p.n_tokens != nullptr ? min(max(max(__ldg(p.n_tokens), 0) - p.t0, 0), p.T)
-                                      : p.T;
+  const int live = p.n_tokens != nullptr ? min(max(__ldg(p.n_tokens), 0), p.T) : p.T;
   if (warp == 0) build_adapter_tables(p, tb, live);
   __syncthreads();
   const int nseg = tb.nseg;
@@ -278,24 +275,16 @@ cudaError_t launch_typed(const AdapterFewParams& p, bool pair, cudaStream_t s) {
 
 cudaError_t launch_adapter_few(const moe_adapter_config& c, const AdapterArgs& a,
                                const AdapterLayout& L, void* ws, cudaStream_t s) {
+  if (c.T > kMaxTokens) return cudaErrorInvalidValue;
   uint8_t* w = static_cast<uint8_t*>(ws);
   unsigned int* sync = reinterpret_cast<unsigned int*>(w + kWsGridSyncOffset);
-  const size_t esz = c.dtype == MOE_BF16 ? 2 : 4;
-  for (int t0 = 0; t0 < c.T; t0 += kMaxTokens) {
-    const size_t xo = static_cast<size_t>(t0) * c.d_in * esz;
-    const size_t yo = static_cast<size_t>(t0) * c.d_out * esz;
-    const AdapterFewParams p{
-        static_cast<const uint8_t*>(a.x) + xo, {a.w[0], a.w[1]}, {a.a[0], a.a[1]},
-        {a.b[0], a.b[1]}, a.scale, a.ids + t0,
-        a.addend != nullptr ? static_cast<const uint8_t*>(a.addend) + yo : nullptr,
-        static_cast<uint8_t*>(a.y) + yo, a.n_tokens, reinterpret_cast<float*>(w + L.u),
-        reinterpret_cast<int32_t*>(w), GridSync{sync, sync + 1}, t0,
-        std::min(kMaxTokens, c.T - t0), c.d_in, c.d_out, c.n_adapters, c.rank, 0};
-    const cudaError_t e = c.dtype == MOE_BF16 ? launch_typed<__nv_bfloat16>(p, a.pair, s)
-                                              : launch_typed<float>(p, a.pair, s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const AdapterFewParams p{a.x, {a.w[0], a.w[1]}, {a.a[0], a.a[1]}, {a.b[0], a.b[1]}, a.scale,
+                           a.ids, a.addend, a.y, a.n_tokens,
+                           reinterpret_cast<float*>(w + L.u), reinterpret_cast<int32_t*>(w),
+                           GridSync{sync, sync + 1}, c.T, c.d_in, c.d_out, c.n_adapters, c.rank,
+                           0};
+  return c.dtype == MOE_BF16 ? launch_typed<__nv_bfloat16>(p, a.pair, s)
+                             : launch_typed<float>(p, a.pair, s);
 }
 
 }  // namespace moe

@@ -1,0 +1,222 @@
+// Projections with per-token low-rank adapters in fp32, beyond the few-token kernel's range
+// (moe_adapter_linear, moe_adapter_gate_up):
+//   p[t] = W x_t + s_a B_a (A_a x_t);  y[t] = p[t] (+ addend[t])  or  SiLU(p_gate) * p_up
+// CUDA cores, as the fp32 expert FFN: tf32 cannot meet its tolerance.  Two launches:
+//   shrink  u[t] = s_a A_a x_t, one warp per token and four ranks.
+//   GEMM    tiles of BT tokens x BC rows of W, staged 32 columns at a time in shared memory
+//           with the next stage's loads in registers; the epilogue adds B_a u.  Bound by FMA
+//           (128 per SM and clock).  Two tile sizes: 64 x 64 (4 x 4 outputs per thread, one
+//           shared float4 load per 8 FMA) when its tiles cover the SMs, else 16 x 32 (1 x 2),
+//           which reads shared memory more often but keeps small batches on all SMs.
+#include <algorithm>
+
+#include "gemm_common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int BKF = 32;  // contraction columns per stage
+
+struct SimtParams {
+  const float* x;
+  const float* w[2];
+  const float* a[2];
+  const float* b[2];
+  const float* scale;
+  const int32_t* ids;
+  const float* addend;
+  float* y;
+  const int32_t* n_tokens;
+  float* u;
+  int32_t* status;
+  int T, d_in, d_out, n, rank;
+};
+
+__device__ __forceinline__ int live_tokens(const SimtParams& p) {
+  return p.n_tokens != nullptr ? min(max(__ldg(p.n_tokens), 0), p.T) : p.T;
+}
+
+__global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const SimtParams p) {
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int quads = p.rank / 4;  // rank is a multiple of 4
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int t = static_cast<int>(item / quads), j0 = static_cast<int>(item % quads) * 4;
+  const int m = blockIdx.y;
+  if (t >= live_tokens(p)) return;
+  const int id = __ldg(p.ids + t);
+  if (id < 0 || id >= p.n) {
+    if (id != -1 && lane == 0 && j0 == 0 && m == 0) record_status(p.status, MOE_ERR_BAD_ADAPTER_ID);
+    return;
+  }
+  const float4* x = reinterpret_cast<const float4*>(p.x + static_cast<size_t>(t) * p.d_in);
+  const float4* a = reinterpret_cast<const float4*>(
+      p.a[m] + (static_cast<size_t>(id) * p.rank + j0) * p.d_in);
+  const int dv = p.d_in / 4;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int v = lane; v < dv; v += 32) {
+    const float4 xv = __ldg(x + v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 av = __ldg(a + static_cast<size_t>(j) * dv + v);
+      s[j] = fmaf(xv.x, av.x, fmaf(xv.y, av.y, fmaf(xv.z, av.z, fmaf(xv.w, av.w, s[j]))));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+  if (lane == 0) {
+    const float sc = p.scale != nullptr ? __ldg(p.scale + id) : 1.f;
+    *reinterpret_cast<float4*>(p.u + (static_cast<size_t>(m) * p.T + t) * p.rank + j0) =
+        make_float4(sc * s[0], sc * s[1], sc * s[2], sc * s[3]);
+  }
+}
+
+template <bool PAIR, int BT, int BC, int RT, int RC>
+__global__ void __launch_bounds__(kThreads) adapter_gemm_f32_kernel(const SimtParams p) {
+  constexpr int M = PAIR ? 2 : 1;
+  constexpr int TX = BC / RC;                 // threads across the rows of W
+  constexpr int ROWS = BT + M * BC;           // rows staged: tokens, then W's
+  constexpr int LOADS = (ROWS * (BKF / 4) + kThreads - 1) / kThreads;
+  static_assert(TX * (BT / RT) == kThreads, "one micro-tile per thread");
+  // [column][row]: a thread's RT tokens and RC rows are consecutive
+  __shared__ __align__(16) float s_x[BKF][BT + 4];
+  __shared__ __align__(16) float s_w[M][BKF][BC + 4];
+  const int live = live_tokens(p);
+  const int t0 = blockIdx.x * BT, c0 = blockIdx.y * BC;
+  if (t0 >= live) return;
+  const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
+
+  float4 next[LOADS];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int at = tid + i * kThreads, row = at / (BKF / 4), k = k0 + at % (BKF / 4) * 4;
+      const float* src = nullptr;
+      if (row < BT) {
+        if (t0 + row < live) src = p.x + static_cast<size_t>(t0 + row) * p.d_in;
+      } else if (row < ROWS) {
+        const int m = (row - BT) / BC, c = c0 + (row - BT) % BC;
+        if (c < p.d_out) src = p.w[m] + static_cast<size_t>(c) * p.d_in;
+      }
+      next[i] = src != nullptr && k < p.d_in ? __ldg(reinterpret_cast<const float4*>(src + k))
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  auto stage = [&] {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int at = tid + i * kThreads, row = at / (BKF / 4), k = at % (BKF / 4) * 4;
+      if (row >= ROWS) continue;
+      const float v[4] = {next[i].x, next[i].y, next[i].z, next[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (row < BT) s_x[k + j][row] = v[j];
+        else s_w[(row - BT) / BC][k + j][(row - BT) % BC] = v[j];
+      }
+    }
+  };
+  float acc[M][RT][RC] = {};
+  fetch(0);
+  for (int k0 = 0; k0 < p.d_in; k0 += BKF) {
+    __syncthreads();
+    stage();
+    __syncthreads();
+    if (k0 + BKF < p.d_in) fetch(k0 + BKF);
+#pragma unroll 8
+    for (int k = 0; k < BKF; ++k) {
+      float xr[RT], wr[M][RC];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) xr[i] = s_x[k][ty * RT + i];
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int j = 0; j < RC; ++j) wr[m][j] = s_w[m][k][tx * RC + j];
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < RC; ++j) acc[m][i][j] = fmaf(xr[i], wr[m][j], acc[m][i][j]);
+    }
+  }
+  pdl_wait();  // u is complete; what read y before this call is done
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int t = t0 + ty * RT + i;
+    if (t >= live) continue;
+    int id = __ldg(p.ids + t);
+    if (id < 0 || id >= p.n) id = -1;
+#pragma unroll
+    for (int j = 0; j < RC; ++j) {
+      const int c = c0 + tx * RC + j;
+      if (c >= p.d_out) continue;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        if (id < 0) continue;
+        const float4* u = reinterpret_cast<const float4*>(
+            p.u + (static_cast<size_t>(m) * p.T + t) * p.rank);
+        const float4* b = reinterpret_cast<const float4*>(
+            p.b[m] + (static_cast<size_t>(id) * p.d_out + c) * p.rank);
+        float v = 0.f;
+#pragma unroll 4
+        for (int r = 0; r < p.rank / 4; ++r) {
+          const float4 uv = __ldcg(u + r), bv = __ldg(b + r);
+          v = fmaf(uv.x, bv.x, fmaf(uv.y, bv.y, fmaf(uv.z, bv.z, fmaf(uv.w, bv.w, v))));
+        }
+        acc[m][i][j] += v;
+      }
+      const size_t o = static_cast<size_t>(t) * p.d_out + c;
+      float out = acc[0][i][j];
+      if constexpr (PAIR) out = out / (1.f + expf(-out)) * acc[M - 1][i][j];
+      else if (p.addend != nullptr) out += p.addend[o];
+      p.y[o] = out;
+    }
+  }
+}
+
+template <bool PAIR, int BT, int BC, int RT, int RC>
+cudaError_t launch_tile(const SimtParams& p, cudaStream_t s) {
+  static DeviceOnce once;
+  cudaError_t e =
+      once.run([] { return prefer_max_shared(adapter_gemm_f32_kernel<PAIR, BT, BC, RT, RC>); });
+  if (e != cudaSuccess) return e;
+  // tokens on grid.x: grid.y ends at 65535 blocks
+  const int rows = (p.d_out + BC - 1) / BC;
+  if (rows > 65535) return cudaErrorInvalidValue;
+  return launch_pdl(adapter_gemm_f32_kernel<PAIR, BT, BC, RT, RC>,
+                    dim3((p.T + BT - 1) / BT, rows), dim3(kThreads), 0, s, p);
+}
+
+template <bool PAIR>
+cudaError_t launch_gemm_f32(const SimtParams& p, cudaStream_t s) {
+  const int64_t big = static_cast<int64_t>((p.d_out + 63) / 64) * ((p.T + 63) / 64);
+  return big >= sm_count() ? launch_tile<PAIR, 64, 64, 4, 4>(p, s)
+                           : launch_tile<PAIR, 16, 32, 1, 2>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_adapter_simt(const moe_adapter_config& c, const AdapterArgs& a,
+                                const AdapterLayout& L, void* ws, cudaStream_t s) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  auto f = [](const void* q) { return static_cast<const float*>(q); };
+  const SimtParams p{f(a.x), {f(a.w[0]), f(a.w[1])}, {f(a.a[0]), f(a.a[1])},
+                     {f(a.b[0]), f(a.b[1])}, a.scale, a.ids, f(a.addend),
+                     static_cast<float*>(a.y), a.n_tokens, reinterpret_cast<float*>(w + L.u),
+                     reinterpret_cast<int32_t*>(w), c.T, c.d_in, c.d_out, c.n_adapters, c.rank};
+  static DeviceOnce once;
+  cudaError_t e = once.run([] { return prefer_max_shared(adapter_shrink_f32_kernel); });
+  if (e != cudaSuccess) return e;
+  const int64_t items = static_cast<int64_t>(c.T) * (c.rank / 4);
+  adapter_shrink_f32_kernel<<<dim3(static_cast<unsigned>((items + 7) / 8), a.pair ? 2 : 1),
+                              kThreads, 0, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return a.pair ? launch_gemm_f32<true>(p, s) : launch_gemm_f32<false>(p, s);
+}
+
+}  // namespace moe

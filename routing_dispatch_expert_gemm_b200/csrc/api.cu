@@ -158,12 +158,12 @@ moe_status validate_adapter(const moe_adapter_config* c) {
   const int64_t limit = int64_t{1} << 40;
   if (c->T > (1 << 24) || static_cast<int64_t>(c->T) * c->d_in >= limit ||
       static_cast<int64_t>(c->T) * c->d_out >= limit ||
-      static_cast<int64_t>(c->d_in) * c->d_out >= limit)
+      static_cast<int64_t>(c->d_in) * c->d_out >= limit || c->d_out > (1 << 20))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
-// Tokens up to which the streaming kernel runs a bf16 projection.
+// Tokens up to which the streaming kernel runs a projection.
 constexpr int kAdapterFewTokens = 32;
 
 AdapterLayout adapter_layout(const moe_adapter_config& c) {
@@ -181,9 +181,9 @@ moe_status adapter_impl(const moe_adapter_config* cfg, const AdapterArgs& a, voi
   if (a.pair && (!a.w[1] || !a.a[1] || !a.b[1])) return MOE_ERR_INVALID;
   if (!aligned16({a.x, a.w[0], a.w[1], a.a[0], a.a[1], a.b[0], a.b[1]})) return MOE_ERR_INVALID;
   const AdapterLayout L = adapter_layout(*cfg);
-  return cuda_status(cfg->dtype == MOE_BF16 && cfg->T > kAdapterFewTokens
-                         ? launch_adapter_sm100(*cfg, a, L, ws, stream)
-                         : launch_adapter_few(*cfg, a, L, ws, stream));
+  if (cfg->T <= kAdapterFewTokens) return cuda_status(launch_adapter_few(*cfg, a, L, ws, stream));
+  return cuda_status(cfg->dtype == MOE_BF16 ? launch_adapter_sm100(*cfg, a, L, ws, stream)
+                                            : launch_adapter_simt(*cfg, a, L, ws, stream));
 }
 
 moe_status record(void* const* events, int i, cudaStream_t s) {

@@ -212,7 +212,10 @@ struct AdapterLayout {
 // bf16, any T: shrink launch + tcgen05 GEMM.
 cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs& a,
                                  const AdapterLayout& L, void* ws, cudaStream_t s);
-// 32 tokens per launch (one launch in the few-token range).
+// fp32, any T: shrink launch + CUDA-core GEMM.
+cudaError_t launch_adapter_simt(const moe_adapter_config& c, const AdapterArgs& a,
+                                const AdapterLayout& L, void* ws, cudaStream_t s);
+// At most 32 tokens, either type, one launch.
 cudaError_t launch_adapter_few(const moe_adapter_config& c, const AdapterArgs& a,
                                const AdapterLayout& L, void* ws, cudaStream_t s);
 
