@@ -4,7 +4,7 @@
 //   linear   y[t] = p[t] (+ addend[t])         gate_up  h[t] = SiLU(p_gate[t]) * p_up[t]
 //
 // Two launches, the second starting under the first (programmatic dependent launch):
-//   adapter_shrink_kernel  u[t] = s_a A_a x_t in fp32.  A CTA takes 16 consecutive tokens and
+//   adapter_shrink_kernel  u[t] = s_a A_a x_t, summed in fp32, kept as two bf16 halves.  A CTA takes 16 consecutive tokens and
 //       runs warp-level MMAs (tokens on M, ranks on N) once per adapter in use among them
 //       (dealt over grid.y when there are few CTAs), its 8 warps splitting the contraction.
 //       A and x are read straight into MMA fragments (16-byte loads; the k permutation inside
@@ -12,9 +12,13 @@
 //       the A matrices: small beside W's product, and overlapped with its start.
 //   adapter_gemm_kernel    W x on tcgen05: 128 rows of W on M, up to 256 tokens on N (128 with
 //       a second projection beside it), fp32 accumulators in TMEM, both operands by TMA.
-//       Only its epilogue waits for u.  The epilogue adds B_a u: a thread holds one row of W
-//       for 32 tokens, the token's u comes from shared memory, and B's row stays in registers
-//       while the adapter does (requests lie back to back), in fp32.
+//       B u is a few more K blocks of the same product: with u split into two bf16 halves
+//       (16 bits in all), a block holds 8 units of 8 ranks, [B_a | B_a] against the high and
+//       low halves of the tokens of adapter a and zeros for the others.  A block costs what 64
+//       columns of W cost; prompts of a few requests need one or two (fp32 FMA in the epilogue
+//       instead: T=4099, rank 16: 165 us; rank 32 gate/up T=1531: 560 us).
+//       Token blocks with more than kMaxBlockAdapters adapters, and the split form below, add
+//       B_a u in the epilogue, in fp32 FMA: a thread holds one row of W for 8 tokens.
 // With enough tiles the GEMM is persistent, the epilogue of a tile overlapping the next tile's
 // MMAs (two accumulator sets).  With few tiles (a decode batch on a small projection) a cluster
 // of 2..8 CTAs splits the contraction of one tile; the partial tiles meet in distributed
@@ -34,6 +38,7 @@ using gemm::BK;
 constexpr int kShrinkWarps = 8;
 constexpr int kShrinkTokens = 16;  // MMA rows
 constexpr int kShrinkRanks = 32;   // ranks per pass: 4 MMA column blocks
+constexpr int kMaxBlockAdapters = 64;
 
 struct ShrinkParams {
   const __nv_bfloat16* x;
@@ -41,10 +46,36 @@ struct ShrinkParams {
   const float* scale;
   const int32_t* ids;
   const int32_t* n_tokens;
-  float* u;  // [2, T, rank]
+  uint4* u;         // [2, T, rank / 8]: 8 ranks as 8 high and 8 low bf16 halves (2 vectors)
+  int32_t* blocks;  // [token blocks][1 + kMaxBlockAdapters]: adapters of each GEMM token block
   int32_t* status;
-  int T, d_in, n, rank;
+  int T, d_in, n, rank, block_tokens;
 };
+
+// Adapters of token block `tb`, by the whole CTA: their number (or kMaxBlockAdapters + 1 when
+// there are more), then the adapters in the order of their first token.
+__device__ __forceinline__ void list_block_adapters(const ShrinkParams& p, int tb, int live,
+                                                    int* s_ids, int* s_count) {
+  const int tid = threadIdx.x, t = tb * p.block_tokens + tid;
+  int id = tid < p.block_tokens && t < live ? __ldg(p.ids + t) : -1;
+  if (id < 0 || id >= p.n) id = -1;
+  s_ids[tid] = id;
+  __syncthreads();
+  bool first = id >= 0;
+  for (int i = 0; i < tid && first; ++i) first = s_ids[i] != id;
+  const uint32_t mask = __ballot_sync(0xffffffffu, first);
+  if ((tid & 31) == 0) s_count[tid >> 5] = __popc(mask);
+  __syncthreads();
+  int before = __popc(mask & ((1u << (tid & 31)) - 1u)), all = 0;
+  for (int w = 0; w < kShrinkWarps; ++w) {
+    if (w < (tid >> 5)) before += s_count[w];
+    all += s_count[w];
+  }
+  int32_t* out = p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters);
+  if (tid == 0) out[0] = min(all, kMaxBlockAdapters + 1);
+  if (first && before < kMaxBlockAdapters) out[1 + before] = id;
+  __syncthreads();
+}
 
 __device__ __forceinline__ int live_tokens(const int32_t* n_tokens, int T) {
   return n_tokens != nullptr ? min(max(__ldg(n_tokens), 0), T) : T;
@@ -66,6 +97,10 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
   const int g = lane >> 2, q = lane & 3;
   const int t0 = blockIdx.x * kShrinkTokens, m = blockIdx.z;
   const int live = live_tokens(p.n_tokens, p.T);
+  if (blockIdx.y == 0 && m == 0 && static_cast<int64_t>(blockIdx.x) * p.block_tokens < live) {
+    __shared__ int s_ids[32 * kShrinkWarps], s_count[kShrinkWarps];
+    list_block_adapters(p, blockIdx.x, live, s_ids, s_count);
+  }
   if (t0 >= live) return;
   const int nt = min(kShrinkTokens, live - t0);
   int id = lane < nt ? __ldg(p.ids + t0 + lane) : -1;
@@ -113,14 +148,25 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
         red[warp][g + 8][8 * n + 2 * q + 1] = c[n][3];
       }
       __syncthreads();
-      for (int o = threadIdx.x; o < kShrinkTokens * kShrinkRanks; o += 32 * kShrinkWarps) {
-        const int t = o / kShrinkRanks, j = o % kShrinkRanks;
-        if (((tokens >> t) & 1u) && j0 + j < p.rank) {
-          float v = 0.f;
+      // a thread: two neighbouring ranks of a token
+      const int t = threadIdx.x / (kShrinkRanks / 2), j = threadIdx.x % (kShrinkRanks / 2) * 2;
+      if (((tokens >> t) & 1u) && j0 + j < p.rank) {
+        float v[2] = {0.f, 0.f};
 #pragma unroll
-          for (int w = 0; w < kShrinkWarps; ++w) v += red[w][t][j];
-          p.u[(static_cast<size_t>(m) * p.T + t0 + t) * p.rank + j0 + j] = sc * v;
+        for (int w = 0; w < kShrinkWarps; ++w) {
+          v[0] += red[w][t][j];
+          v[1] += red[w][t][j + 1];
         }
+        v[0] *= sc;
+        v[1] *= sc;
+        const uint32_t hi = gemm::pack_bf16(v[0], v[1]);
+        const uint32_t lo = gemm::pack_bf16(v[0] - __uint_as_float(hi << 16),
+                                            v[1] - __uint_as_float(hi & 0xffff0000u));
+        uint32_t* u = reinterpret_cast<uint32_t*>(
+            p.u + ((static_cast<size_t>(m) * p.T + t0 + t) * p.rank + j0) / 4) + (j / 8) * 8 +
+            (j % 8) / 2;
+        u[0] = hi;
+        u[4] = lo;
       }
       __syncthreads();
     }
@@ -133,14 +179,20 @@ constexpr int kTokBox = 64;           // token rows per TMA box
 constexpr int kEpiWarps = 8;
 constexpr int kProducerWarp = kEpiWarps;
 constexpr int kMmaWarp = kEpiWarps + 1;
-constexpr int kGemmThreads = 32 * (kEpiWarps + 2);
+constexpr int kExtWarp0 = kEpiWarps + 2;  // two warps fill the adapters' K blocks
+constexpr int kExtThreads = 64;
+constexpr int kGemmThreads = 32 * (kEpiWarps + 2) + kExtThreads;
 constexpr int W_BYTES = BW * BK * 2;
 constexpr int kBoxBytes = kTokBox * BK * 2;
 constexpr int kMaxStages = 8;
+constexpr int kFlags = 16;
 constexpr int kRingBytes = 192 * 1024;
-constexpr int kChunk = 32;            // tokens an epilogue thread finishes together
-constexpr int kRankStep = 16;         // ranks per pass of the epilogue
-constexpr int kUBytes = kChunk * kRankStep * 4;  // per epilogue warp
+// Tokens an epilogue thread finishes together.  Small on purpose: the loops over tokens stay
+// rolled, and a launch that runs this code once reads it from a cold instruction cache (with 32
+// tokens unrolled, a one-token gate/up call took 50 us instead of 20).
+constexpr int kChunk = 8;
+constexpr int kMaxRank = 128;
+constexpr int kUBytes = kChunk * kMaxRank * 4;  // per epilogue warp
 constexpr int kGemmSmem = 1024 + kRingBytes + kEpiWarps * kUBytes + 512;
 
 template <bool PAIR> constexpr int kTileTokens = PAIR ? 128 : 256;  // MMA N at most
@@ -152,7 +204,8 @@ struct GemmMaps {
 
 struct GemmParams {
   const __nv_bfloat16* b[2];
-  const float* u;
+  const uint4* u;
+  const int32_t* blocks;
   const int32_t* ids;
   const __nv_bfloat16* addend;
   __nv_bfloat16* y;
@@ -162,87 +215,78 @@ struct GemmParams {
   int row_blocks, tok_blocks, boxes, stages, split;  // split: CTAs of a cluster per tile
 };
 
-// Adds s B u for `cnt` tokens from t0 on (row c of each projection), then finishes and stores
-// them.  v[m][i]: row c of projection m for token t0 + i.  One warp; su: its shared memory.
+// What of s B u the epilogue adds: nothing, all of it, or the products with the non-finite
+// elements of B, which the adapters' K blocks leave out (there they would reach the zeros that
+// stand for the other adapters' tokens).
+enum Expand { kExpandNone, kExpandAll, kExpandNonFinite };
+
+// Finishes and stores `cnt` tokens from t0 on (row c of each projection).  v[m][i]: row c of projection m for token t0 + i.  One warp; su: its shared memory.
 template <bool PAIR>
 __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PAIR ? 2 : 1][kChunk],
-                                              int t0, int cnt, int c, float* su) {
+                                              int t0, int cnt, int c, Expand expand, float* su) {
   constexpr int M = PAIR ? 2 : 1;
   const int lane = threadIdx.x & 31;
-  const bool row_ok = c < p.d_out;
-  int id = lane < cnt ? __ldg(p.ids + t0 + lane) : -1;
+  const int row = min(c, p.d_out - 1);  // lanes past the last row compute it again
+  int id = expand != kExpandNone && lane < cnt ? __ldg(p.ids + t0 + lane) : -1;
   if (id < 0 || id >= p.n) id = -1;
-  if (!PAIR && p.addend != nullptr && row_ok) {
-    const __nv_bfloat16* ad = p.addend + static_cast<size_t>(t0) * p.d_out + c;
+  const uint32_t with = __ballot_sync(0xffffffffu, id >= 0);
+  if (!PAIR && p.addend != nullptr) {
+    const __nv_bfloat16* ad = p.addend + static_cast<size_t>(t0) * p.d_out + row;
     __nv_bfloat16 a[kChunk];
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i)
-      a[i] = i < cnt ? ad[static_cast<size_t>(i) * p.d_out] : __nv_bfloat16(0.f);
+    for (int i = 0; i < kChunk; ++i) a[i] = ad[static_cast<size_t>(min(i, cnt - 1)) * p.d_out];
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) v[0][i] += __bfloat162float(a[i]);
   }
-  if (__ballot_sync(0xffffffffu, id >= 0) != 0) {
+  if (with != 0) {
+    // tokens without an adapter run along with the first one that has one, and add nothing
+    const int some = __shfl_sync(0xffffffffu, id, __ffs(with) - 1);
+    const int eights = p.rank / 8;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      const float* u = p.u + (static_cast<size_t>(m) * p.T + t0) * p.rank;
-      const __nv_bfloat16* brow = p.b[m] + static_cast<size_t>(min(c, p.d_out - 1)) * p.rank;
-      const size_t bstep = static_cast<size_t>(p.d_out) * p.rank;
-      for (int j0 = 0; j0 < p.rank; j0 += kRankStep) {
-        // u of the tokens into shared memory; ranks past the last one as zeros
-#pragma unroll
-        for (int k = 0; k < kChunk * kRankStep / 4 / 32; ++k) {
-          const int at = lane + 32 * k, t = at >> 2, j = j0 + (at & 3) * 4;
-          float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (t < cnt && j < p.rank)
-            w = __ldcg(reinterpret_cast<const float4*>(u + static_cast<size_t>(t) * p.rank + j));
-          reinterpret_cast<float4*>(su)[at] = w;
+      const uint4* u = p.u + (static_cast<size_t>(m) * p.T + t0) * eights * 2;
+      __syncwarp();
+      for (int at = lane; at < kChunk * eights; at += 32) {
+        const int t = at / eights;
+        float h[8] = {}, l[8] = {};
+        if ((with >> t) & 1u) {
+          Vec<__nv_bfloat16>::to_f32(__ldcg(u + 2 * at), h);
+          Vec<__nv_bfloat16>::to_f32(__ldcg(u + 2 * at + 1), l);
         }
-        __syncwarp();
-        const bool second = j0 + 8 < p.rank;
-        int cur = -1;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        float* o = su + t * kMaxRank + at % eights * 8;
 #pragma unroll
-        for (int i0 = 0; i0 < kChunk; i0 += 4) {
-          int e[4];
-          uint4 bl[4], bh[4];
-          // the four tokens' rows of B together, unless the adapter stays
+        for (int i = 0; i < 8; ++i) o[i] = h[i] + l[i];
+      }
+      __syncwarp();
+      const __nv_bfloat16* brow[kChunk];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            e[k] = __shfl_sync(0xffffffffu, id, i0 + k);
-            if (e[k] >= 0 && e[k] != cur) {
-              const __nv_bfloat16* b = brow + e[k] * bstep + j0;
-              bl[k] = ld_vec(b);
-              bh[k] = second ? ld_vec(b + 8) : make_uint4(0, 0, 0, 0);
-            } else {
-              bl[k] = lo;
-              bh[k] = hi;
-            }
+      for (int i = 0; i < kChunk; ++i) {
+        const int e = ((with >> i) & 1u) ? __shfl_sync(0xffffffffu, id, i) : some;
+        brow[i] = p.b[m] + (static_cast<size_t>(e) * p.d_out + row) * p.rank;
+      }
+#pragma unroll 1
+      for (int j0 = 0; j0 < p.rank; j0 += 8) {  // rank is a multiple of 8
+        uint4 b[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) b[i] = ld_vec(brow[i] + j0);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          float bf[8];
+          Vec<__nv_bfloat16>::to_f32(b[i], bf);
+          if (expand == kExpandNonFinite) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) bf[q] = isfinite(bf[q]) ? 0.f : bf[q];
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (e[k] < 0) continue;
-            float bf[kRankStep];
-            Vec<__nv_bfloat16>::to_f32(bl[k], bf);
-            Vec<__nv_bfloat16>::to_f32(bh[k], bf + 8);
-            const float4* uv = reinterpret_cast<const float4*>(su + (i0 + k) * kRankStep);
-            float s = 0.f;
-#pragma unroll
-            for (int j = 0; j < kRankStep / 4; ++j) {
-              const float4 w = uv[j];
-              s = fmaf(bf[4 * j], w.x, s);
-              s = fmaf(bf[4 * j + 1], w.y, s);
-              s = fmaf(bf[4 * j + 2], w.z, s);
-              s = fmaf(bf[4 * j + 3], w.w, s);
-            }
-            v[m][i0 + k] += s;
-          }
-          if (e[3] >= 0) { cur = e[3]; lo = bl[3]; hi = bh[3]; }
+          const float4* uv = reinterpret_cast<const float4*>(su + i * kMaxRank + j0);
+          const float4 w0 = uv[0], w1 = uv[1];
+          float s = fmaf(bf[0], w0.x, fmaf(bf[1], w0.y, fmaf(bf[2], w0.z, bf[3] * w0.w)));
+          s = fmaf(bf[4], w1.x, fmaf(bf[5], w1.y, fmaf(bf[6], w1.z, fmaf(bf[7], w1.w, s))));
+          if ((with >> i) & 1u) v[m][i] += s;
         }
-        __syncwarp();
       }
     }
   }
-  if (row_ok) {
+  if (c < p.d_out) {
     __nv_bfloat16* y = p.y + static_cast<size_t>(t0) * p.d_out + c;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
@@ -253,32 +297,49 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
   }
 }
 
-// Totals of `cnt` tokens of one weight row over the cluster's S partial tiles, in rank order.
-// Four tokens' loads are in flight at a time.
+// Barrier of the ext warps; whether `v` held on all of their threads.
+__device__ __forceinline__ bool ext_all(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 2, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(kExtThreads)
+      : "memory");
+  return r != 0;
+}
+// Zeros the infinities and NaNs among 8 bf16 of shared memory; whether there were any.
+__device__ __forceinline__ bool zero_nonfinite(uint8_t* p) {
+  uint4 v = *reinterpret_cast<const uint4*>(p);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) { w[i] &= 0x0000ffffu; any = true; }
+    if ((w[i] & 0x7f80u) == 0x7f80u) { w[i] &= 0xffff0000u; any = true; }
+  }
+  if (any) *reinterpret_cast<uint4*>(p) = v;
+  return any;
+}
+
+// Totals of `cnt` tokens of one weight row over the cluster's S partial tiles, in rank order,
+// all loads in flight together.
 template <int S>
 __device__ __forceinline__ void gather_partials(const float* part, int cnt, float (&v)[kChunk]) {
-  uint32_t peer[S];
+  float r[S][kChunk];
 #pragma unroll
-  for (int s = 0; s < S; ++s) peer[s] = cluster_map(part, s);
+  for (int s = 0; s < S; ++s) {
+    const uint32_t peer = cluster_map(part, s);
 #pragma unroll
-  for (int i0 = 0; i0 < kChunk; i0 += 4) {
-    if (i0 < cnt) {
-      float r[4][S];
+    for (int i = 0; i < kChunk; ++i) r[s][i] = ld_cluster_f32(peer + min(i, cnt - 1) * (BW * 4));
+  }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kChunk; ++i) {
+    v[i] = r[0][i];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-          r[i][s] = ld_cluster_f32(peer[s] + min(i0 + i, cnt - 1) * (BW * 4));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i0 + i] = r[i][0];
-#pragma unroll
-        for (int s = 1; s < S; ++s) v[i0 + i] += r[i][s];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i0 + i] = 0.f;
-    }
+    for (int s = 1; s < S; ++s) v[i] += r[s][i];
   }
 }
 
@@ -298,9 +359,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* ext_go = tempty + 2;  // a stage is the ext warps' to fill
+  uint64_t* drain = ext_go + kMaxStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // per tile of this CTA, modulo kFlags: its K blocks of adapters met a non-finite element of B
+  // (the ext warps run at most kMaxStages tiles ahead of the epilogue's two)
+  volatile int* nonfinite = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -309,7 +374,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int stage_bytes = M * W_BYTES + p.boxes * kBoxBytes;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&ext_go[s], 1);
+    }
     for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], kEpiWarps); }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -335,6 +404,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int total = p.row_blocks * tok_blocks;
   const int k_all = (p.d_in + BK - 1) / BK;
   const int k_lo = k_all * rank / p.split, k_hi = k_all * (rank + 1) / p.split;
+  // K blocks that the adapters of a token block add per projection; 0: the epilogue adds them,
+  // or there are none.  Written by the shrink kernel: after pdl_wait only.
+  const int units_per = p.rank / 8 * 2;  // 8-rank units of an adapter, high and low
+  auto ext_blocks = [&](int tb) {
+    if (p.split > 1) return 0;
+    const int n = __ldcg(p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters));
+    return n > kMaxBlockAdapters ? 0 : (n * units_per + 7) / 8;
+  };
 
   if (warp == kProducerWarp && lane == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -357,6 +434,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int i = 0; i < boxes; ++i)
           tma_load_2d(dst + M * W_BYTES + i * kBoxBytes, &maps.x, &full[stage], kb * BK,
                       tb * NT + i * kTokBox);
+        if (++stage == stages) { stage = 0; phase ^= 1u; wrapped = true; }
+      }
+      if (!ok) break;
+      pdl_wait();
+      for (int e = M * ext_blocks(tb); e > 0; --e) {  // the ext warps fill these stages
+        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs, p.status)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive(&ext_go[stage]);
         if (++stage == stages) { stage = 0; phase ^= 1u; wrapped = true; }
       }
     }
@@ -401,6 +488,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tc_commit(&empty[stage]);
         if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
+      if (ok) pdl_wait();
+      for (int e = 0, n = ok ? ext_blocks(tb) : 0; e < M * n; ++e) {
+        if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint8_t* src = ring + stage * stage_bytes;
+        const uint64_t wd = smem_desc_k_sw128(src), xd = smem_desc_k_sw128(src + M * W_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          tc_mma_bf16(d_tmem + (e >= n ? NT : 0), wd + 2 * kk, xd + 2 * kk, idesc, 1u);
+        tc_commit(&empty[stage]);
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
+      }
       if (!ok) break;
       tc_commit(&tfull[acc]);
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
@@ -409,13 +511,86 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_commit(drain);
       mbar_wait_bounded(drain, 0, nullptr, kWaitLimitNs, p.status);
     }
+  } else if (warp >= kExtWarp0 && p.split == 1) {
+    // ------------------------------------------------------------ the adapters' K blocks
+    const int et = threadIdx.x - kExtWarp0 * 32;
+    // The TMA producer, which follows every use of a stage, hands a stage over (ext_go): these
+    // warps skip the others' uses and could not tell a stage's phases apart by parity.
+    int stage = 0;
+    uint32_t go_phase = 0;  // bit s: parity of the next hand-over of stage s
+    bool ok = true;
+    pdl_wait();
+    for (int tile = first_tile, iter = 0; tile < total && ok; tile += tile_step, ++iter) {
+      const int rb = tile / tok_blocks, tb = tile - rb * tok_blocks;
+      const int n = ext_blocks(tb);
+      bool found = false;
+      stage = (stage + k_hi - k_lo) % stages;
+      if (n == 0) continue;
+      const int32_t* list = p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters);
+      const int units = __ldcg(list) * units_per;
+      const int ntok = min(NT, live - tb * NT), rows = (ntok + 15) / 16 * 16;
+      for (int e = 0; e < M * n; ++e) {
+        const int m = e >= n ? 1 : 0;
+        ok = ext_all(mbar_wait_bounded(&ext_go[stage], (go_phase >> stage) & 1u, abort_flag,
+                                       kWaitLimitNs, p.status));
+        if (!ok) break;
+        go_phase ^= 1u << stage;
+        uint8_t* dst = ring + stage * stage_bytes;
+        // this thread's 16-byte chunk of every row: unit q, in rows et / 8, et / 8 + 8, ...
+        const int j = et & 7, q = (m == 0 ? e : e - n) * 8 + j;
+        const int id = q < units ? __ldcg(list + 1 + q / units_per) : -1;
+        const int g8 = q % units_per / 2;
+        const __nv_bfloat16* b = p.b[m] + (static_cast<size_t>(max(id, 0)) * p.d_out) * p.rank +
+                                 g8 * 8;
+        for (int r = et >> 3; r < BW; r += 8) {
+          const int c = rb * BW + r;
+          cp_async_16_zfill(dst + r * 128 + ((j ^ (r & 7)) << 4),
+                            b + static_cast<size_t>(min(c, p.d_out - 1)) * p.rank,
+                            id >= 0 && c < p.d_out);
+        }
+        const uint4* u = p.u + (static_cast<size_t>(m) * p.T * (p.rank / 8) + g8) * 2 + (q & 1);
+        uint8_t* xdst = dst + M * W_BYTES;
+        for (int r = et >> 3; r < rows; r += 8) {
+          const int t = tb * NT + min(r, ntok - 1);
+          cp_async_16_zfill(xdst + r * 128 + ((j ^ (r & 7)) << 4),
+                            u + static_cast<size_t>(t) * (p.rank / 8) * 2,
+                            id >= 0 && r < ntok && __ldg(p.ids + t) == id);
+        }
+        cp_async_wait_all();
+        for (int r = et >> 3; r < BW; r += 8)  // this thread's own copies
+          found |= zero_nonfinite(dst + r * 128 + ((j ^ (r & 7)) << 4));
+        fence_proxy_async_smem();  // for the tensor core
+        found = !ext_all(!found);
+        if (et == 0) {
+          nonfinite[iter % kFlags] = found;
+          mbar_arrive(&full[stage]);
+        }
+        if (++stage == stages) stage = 0;
+      }
+    }
   } else if (warp < kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = warp >> 2;
     int acc = 0;
     uint32_t acc_phase = 0;
+    if (p.split > 1 && first_tile < total) {
+      // bring the rows of B that this CTA's share of the tokens needs into L2 meanwhile
+      const int rb = first_tile / tok_blocks, tb = first_tile - rb * tok_blocks;
+      const int ntok = min(NT, live - tb * NT), c = rb * BW + quarter * 32 + lane;
+      const int lo = ntok * rank / p.split, hi = ntok * (rank + 1) / p.split;
+      for (int t = tb * NT + lo + half; t < tb * NT + hi && c < p.d_out; t += 2) {
+        const int id = __ldg(p.ids + t);
+        if (id < 0 || id >= p.n) continue;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const __nv_bfloat16* b = p.b[m] + (static_cast<size_t>(id) * p.d_out + c) * p.rank;
+          for (int j = 0; j < p.rank; j += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(b + j));
+        }
+      }
+    }
     pdl_wait();  // u is complete; what read y before this call is done
-    for (int tile = first_tile; tile < total; tile += tile_step) {
+    for (int tile = first_tile, iter = 0; tile < total; tile += tile_step, ++iter) {
       const int rb = tile / tok_blocks, tb = tile - rb * tok_blocks;
       const int ntok = min(NT, live - tb * NT);
       int ok = 1;
@@ -424,6 +599,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
+      // the token block's adapters are in K blocks, or all of them are left to the epilogue
+      const Expand expand = ext_blocks(tb) == 0 ? kExpandAll
+                            : nonfinite[iter % kFlags] ? kExpandNonFinite : kExpandNone;
       const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                               static_cast<uint32_t>(acc * ACC_COLS);
 #pragma unroll 1
@@ -432,14 +610,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
         for (int m = 0; m < M; ++m) {
           uint32_t r[kChunk];
-          tmem_ld_32x32b_x32(t_lane + m * NT + c0, r);
+          tmem_ld_32x32b_x8(t_lane + m * NT + c0, r);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < kChunk; ++i) v[m][i] = __uint_as_float(r[i]);
         }
         if (p.split == 1) {
           finish_tokens<PAIR>(p, v, tb * NT + c0, min(kChunk, ntok - c0),
-                              rb * BW + quarter * 32 + lane, su_all + warp * (kUBytes / 4));
+                              rb * BW + quarter * 32 + lane, expand, su_all + warp * (kUBytes / 4));
         } else {  // this CTA's partial tile, token-major, over the drained ring
           float* part = reinterpret_cast<float*>(ring);
 #pragma unroll
@@ -478,7 +656,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           else gather_partials<8>(at, cnt, v[m]);
         }
         finish_tokens<PAIR>(p, v, tb * NT + c0, cnt, rb * BW + quarter * 32 + lane,
-                            su_all + warp * (kUBytes / 4));
+                            kExpandAll, su_all + warp * (kUBytes / 4));
       }
     }
     __syncwarp();
@@ -521,11 +699,17 @@ cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, cudaStream_t s) {
 
 }  // namespace
 
+size_t adapter_block_table_bytes(int T) {
+  const size_t blocks = (static_cast<size_t>(T) + kTileTokens<true> - 1) / kTileTokens<true>;
+  return blocks * (1 + kMaxBlockAdapters) * 4;
+}
+
 cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs& a,
                                  const AdapterLayout& L, void* ws, cudaStream_t s) {
   using bf16 = __nv_bfloat16;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  float* u = reinterpret_cast<float*>(w + L.u);
+  uint4* u = reinterpret_cast<uint4*>(w + L.u);
+  int32_t* blocks = reinterpret_cast<int32_t*>(w + L.blocks);
   int32_t* status = reinterpret_cast<int32_t*>(w);
   GemmMaps maps;
   bool ok = encode_2d_box(&maps.x, a.x, c.d_in, c.T, kTokBox) &&
@@ -539,14 +723,15 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   const int deal = std::max(1, std::min(kShrinkTokens, 2 * sm_count() / (tiles * m)));
   const ShrinkParams sp{static_cast<const bf16*>(a.x),
                         {static_cast<const bf16*>(a.a[0]), static_cast<const bf16*>(a.a[1])},
-                        a.scale, a.ids, a.n_tokens, u, status, c.T, c.d_in, c.n_adapters, c.rank};
+                        a.scale, a.ids, a.n_tokens, u, blocks, status, c.T, c.d_in, c.n_adapters, c.rank,
+                        a.pair ? kTileTokens<true> : kTileTokens<false>};
   static DeviceOnce once;
   cudaError_t e = once.run([] { return prefer_max_shared(adapter_shrink_kernel); });
   if (e != cudaSuccess) return e;
   adapter_shrink_kernel<<<dim3(tiles, deal, m), 32 * kShrinkWarps, 0, s>>>(sp);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
-  GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u, a.ids,
+  GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u, blocks, a.ids,
                static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y), a.n_tokens, status,
                c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, 1};
   return a.pair ? launch_gemm<true>(maps, p, s) : launch_gemm<false>(maps, p, s);

@@ -169,7 +169,8 @@ constexpr int kAdapterFewTokens = 32;
 AdapterLayout adapter_layout(const moe_adapter_config& c) {
   AdapterLayout L{};
   L.u = kWsHeaderBytes;
-  L.total = align256(L.u + 2 * static_cast<size_t>(c.T) * c.rank * 4);
+  L.blocks = align256(L.u + 2 * static_cast<size_t>(c.T) * c.rank * 4);
+  L.total = align256(L.blocks + adapter_block_table_bytes(c.T));
   return L;
 }
 

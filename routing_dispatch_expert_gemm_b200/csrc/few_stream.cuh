@@ -335,7 +335,8 @@ template <int NT> struct Acc<false, NT> {
   // One 32-wide block: two k-steps.  The k-step is the outer loop so that consecutive MMAs
   // have different accumulators (an MMA's result is 21 cycles away, its issue slot 8).
   template <bool TWO, int NB>
-  __device__ __forceinline__ void block(const uint4 (&w)[4], const uint4 (&x)[NB]) {
+  __device__ __forceinline__ static void block(float (&c)[2][NT][4], const uint4 (&w)[4],
+                                               const uint4 (&x)[NB]) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       mma_bf16(c[0][n], w[0].x, w[1].x, w[0].y, w[1].y, x[n].x, x[n].y);
@@ -369,6 +370,7 @@ template <int NT> struct Acc<false, NT> {
       if (d.scatter) row = ((d.mask >> t) & 1u) ? __popc(d.mask & ((1u << t) - 1u)) : -1;
       b[n] = row >= 0 ? base + (d.r0 + d.r1 + row) * P + at : smem_u32(s.zeros) + at;
     }
+    float part_c[2][NT][4] = {};
     constexpr int kStep = kGroupWarps * 64;                // bytes between a warp's blocks
     constexpr int kBlocks = kChunkBytes / kStep;
     constexpr int HB = NB == 4 ? 2 : 4;  // blocks loaded together, so that latencies overlap
@@ -385,7 +387,7 @@ template <int NT> struct Acc<false, NT> {
           for (int n = 0; n < NB; ++n) x[h][n] = lds_vec(b[n] + o);
         }
 #pragma unroll
-        for (int h = 0; h < HB; ++h) block<TWO, NB>(w[h], x[h]);
+        for (int h = 0; h < HB; ++h) block<TWO, NB>(part_c, w[h], x[h]);
       }
     } else {
 #pragma unroll 1
@@ -397,8 +399,19 @@ template <int NT> struct Acc<false, NT> {
         for (int j = 0; j < (TWO ? 4 : 2); ++j) w[j] = in ? lds_vec(a[j] + o) : z;
 #pragma unroll
         for (int n = 0; n < NB; ++n) x[n] = in ? lds_vec(b[n] + o) : z;
-        block<TWO, NB>(w, x);
+        block<TWO, NB>(part_c, w, x);
       }
+    }
+    // A token column that the slot does not hold stays as it is, whatever zero times the
+    // weights gave (infinities and NaNs of an expert's weights reach its own tokens only).
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const uint32_t keep = d.scatter ? d.mask >> (8 * n + 2 * q) : 3u;
+#pragma unroll
+      for (int m = 0; m < (TWO ? 2 : 1); ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((keep >> (i & 1)) & 1u) c[m][n][i] += part_c[m][n][i];
     }
   }
   template <int NB>

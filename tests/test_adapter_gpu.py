@@ -251,3 +251,36 @@ def test_layer_with_adapted_shared_expert(N, T):
     check(h, reference(up, True), T)
     check(y, reference(dict(down, x=h, ids=ids, addend=routed), False, True), T)
     assert N.moe_get_device_status(ws) == 0 and N.moe_get_device_status(aws) == 0
+
+
+@pytest.mark.parametrize("T,d_out", [(6, 64), (90, 64), (700, 5000), (700, 64)])
+def test_broken_adapter_reaches_its_own_tokens_only(N, T, d_out):
+    """Infinities and NaNs in one request's adapter, also in matrices that no token uses."""
+    for dtype in ("bf16", "f32"):
+        for mix in ("tokens", "requests"):
+            p = make(T, 128, d_out, 5, 16, dtype, mix, seed=7)
+            p["ids"][T // 2] = 2
+            clean = [call(N, p, pair) for pair in (False, True)]
+            for i in range(2):
+                p["a"][i][1, 3, 5] = float("inf")
+                p["b"][i][2, 7, 3] = float("nan")
+                p["b"][i][2, d_out - 1, 0] = float("inf")
+                p["a"][i][4].fill_(float("nan"))
+            p["ids"][p["ids"] == 1] = 0
+            p["ids"][p["ids"] == 4] = -1
+            good = p["ids"] != 2
+            for pair in (False, True):
+                q = dict(p, a=[a.clone() for a in p["a"]], b=[b.clone() for b in p["b"]])
+                for i in range(2):
+                    q["a"][i][1, 3, 5], q["b"][i][2, 7, 3], q["b"][i][2, -1, 0] = 0.0, 0.0, 0.0
+                    q["a"][i][4].fill_(0.0)
+                y = call(N, p, pair)
+                want, bound = reference(q, pair)
+                err = (y.double() - want).abs() <= bound
+                assert bool(err[good].all())
+                own = ~good
+                assert bool(torch.isnan(y[own][:, 7]).all())
+                assert not bool(torch.isfinite(y[own][:, -1]).any())
+                rest = [c for c in range(d_out) if c not in (7, d_out - 1)]
+                assert bool(err[own][:, rest].all())
+            del clean

@@ -275,3 +275,28 @@ def test_in_place_graph_and_streams(N):
     torch.cuda.synchronize()
     for o, w in outs:
         assert torch.equal(o, want) and N.moe_get_device_status(w) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [4, 15, 30])
+def test_broken_expert_reaches_its_own_tokens_only(N, T, dtype):
+    """Infinities and NaNs in an expert's weights, and in a token, stay with the tokens that
+    chose the expert and with that token."""
+    p = make(T, 256, 8, 2, 128, dtype, seed=T)
+    cfg = N.make_config(T, 256, 8, 2, 128, dtype=dtype)
+    before = call(N, cfg, p)
+    hit = (before["ids"] == 3).any(1)
+    p["w_down"][3, 5, 7], p["w_down"][3, 9, 1] = float("nan"), float("inf")
+    p["w_up"][3, 0, 0] = float("inf")
+    after = call(N, cfg, p)
+    assert torch.equal(before["ids"], after["ids"])
+    assert torch.equal(before["y"][~hit], after["y"][~hit])
+    assert not bool(torch.isfinite(after["y"][hit][:, 5]).any())
+    p = make(T, 256, 8, 2, 128, dtype, seed=T)
+    ref = reference(p, before, 2, "topk_softmax")
+    p["x"][1, 17] = float("nan")  # it routes to the first experts, which changes the others' shares
+    after = call(N, cfg, p)
+    rest = torch.arange(T, device="cuda") != 1
+    assert torch.equal(before["ids"][rest], after["ids"][rest])
+    assert bool(((after["y"].double() - ref["y"]).abs() <= ref["by"])[rest].all())
+    assert bool(torch.isnan(after["y"][1]).all())
