@@ -52,17 +52,19 @@ struct ShrinkParams {
   int T, d_in, n, rank, block_tokens;
 };
 
-// Adapters of token block `tb`, by the whole CTA: their number (or kMaxBlockAdapters + 1 when
-// there are more), then the adapters in the order of their first token.
-__device__ __forceinline__ void list_block_adapters(const ShrinkParams& p, int tb, int live,
-                                                    int* s_ids, int* s_count) {
+// Adapters of token block `tb`, by the whole CTA: their number, then the adapters in the order
+// of their first token; or kMaxBlockAdapters + 1 when the epilogue is to expand them: more than
+// the table holds, or fewer than 16 tokens each (a K block costs about 1.5 us to fill).
+__device__ __forceinline__ void list_block_adapters(const ShrinkParams& p, int tb, int live) {
+  __shared__ int s_ids[32 * kShrinkWarps], s_count[kShrinkWarps];
   const int tid = threadIdx.x, t = tb * p.block_tokens + tid;
   int id = tid < p.block_tokens && t < live ? __ldg(p.ids + t) : -1;
   if (id < 0 || id >= p.n) id = -1;
   s_ids[tid] = id;
   __syncthreads();
   bool first = id >= 0;
-  for (int i = 0; i < tid && first; ++i) first = s_ids[i] != id;
+#pragma unroll 8
+  for (int i = 0; i < tid; ++i) first = first && s_ids[i] != id;
   const uint32_t mask = __ballot_sync(0xffffffffu, first);
   if ((tid & 31) == 0) s_count[tid >> 5] = __popc(mask);
   __syncthreads();
@@ -72,9 +74,9 @@ __device__ __forceinline__ void list_block_adapters(const ShrinkParams& p, int t
     all += s_count[w];
   }
   int32_t* out = p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters);
-  if (tid == 0) out[0] = min(all, kMaxBlockAdapters + 1);
+  const bool few = all <= kMaxBlockAdapters && all * 16 <= min(p.block_tokens, live - tb * p.block_tokens);
+  if (tid == 0) out[0] = few || all == 0 ? all : kMaxBlockAdapters + 1;
   if (first && before < kMaxBlockAdapters) out[1 + before] = id;
-  __syncthreads();
 }
 
 __device__ __forceinline__ int live_tokens(const int32_t* n_tokens, int T) {
@@ -90,6 +92,41 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Partial product of one warp: its share of the contraction of 16 tokens with 8 NB ranks.
+// U 32-wide blocks are loaded before the first MMA (one at a time the loads' latency bounds).
+template <int NB>
+__device__ __forceinline__ void shrink_partial(float (&c)[4][4], const __nv_bfloat16* x0,
+                                               const __nv_bfloat16* x1, const __nv_bfloat16* ar,
+                                               int d_in, int warp, int q) {
+  constexpr int U = NB == 4 ? 2 : 4;
+  constexpr int kStep = 4 * kShrinkWarps;  // vectors between a warp's blocks
+  const int dv = d_in / 8;
+  const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int v0 = warp * 4; v0 < dv; v0 += U * kStep) {
+    uint4 a[U][2], b[U][NB];
+#pragma unroll
+    for (int h = 0; h < U; ++h) {
+      const int v = v0 + h * kStep + q;
+      const bool in = v < dv;
+      a[h][0] = in ? ld_vec(x0 + v * 8) : z;
+      a[h][1] = in ? ld_vec(x1 + v * 8) : z;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        b[h][n] = in ? ld_vec(ar + static_cast<size_t>(n) * 8 * d_in + v * 8) : z;
+    }
+#pragma unroll
+    for (int h = 0; h < U; ++h) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        mma_16816(c[n], a[h][0].x, a[h][1].x, a[h][0].y, a[h][1].y, b[h][n].x, b[h][n].y);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        mma_16816(c[n], a[h][0].z, a[h][1].z, a[h][0].w, a[h][1].w, b[h][n].z, b[h][n].w);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(const ShrinkParams p) {
   __shared__ float red[kShrinkWarps][kShrinkTokens][kShrinkRanks + 1];
   pdl_trigger();  // the GEMM may start; it waits for this grid before it reads u
@@ -97,9 +134,11 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
   const int g = lane >> 2, q = lane & 3;
   const int t0 = blockIdx.x * kShrinkTokens, m = blockIdx.z;
   const int live = live_tokens(p.n_tokens, p.T);
-  if (blockIdx.y == 0 && m == 0 && static_cast<int64_t>(blockIdx.x) * p.block_tokens < live) {
-    __shared__ int s_ids[32 * kShrinkWarps], s_count[kShrinkWarps];
-    list_block_adapters(p, blockIdx.x, live, s_ids, s_count);
+  const int tiles = (p.T + kShrinkTokens - 1) / kShrinkTokens;
+  if (blockIdx.x >= tiles) {  // the CTAs behind the token tiles list the blocks' adapters
+    const int tb = blockIdx.x - tiles;
+    if (blockIdx.y == 0 && m == 0 && tb * p.block_tokens < live) list_block_adapters(p, tb, live);
+    return;
   }
   if (t0 >= live) return;
   const int nt = min(kShrinkTokens, live - t0);
@@ -110,11 +149,9 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
   }
   const uint32_t same = __match_any_sync(0xffffffffu, id);
   uint32_t leaders = __ballot_sync(0xffffffffu, id >= 0 && __ffs(same) - 1 == lane);
-  const int dv = p.d_in / 8;
   // x rows of this lane's fragment rows (rows past the last token: the last one's, unused)
   const __nv_bfloat16* x0 = p.x + static_cast<size_t>(t0 + min(g, nt - 1)) * p.d_in;
   const __nv_bfloat16* x1 = p.x + static_cast<size_t>(t0 + min(g + 8, nt - 1)) * p.d_in;
-  const uint4 z = make_uint4(0, 0, 0, 0);
 
   for (int i = 0; leaders != 0; leaders &= leaders - 1, ++i) {
     if (i % gridDim.y != blockIdx.y) continue;  // the same for every warp
@@ -127,19 +164,10 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
       const int nb = min(4, (p.rank - j0) / 8);  // rank is a multiple of 8
       const __nv_bfloat16* ar = A + static_cast<size_t>(j0 + g) * p.d_in;
       float c[4][4] = {};
-#pragma unroll 2
-      for (int v = warp * 4 + q; v - q < dv; v += 4 * kShrinkWarps) {
-        const bool in = v < dv;
-        const uint4 a0 = in ? ld_vec(x0 + v * 8) : z, a1 = in ? ld_vec(x1 + v * 8) : z;
-        uint4 b[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          b[n] = in && n < nb ? ld_vec(ar + static_cast<size_t>(n) * 8 * p.d_in + v * 8) : z;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) mma_16816(c[n], a0.x, a1.x, a0.y, a1.y, b[n].x, b[n].y);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) mma_16816(c[n], a0.z, a1.z, a0.w, a1.w, b[n].z, b[n].w);
-      }
+      if (nb == 1) shrink_partial<1>(c, x0, x1, ar, p.d_in, warp, q);
+      else if (nb == 2) shrink_partial<2>(c, x0, x1, ar, p.d_in, warp, q);
+      else if (nb == 3) shrink_partial<3>(c, x0, x1, ar, p.d_in, warp, q);
+      else shrink_partial<4>(c, x0, x1, ar, p.d_in, warp, q);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         red[warp][g][8 * n + 2 * q] = c[n][0];
@@ -193,7 +221,7 @@ constexpr int kRingBytes = 192 * 1024;
 constexpr int kChunk = 8;
 constexpr int kMaxRank = 128;
 constexpr int kUBytes = kChunk * kMaxRank * 4;  // per epilogue warp
-constexpr int kGemmSmem = 1024 + kRingBytes + kEpiWarps * kUBytes + 512;
+constexpr int kGemmSmem = 1024 + kRingBytes + kEpiWarps * kUBytes + 512 + 256 * 4;
 
 template <bool PAIR> constexpr int kTileTokens = PAIR ? 128 : 256;  // MMA N at most
 
@@ -366,6 +394,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // per tile of this CTA, modulo kFlags: its K blocks of adapters met a non-finite element of B
   // (the ext warps run at most kMaxStages tiles ahead of the epilogue's two)
   volatile int* nonfinite = abort_flag + 1;
+  int* s_ids = reinterpret_cast<int*>(ctl + 512);  // the ext warps': adapters of their tile's tokens
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -405,7 +434,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int k_all = (p.d_in + BK - 1) / BK;
   const int k_lo = k_all * rank / p.split, k_hi = k_all * (rank + 1) / p.split;
   // K blocks that the adapters of a token block add per projection; 0: the epilogue adds them,
-  // or there are none.  Written by the shrink kernel: after pdl_wait only.
+  // or there are none (then it has nothing to add).  Written by the shrink kernel: after pdl_wait only.
   const int units_per = p.rank / 8 * 2;  // 8-rank units of an adapter, high and low
   auto ext_blocks = [&](int tb) {
     if (p.split > 1) return 0;
@@ -529,6 +558,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int32_t* list = p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters);
       const int units = __ldcg(list) * units_per;
       const int ntok = min(NT, live - tb * NT), rows = (ntok + 15) / 16 * 16;
+      // the barrier at the end of the last block has passed: the table is free
+      for (int i = et; i < rows; i += kExtThreads)
+        s_ids[i] = i < ntok ? __ldg(p.ids + tb * NT + i) : -1;
       for (int e = 0; e < M * n; ++e) {
         const int m = e >= n ? 1 : 0;
         ok = ext_all(mbar_wait_bounded(&ext_go[stage], (go_phase >> stage) & 1u, abort_flag,
@@ -542,6 +574,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int g8 = q % units_per / 2;
         const __nv_bfloat16* b = p.b[m] + (static_cast<size_t>(max(id, 0)) * p.d_out) * p.rank +
                                  g8 * 8;
+#pragma unroll 4
         for (int r = et >> 3; r < BW; r += 8) {
           const int c = rb * BW + r;
           cp_async_16_zfill(dst + r * 128 + ((j ^ (r & 7)) << 4),
@@ -550,13 +583,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         const uint4* u = p.u + (static_cast<size_t>(m) * p.T * (p.rank / 8) + g8) * 2 + (q & 1);
         uint8_t* xdst = dst + M * W_BYTES;
+#pragma unroll 4
         for (int r = et >> 3; r < rows; r += 8) {
           const int t = tb * NT + min(r, ntok - 1);
           cp_async_16_zfill(xdst + r * 128 + ((j ^ (r & 7)) << 4),
                             u + static_cast<size_t>(t) * (p.rank / 8) * 2,
-                            id >= 0 && r < ntok && __ldg(p.ids + t) == id);
+                            id >= 0 && s_ids[r] == id);
         }
         cp_async_wait_all();
+#pragma unroll 4
         for (int r = et >> 3; r < BW; r += 8)  // this thread's own copies
           found |= zero_nonfinite(dst + r * 128 + ((j ^ (r & 7)) << 4));
         fence_proxy_async_smem();  // for the tensor core
@@ -728,7 +763,8 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   static DeviceOnce once;
   cudaError_t e = once.run([] { return prefer_max_shared(adapter_shrink_kernel); });
   if (e != cudaSuccess) return e;
-  adapter_shrink_kernel<<<dim3(tiles, deal, m), 32 * kShrinkWarps, 0, s>>>(sp);
+  const int blocks_n = (c.T + sp.block_tokens - 1) / sp.block_tokens;
+  adapter_shrink_kernel<<<dim3(tiles + blocks_n, deal, m), 32 * kShrinkWarps, 0, s>>>(sp);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
   GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u, blocks, a.ids,
