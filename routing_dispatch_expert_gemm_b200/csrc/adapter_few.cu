@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
   extern __shared__ __align__(128) uint8_t smem[];
   const Shared s = carve<NT>(smem, kAdapterTableBytes, p.smem_bytes);
   AdapterTables& tb = *reinterpret_cast<AdapterTables*>(smem + kCtlBytes + 2 * kRedFloats<NT> * 4);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
 
   init_shared(s);
   const int live = p.n_tokens != nullptr ? min(max(__ldg(p.n_tokens), 0), p.T) : p.T;
@@ -120,14 +120,15 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
   const int nseg = tb.nseg;
   const uint32_t all = live == 32 ? 0xffffffffu : (1u << live) - 1u;
   // this CTA's rows: of the A matrices in use ((projection, adapter, rank) order), and of W
-  int64_t a0, a1, c0, c1;
-  share(static_cast<int64_t>(M) * nseg * p.rank, &a0, &a1);
-  share(live > 0 ? p.d_out : 0, &c0, &c1);
+  const int rows_a = M * nseg * p.rank, rows_w = live > 0 ? p.d_out : 0;
+  const int a0 = static_cast<int>(share_begin(rows_a, blockIdx.x));
+  const int a1 = static_cast<int>(share_begin(rows_a, blockIdx.x + 1));
+  const int c0 = static_cast<int>(share_begin(rows_w, blockIdx.x));
+  const int c1 = static_cast<int>(share_begin(rows_w, blockIdx.x + 1));
   const int dv = p.d_in / VEC;
   const int chunks = (dv + kChunkVecs - 1) / kChunkVecs;
-  auto shrink_rows = [&](int64_t at) {  // rows of the shrink tile at `at`: within one matrix
-    return static_cast<int>(min(min(static_cast<int64_t>(kTileRows), a1 - at),
-                                p.rank - at % p.rank));
+  auto shrink_rows = [&](int at) {  // rows of the shrink tile at `at`: within one matrix
+    return min(min(kTileRows, a1 - at), p.rank - at % p.rank);
   };
 
   if (warp >= kConsumerWarps) {
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
     bool go = true;
     // a tile: n0 rows from w0, then n1 rows from w1, against the tokens of `mask`
     auto tile = [&](const uint8_t* w0, int n0, const uint8_t* w1, int n1, uint32_t mask, int seg,
-                    int row) {
+                    int row, int kind) {
       const uint32_t rows = n0 + n1 + __popc(mask);
       int c = blockIdx.x % chunks;  // not all CTAs read the same token chunk at once
       for (int i = 0; i < chunks; ++i, c = c + 1 == chunks ? 0 : c + 1) {
@@ -150,7 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
           const int n = min(kChunkVecs, dv - kv);
           const uint32_t bytes = n * 16, o = kv * 16;
           pr.open(SlotDesc{0, static_cast<int16_t>(n0), static_cast<int16_t>(n1),
-                           static_cast<int16_t>(n), i + 1 == chunks, mask, 0, seg, row},
+                           static_cast<int16_t>(n), i + 1 == chunks,
+                           static_cast<int8_t>(kind), mask, 0, seg, row},
                   rows * bytes);
           pr.copy_rows(pr.it, pr.head, 0, w0 + o, xs, n0, bytes);
           pr.copy_rows(pr.it, pr.head, n0, w1 + o, xs, n1, bytes);
@@ -159,23 +161,37 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
         pr.pass(rows * P);
       }
     };
-    for (int64_t at = a0; at < a1 && go;) {
-      const int n = shrink_rows(at), r0 = min(16, n);
-      const int seg = static_cast<int>(at / p.rank), j = static_cast<int>(at % p.rank);
-      const int m = PAIR && seg >= nseg ? 1 : 0;
-      const uint8_t* w = static_cast<const uint8_t*>(p.a[m]) +
-                         (static_cast<size_t>(tb.seg_id[seg - m * nseg]) * p.rank + j) * xs;
-      tile(w, r0, w + 16 * xs, n - r0, tb.seg_mask[seg - m * nseg], seg, j);
-      at += n;
-    }
-    for (int64_t at = c0; at < c1 && go; at += TILE) {
-      const int n = static_cast<int>(min(static_cast<int64_t>(TILE), c1 - at));
-      const uint8_t* w = static_cast<const uint8_t*>(p.w[0]) + static_cast<size_t>(at) * xs;
-      if (PAIR)
-        tile(w, n, static_cast<const uint8_t*>(p.w[1]) + static_cast<size_t>(at) * xs, n, all, 0,
-             static_cast<int>(at));
-      else
-        tile(w, min(16, n), w + 16 * xs, n - min(16, n), all, 0, static_cast<int>(at));
+    // one loop over the tiles of both phases: the copies' code once
+    const int w_tiles = (c1 - c0 + TILE - 1) / TILE;
+#pragma unroll 1
+    for (int at = a0, i = 0; (at < a1 || i < w_tiles) && go;) {
+      const uint8_t *w0, *w1;
+      int n0, n1, seg = 0, row, kind = 0;
+      uint32_t mask = all;
+      if (at < a1) {
+        const int n = shrink_rows(at);
+        seg = at / p.rank;
+        row = at - seg * p.rank;
+        const int m = PAIR && seg >= nseg ? 1 : 0;
+        w0 = static_cast<const uint8_t*>(p.a[m]) +
+             (static_cast<size_t>(tb.seg_id[seg - m * nseg]) * p.rank + row) * xs;
+        w1 = w0 + 16 * xs;
+        n0 = min(16, n);
+        n1 = n - n0;
+        mask = tb.seg_mask[seg - m * nseg];
+        at += n;
+      } else {
+        row = c0 + i * TILE;
+        const int n = min(TILE, c1 - row);
+        w0 = static_cast<const uint8_t*>(p.w[0]) + static_cast<size_t>(row) * xs;
+        n0 = PAIR ? n : min(16, n);
+        n1 = PAIR ? n : n - n0;
+        w1 = PAIR ? static_cast<const uint8_t*>(p.w[M - 1]) + static_cast<size_t>(row) * xs
+                  : w0 + 16 * xs;
+        kind = 1;
+        ++i;
+      }
+      tile(w0, n0, w1, n1, mask, seg, row, kind);
     }
     if (!go) pr.drain();
   } else {
@@ -184,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
     {
       const uint32_t bytes = static_cast<uint32_t>(c1 - c0) * p.rank * sizeof(Tin);
       const int lines = (bytes + 127) / 128;
+#pragma unroll 1
       for (int i = tid; i < M * nseg * lines; i += kConsumers) {
         const int seg = i / lines, m = PAIR && seg >= nseg ? 1 : 0;
         const uint8_t* b =
@@ -192,33 +209,32 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
         asm volatile("prefetch.global.L2 [%0];" ::"l"(b + min((i % lines) * 128u, bytes - 1)));
       }
     }
-    uint32_t it = 0, tile = 0;
-    int tiles = 0;
-    for (int64_t at = a0; at < a1; ++tiles) at += shrink_rows(at);
-    bool ok = consume<F32, NT>(s, it, tile, tiles, chunks, p.status,
-                               [&](const SlotDesc& d, const float* red) {
-      const int m = PAIR && d.seg >= nseg ? 1 : 0, seg = d.seg - m * nseg;
-      const int nr = d.r0 + d.r1, nb = __popc(d.mask);
-      const float sc = p.scale != nullptr ? __ldg(p.scale + tb.seg_id[seg]) : 1.f;
-      for (int i = tid; i < kTileRows * nb; i += kConsumers) {
-        const int r = i & 31, n = i >> 5;
-        // rows 0..15 and 16..31 are the two row blocks
-        if (r < nr)
-          p.u[(static_cast<size_t>(m) * p.T + tb.tok[tb.seg_tok[seg] + n]) * p.rank + d.row + r] =
-              sc * red_sum<NT>(red, 0, r, n);
-      }
-    });
-    ok = consumer_all(ok);
-    if (tid == 0) grid_arrive(p.sync);
+    int a_tiles = 0;
+#pragma unroll 1
+    for (int at = a0; at < a1; ++a_tiles) at += shrink_rows(at);
+    const int tiles[2] = {a_tiles, (c1 - c0 + TILE - 1) / TILE};
+    const int n_chunks[2] = {chunks, chunks};
     bool waited = nseg == 0;
-    const int wt = ok ? static_cast<int>((c1 - c0 + TILE - 1) / TILE) : 0;
-    ok = consume<F32, NT>(s, it, tile, wt, chunks, p.status,
-                          [&](const SlotDesc& d, const float* red) {
+    auto epilogue = [&](const SlotDesc& d, const float* red) {
+      if (d.kind == 0) {
+        const int m = PAIR && d.seg >= nseg ? 1 : 0, seg = d.seg - m * nseg;
+        const int nr = d.r0 + d.r1, nb = __popc(d.mask);
+        const float sc = p.scale != nullptr ? __ldg(p.scale + tb.seg_id[seg]) : 1.f;
+#pragma unroll 1
+        for (int i = tid; i < kTileRows * nb; i += kConsumers) {
+          const int r = i & 31, n = i >> 5;
+          if (r < nr)
+            p.u[(static_cast<size_t>(m) * p.T + tb.tok[tb.seg_tok[seg] + n]) * p.rank + d.row +
+                r] = sc * red_sum<NT>(red, 0, r, n);
+        }
+        return;
+      }
       if (!waited) {  // u is complete
         if (!grid_wait_warp(p.sync, gridDim.x, s.abort_flag, p.status)) return;
         waited = true;
       }
       const int nr = PAIR ? d.r0 : d.r0 + d.r1;
+#pragma unroll 1
       for (int i = tid; i < TILE * live; i += kConsumers) {
         const int r = i % TILE, t = i / TILE;
         if (r >= nr) continue;
@@ -244,7 +260,13 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
           static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(out);
         }
       }
-    });
+    };
+    auto between = [&](bool well) {
+      well = consumer_all(well);
+      if (tid == 0) grid_arrive(p.sync);
+      return well;
+    };
+    consume<F32, NT>(s, tiles, n_chunks, p.status, epilogue, between);
   }
   __syncthreads();
   if (tid == 0 && *s.abort_flag == 0) grid_leave(p.sync);

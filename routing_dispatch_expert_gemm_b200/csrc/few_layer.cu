@@ -22,6 +22,7 @@
 //            is folded into H before it is rounded to the storage type (one rounding, as for
 //            H without the gate), the sum over experts stays in fp32 and there is no
 //            combine pass and no atomics.
+#include <climits>
 #include <cmath>
 
 #include "few_stream.cuh"
@@ -69,7 +70,8 @@ struct Tables {
   float gates[kMaxTokens * 32];    // [T, k]
   float gate_of_row[kMaxTokens * 33];
   int32_t cost[kMaxExperts + 2];   // per hidden row, summed over the segments before
-  int64_t lo, hi;                  // this CTA's (segment, hidden row) pairs of gate/up
+  int32_t lo, hi;                  // this CTA's (segment, hidden row) pairs of gate/up
+  int32_t c0, c1;                  // and its output rows of down
   int32_t nseg;
 };
 // Cost of a gate/up row pair with nb tokens: two weight rows and, per 16 pairs, nb token
@@ -98,7 +100,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Router logits: item (expert, group of tokens) per warp, spread over the grid.
 template <typename Tin>
 __device__ __forceinline__ void router_logits(const FewParams& p, int live) {
-  constexpr int VEC = Vec<Tin>::N;
+  constexpr int VEC = Vec<Tin>::N, U = 4;  // vectors in flight per lane and operand
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = gridDim.x * kConsumerWarps;
   const int per = (live * p.E <= warps) ? 1 : (live * p.E <= 2 * warps) ? 2 : 4;
@@ -107,31 +109,32 @@ __device__ __forceinline__ void router_logits(const FewParams& p, int live) {
   // neighbouring items on different SMs
   for (int item = warp * gridDim.x + blockIdx.x; item < p.E * groups; item += warps) {
     const int e = item % p.E, t0 = (item / p.E) * per;
-    const int nt = min(per, live - t0);
     const Tin* w = static_cast<const Tin*>(p.w_router) + static_cast<size_t>(e) * p.d;
-    const Tin* x = static_cast<const Tin*>(p.x) + static_cast<size_t>(t0) * p.d;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int v = lane; v < nv; v += 32) {
-      float wf[VEC];
-      Vec<Tin>::to_f32(ld_vec(w + v * VEC), wf);
+    const float bias = p.bias != nullptr ? __ldg(p.bias + e) : 0.f;
+#pragma unroll 1
+    for (int t = t0; t < min(t0 + per, live); ++t) {  // W_r's row stays in L1
+      const Tin* x = static_cast<const Tin*>(p.x) + static_cast<size_t>(t) * p.d;
+      float acc = 0.f;
+#pragma unroll 1
+      for (int v0 = lane; v0 < nv; v0 += 32 * U) {
+        uint4 wv[U], xv[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i < nt) {
-          float xf[VEC];
-          Vec<Tin>::to_f32(ld_vec(x + static_cast<size_t>(i) * p.d + v * VEC), xf);
+        for (int h = 0; h < U; ++h) {
+          const int v = v0 + 32 * h;
+          wv[h] = v < nv ? ld_vec(w + v * VEC) : make_uint4(0, 0, 0, 0);
+          xv[h] = v < nv ? ld_vec(x + v * VEC) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-          for (int q = 0; q < VEC; ++q) acc[i] = fmaf(xf[q], wf[q], acc[i]);
+        for (int h = 0; h < U; ++h) {
+          float wf[VEC], xf[VEC];
+          Vec<Tin>::to_f32(wv[h], wf);
+          Vec<Tin>::to_f32(xv[h], xf);
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) acc = fmaf(xf[q], wf[q], acc);
         }
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < nt) {
-        const float z = warp_sum(acc[i]);
-        if (lane == 0)
-          p.logits[(t0 + i) * p.E + e] = z + (p.bias != nullptr ? __ldg(p.bias + e) : 0.f);
-      }
+      acc = warp_sum(acc);
+      if (lane == 0) p.logits[t * p.E + e] = acc + bias;
     }
   }
 }
@@ -150,6 +153,7 @@ __device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, int
   uint32_t taken = 0;
   float sel_z = -INFINITY;
   int sel_e = 0;
+#pragma unroll 1
   for (int j = 0; j < p.k; ++j) {
     uint32_t best = 0;
     int be = 0x7fffffff;
@@ -240,7 +244,7 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
       }
       tb.nseg = nseg;
       tb.cost[nseg] = cost;
-      tb.lo = tb.hi = static_cast<int64_t>(nseg) * p.F;  // the end, unless a segment has it
+      tb.lo = tb.hi = nseg * p.F;  // the end, unless a segment has it
       if (blockIdx.x == 0 && p.offsets_out != nullptr) {
         p.offsets_out[p.E] = rows;
         p.offsets_out[p.E + 1] = total;
@@ -251,14 +255,18 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
   consumer_sync();
   // equal cost for every CTA: where this one's share of the pairs begins and ends
   const int64_t sum = static_cast<int64_t>(tb.cost[tb.nseg]) * p.F;
-  int64_t from, to;
-  share(sum, &from, &to);
+  const int64_t from = share_begin(sum, blockIdx.x), to = share_begin(sum, blockIdx.x + 1);
+  if (tid == 0) {
+    tb.c0 = static_cast<int>(share_begin(p.d, blockIdx.x));
+    tb.c1 = static_cast<int>(share_begin(p.d, blockIdx.x + 1));
+  }
   for (int s = tid; s < tb.nseg; s += kConsumers) {
     const int64_t a = static_cast<int64_t>(tb.cost[s]) * p.F;
     const int64_t b = static_cast<int64_t>(tb.cost[s + 1]) * p.F;
     const int w = tb.cost[s + 1] - tb.cost[s];
-    if (from >= a && from < b) tb.lo = static_cast<int64_t>(s) * p.F + (from - a) / w;
-    if (to >= a && to < b) tb.hi = static_cast<int64_t>(s) * p.F + (to - a) / w;
+    // (from - a) / w < F fits 32 bits: (E + 1) F < 2^31
+    if (from >= a && from < b) tb.lo = s * p.F + static_cast<int>((from - a) / w);
+    if (to >= a && to < b) tb.hi = s * p.F + static_cast<int>((to - a) / w);
   }
   // gate of each kept route's H row
   for (int s = warp; s < tb.nseg; s += kConsumerWarps) {
@@ -266,12 +274,14 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
     const uint32_t m = tb.seg_mask[s];
     if (e < p.E && ((m >> lane) & 1u)) {
       float g = 0.f;
+#pragma unroll 1
       for (int j = 0; j < p.k; ++j)
         if (tb.ids[lane * p.k + j] == e) g = tb.gates[lane * p.k + j];
       tb.gate_of_row[tb.seg_hrow[s] + __popc(m & ((1u << lane) - 1u))] = g;
     }
   }
   if (blockIdx.x == 0)
+#pragma unroll 1
     for (int i = tid; i < live * p.k; i += kConsumers) {
       if (p.ids_out != nullptr) p.ids_out[i] = tb.ids[i];
       if (p.gates_out != nullptr) p.gates_out[i] = tb.gates[i];
@@ -313,13 +323,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     consumer_sync();
     ok = *s.abort_flag == 0;  // written before the barrier: the same for all
     if (ok) build_tables(p, tb, live);
-    else if (tid == 0) tb.nseg = 0;
+    else if (tid == 0) tb.nseg = tb.c0 = tb.c1 = 0;
   }
   __syncthreads();
   const int nseg = tb.nseg;
-  const int64_t g0 = nseg > 0 ? tb.lo : 0, g1 = nseg > 0 ? tb.hi : 0;
-  int64_t c0, c1;
-  share(p.d, &c0, &c1);
+  const int g0 = nseg > 0 ? tb.lo : 0, g1 = nseg > 0 ? tb.hi : 0;
+  const int c0 = tb.c0, c1 = tb.c1;
   const int dv = p.d / VEC, fv = p.F / VEC;  // 16-byte vectors of a row
 
   if (warp >= kConsumerWarps) {
@@ -329,10 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     const size_t hs = static_cast<size_t>(p.F) * sizeof(Tin);  // bytes of a row of F
     Producer<F32> pr(s, p.status);
     bool go = *s.abort_flag == 0;
-    for (int64_t at = g0; at < g1 && go;) {
-      const int seg = static_cast<int>(at / p.F), f0 = static_cast<int>(at % p.F);
-      const int np = static_cast<int>(min(min(static_cast<int64_t>(16), g1 - at),
-                                          static_cast<int64_t>(p.F - f0)));
+    for (int at = g0; at < g1 && go;) {
+      const int seg = at / p.F, f0 = at - seg * p.F;
+      const int np = min(min(16, g1 - at), p.F - f0);
       const int e = tb.seg_e[seg];
       const uint32_t mask = tb.seg_mask[seg];
       const uint32_t rows = 2 * np + __popc(mask);
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
           const int n = min(kChunkVecs, dv - kv);
           const uint32_t bytes = n * 16, o = kv * 16;
           pr.open(SlotDesc{0, static_cast<int16_t>(np), static_cast<int16_t>(np),
-                           static_cast<int16_t>(n), i + 1 == chunks, mask, 0, seg, f0},
+                           static_cast<int16_t>(n), i + 1 == chunks, 0, mask, 0, seg, f0},
                   rows * bytes);
           pr.copy_rows(pr.it, pr.head, 0, wg + o, xs, np, bytes);
           pr.copy_rows(pr.it, pr.head, np, wu + o, xs, np, bytes);
@@ -368,8 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     uint32_t h_it = first;
     const int fch = (fv + kChunkVecs - 1) / kChunkVecs, pairs = fch * nseg;
     const int turn = static_cast<int>(static_cast<int64_t>(pairs) * blockIdx.x / gridDim.x);
-    DownPos w{static_cast<int>(c0), static_cast<int>(min(static_cast<int64_t>(kTileRows),
-                                                         c1 - c0)),
+    DownPos w{c0, min(kTileRows, c1 - c0),
               turn / fch, turn % fch * kChunkVecs, pairs};
     DownPos b = w;
     auto next = [&](DownPos& q) {
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
       if (--q.left > 0) return;
       q.left = pairs;  // back at the turn: the next tile
       q.row += q.nrows;
-      q.nrows = min(kTileRows, static_cast<int>(c1) - q.row);
+      q.nrows = min(kTileRows, c1 - q.row);
     };
     auto load_h = [&](const DownPos& q, uint32_t it) {
       const int nb = __popc(tb.seg_mask[q.seg]);
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
                             ((sh ? 0 : static_cast<size_t>(e) * p.d) + w.row) * hs + w.kv * 16;
         const int r0 = min(16, w.nrows);
         pr.open(SlotDesc{0, static_cast<int16_t>(r0), static_cast<int16_t>(w.nrows - r0),
-                         static_cast<int16_t>(n), w.left == 1, mask, 1, w.seg, w.row},
+                         static_cast<int16_t>(n), w.left == 1, 1, mask, 1, w.seg, w.row},
                 rows * n * 16);
         pr.copy_rows(pr.it, pr.head, 0, wd, hs, w.nrows, n * 16);
         if (passed) load_h(w, pr.it);
@@ -433,28 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     }
   } else {
     // ------------------------------------------------------------------ consumers
-    uint32_t it = 0, tile = 0;
-    int tiles = 0;
-    for (int64_t at = g0; at < g1; ++tiles)
-      at += min(min(static_cast<int64_t>(16), g1 - at), p.F - at % p.F);
-    ok = consume<F32, NT>(s, it, tile, ok ? tiles : 0, (dv + kChunkVecs - 1) / kChunkVecs,
-                          p.status, [&](const SlotDesc& d,
-                                                                     const float* red) {
-      const int nb = __popc(d.mask), hrow = tb.seg_hrow[d.seg];
-      for (int i = tid; i < 16 * nb; i += kConsumers) {
-        const int r = i & 15, n = i >> 4;
-        if (r >= d.r0) continue;
-        const float g = red_sum<NT>(red, 0, r, n), u = red_sum<NT>(red, 1, r, n);
-        const float v = g / (1.f + expf(-g)) * u * tb.gate_of_row[hrow + n];
-        Tin* o = H + static_cast<size_t>(hrow + n) * p.F + d.row + r;
-        if constexpr (F32) *o = v;
-        else *o = __float2bfloat16_rn(v);
-      }
-    }) && ok;
-    fence_proxy_async_all();  // H is read by bulk copies
-    ok = consumer_all(ok);    // one decision for the barriers below
-    if (tid == 0) grid_arrive(p.sync);
-    const int rows = static_cast<int>(c1 - c0);
+    const int rows = c1 - c0;
+    int gu_tiles = 0;
+#pragma unroll 1
+    for (int at = g0; at < g1; ++gu_tiles) at += min(min(16, g1 - at), p.F - at % p.F);
+    const int tiles[2] = {ok ? gu_tiles : 0,
+                          ok && nseg > 0 ? (rows + kTileRows - 1) / kTileRows : 0};
+    const int chunks[2] = {(dv + kChunkVecs - 1) / kChunkVecs,
+                           (fv + kChunkVecs - 1) / kChunkVecs * nseg};
     auto put = [&](int t, int c, float v) {
       const size_t o = static_cast<size_t>(t) * p.d + c;
       Tin* yo = static_cast<Tin*>(p.y) + o;
@@ -464,20 +457,38 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
         *yo = __float2bfloat16_rn(p.residual ? v + __bfloat162float(X[o]) : v);
       }
     };
-    if (nseg == 0) {  // capacity 0 and no shared expert: only the residual is left
-      if (ok)
-        for (int i = tid; i < rows * live; i += kConsumers)
-          put(i / rows, static_cast<int>(c0) + i % rows, 0.f);
-    } else {
-      consume<F32, NT>(s, it, tile, ok ? (rows + kTileRows - 1) / kTileRows : 0,
-                       (fv + kChunkVecs - 1) / kChunkVecs * nseg, p.status,
-                       [&](const SlotDesc& d, const float* red) {
+    auto epilogue = [&](const SlotDesc& d, const float* red) {
+      if (d.kind == 0) {
+        const int nb = __popc(d.mask), hrow = tb.seg_hrow[d.seg];
+#pragma unroll 1
+        for (int i = tid; i < 16 * nb; i += kConsumers) {
+          const int r = i & 15, n = i >> 4;
+          if (r >= d.r0) continue;
+          const float g = red_sum<NT>(red, 0, r, n), u = red_sum<NT>(red, 1, r, n);
+          const float v = g / (1.f + expf(-g)) * u * tb.gate_of_row[hrow + n];
+          Tin* o = H + static_cast<size_t>(hrow + n) * p.F + d.row + r;
+          if constexpr (F32) *o = v;
+          else *o = __float2bfloat16_rn(v);
+        }
+      } else {
         const int nr = d.r0 + d.r1;
+#pragma unroll 1
         for (int i = tid; i < kTileRows * live; i += kConsumers) {
           const int r = i & 31, t = i >> 5;
           if (r < nr) put(t, d.row + r, red_sum<NT>(red, 0, r, t));
         }
-      });
+      }
+    };
+    auto between = [&](bool well) {
+      fence_proxy_async_all();  // H is read by bulk copies
+      well = consumer_all(well);
+      if (tid == 0) grid_arrive(p.sync);
+      return well;
+    };
+    consume<F32, NT>(s, tiles, chunks, p.status, epilogue, between);
+    if (nseg == 0 && ok) {  // capacity 0 and no shared expert: only the residual is left
+#pragma unroll 1
+      for (int i = tid; i < rows * live; i += kConsumers) put(i / rows, c0 + i % rows, 0.f);
     }
   }
   __syncthreads();
@@ -518,7 +529,7 @@ FewLayout few_layer_layout(const moe_config& c) {
 }
 
 bool few_layer_supported(const moe_config& c) {
-  return c.T <= kMaxTokens && !c.stats && c.layout == MOE_LAYOUT_RAGGED &&
+  return c.T <= kMaxTokens && (c.E + 1) * static_cast<int64_t>(c.d_ff) <= INT_MAX && !c.stats && c.layout == MOE_LAYOUT_RAGGED &&
          c.overflow == MOE_OVERFLOW_DROP && c.fuse == MOE_FUSE_NONE;
 }
 

@@ -63,6 +63,7 @@ struct alignas(16) SlotDesc {
                    // first in the slot; in a pair tile they are the gate and the up rows)
   int16_t kvec;    // valid 16-byte vectors along the contraction
   int8_t last;     // last chunk of the tile
+  int8_t kind;     // caller's: which phase
   uint32_t mask;   // tokens whose rows the slot holds, ascending
   int32_t scatter; // 1: the token of mask bit t is column t; 0: columns are 0..popc(mask)-1
   int32_t seg;     // caller's: what the tile belongs to
@@ -124,6 +125,18 @@ __device__ __forceinline__ void init_shared(const Shared& s) {
   }
 }
 
+// The engine's waits: one inlined try, the bounded loop out of line.  These kernels run once per
+// layer from a cold instruction cache, where code size is latency: inlined everywhere the
+// kernels were 175 KB.
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                       int32_t* status) {
+  return mbar_wait_bounded(bar, parity, abort_flag, kWaitLimitNs, status);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                     int32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status);
+}
+
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
 }
@@ -141,11 +154,8 @@ __device__ __forceinline__ bool consumer_all(bool v) {
   return r != 0;
 }
 
-// This CTA's share of n rows.
-__device__ __forceinline__ void share(int64_t n, int64_t* lo, int64_t* hi) {
-  *lo = n * blockIdx.x / gridDim.x;
-  *hi = n * (blockIdx.x + 1) / gridDim.x;
-}
+// Where CTA i's share of n rows begins.
+static __device__ __noinline__ int64_t share_begin(int64_t n, uint32_t i) { return n * i / gridDim.x; }
 
 // ---------------------------------------------------------------------------------
 // Grid barrier: counts arrivals in the workspace header (all CTAs are resident).  Both
@@ -161,7 +171,7 @@ __device__ __forceinline__ void grid_arrive(const GridSync& g) {  // one thread,
   atomicAdd(g.count, 1u);
 }
 // One thread.  Bounded: returns false (and records MOE_ERR_TIMEOUT) when the arrivals do not come.
-__device__ __forceinline__ bool grid_wait(const GridSync& g, unsigned int target,
+static __device__ __noinline__ bool grid_wait(const GridSync& g, unsigned int target,
                                           volatile int* abort_flag, int32_t* status) {
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
@@ -249,9 +259,8 @@ struct Producer {
     while (tail != it &&  // warp-uniform: every lane sees the same state
            (it - tail >= kInFlight || line + bytes - start[tail % kSlots] > s.ring_bytes)) {
       if (tail >= stop) return 0;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s.empty[tail % kSlots],
-                                                     (tail / kSlots) & 1u, s.abort_flag,
-                                                     kWaitLimitNs, status)))
+      if (!__all_sync(0xffffffffu, wait(&s.empty[tail % kSlots], (tail / kSlots) & 1u,
+                                        s.abort_flag, status)))
         return -1;
       ++tail;
     }
@@ -293,8 +302,7 @@ struct Producer {
   __device__ __forceinline__ void drain() {
     for (uint32_t i = it - min(it, static_cast<uint32_t>(kSlots)); i < it; ++i)
       if (i % kProducerWarps == me &&
-          !mbar_wait_bounded(&s.full[i % kSlots], (i / kSlots) & 1u, nullptr, kWaitLimitNs,
-                             status))
+          !wait_slow(&s.full[i % kSlots], (i / kSlots) & 1u, nullptr, status))
         break;
   }
 };
@@ -507,50 +515,74 @@ __device__ __forceinline__ float red_sum(const float* red, int m, int i, int n) 
   return v;
 }
 
-// Consume `tiles` tiles of `chunks` slots each; `it` and `tile` count the CTA's slots and
-// tiles across phases.  epilogue(desc, red) runs on all consumer threads once per tile, with
-// the descriptor of its last slot and the 8 warps' partial sums, after the next tile's slots
-// are consumed.  A buffer of partial sums is written again only after its tile's epilogue:
-// each warp arrives for a tile after its own epilogue of the tile before, and waits for all
-// arrivals of that one first.  Returns false on abort (every wait is bounded).
-template <bool F32, int NT, typename Epi>
-__device__ __forceinline__ bool consume(const Shared& s, uint32_t& it, uint32_t& tile,
-                                        int tiles, int chunks, int32_t* status, Epi&& epilogue) {
+// Consume the tiles of two phases: tiles[0] of chunks[0] slots each, then `between`, then
+// tiles[1] of chunks[1].  epilogue(desc, red) runs on all consumer threads once per tile, with
+// the descriptor of its last slot and the 8 warps' partial sums: after the next tile's slots are
+// consumed, or, for the last tile of a phase, at once.  A buffer of partial sums is written again
+// only after its tile's epilogue: each warp arrives for a tile after its own epilogue of the tile
+// before, and waits for all arrivals of that one first.
+//   between(ok) holds barriers of the consumer threads: every warp calls it once, also one that
+// gives up before (every wait is bounded); it returns whether all are well.
+// One loop for both phases on purpose: its code is there once.
+template <bool F32, int NT, typename Epi, typename Between>
+__device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
+                                        const int (&chunks)[2], int32_t* status, Epi&& epilogue,
+                                        Between&& between) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t group = warp / kGroupWarps;
   const int part = warp % kGroupWarps;
+  const int total = tiles[0] + tiles[1];
+  uint32_t it = 0;       // slots passed
+  int tile = 0;
+  bool pending = false;  // tile - 1 awaits its epilogue
+  bool crossed = false, ok = true;
   Acc<F32, NT> acc;
-  auto finish = [&](uint32_t t) {
-    const bool ok = mbar_wait_bounded(&s.sums[t & 1u], (t >> 1) & 1u, s.abort_flag,
-                                      kWaitLimitNs, status);
-    if (!__all_sync(0xffffffffu, ok)) return false;
-    epilogue(s.tile[t & 1u], s.red + (t & 1u) * kRedFloats<NT>);
-    return true;
-  };
-  for (int i = 0; i < tiles; ++i, ++tile) {
-    acc.zero();
-    const uint32_t end = it + chunks;
+#pragma unroll 1
+  for (;;) {
+    const bool flush = pending && ((tile == tiles[0] && !crossed) || tile == total);
     bool last = false;
     SlotDesc d;
-    for (it += (group - it) % kGroups; it < end; it += kGroups) {
-      const uint32_t slot = it % kSlots;
-      const bool ok = mbar_wait_bounded(&s.full[slot], (it / kSlots) & 1u, s.abort_flag,
-                                        kWaitLimitNs, status);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      d = s.desc[slot];
-      acc.chunk(d, s, part, lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.empty[slot]);
-      last = d.last != 0;
+    if (!flush) {
+      if (tile == tiles[0] && !crossed) {
+        crossed = true;
+        if (!between(ok)) return;
+      }
+      if (tile == total) return;
+      acc.zero();
+      const uint32_t end = it + chunks[crossed ? 1 : 0];
+#pragma unroll 1
+      for (it += (group - it) % kGroups; it < end; it += kGroups) {
+        const uint32_t slot = it % kSlots;
+        ok = __all_sync(0xffffffffu,
+                        wait(&s.full[slot], (it / kSlots) & 1u, s.abort_flag, status));
+        if (!ok) break;
+        d = s.desc[slot];
+        acc.chunk(d, s, part, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.empty[slot]);
+        last = d.last != 0;
+      }
+      it = end;
     }
-    it = end;
-    if (i > 0 && !finish(tile - 1)) return false;
-    acc.store(s.red + (tile & 1u) * kRedFloats<NT>, warp, lane);
-    if (last && part == 0 && lane == 0) s.tile[tile & 1u] = d;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.sums[tile & 1u]);
+    if (pending && ok) {
+      const uint32_t t = tile - 1;
+      ok = __all_sync(0xffffffffu, wait(&s.sums[t & 1u], (t >> 1) & 1u, s.abort_flag, status));
+      if (ok) epilogue(s.tile[t & 1u], s.red + (t & 1u) * kRedFloats<NT>);
+    }
+    pending = false;
+    if (!ok) {
+      if (!crossed) between(false);
+      return;
+    }
+    if (!flush) {
+      acc.store(s.red + (tile & 1) * kRedFloats<NT>, warp, lane);
+      if (last && part == 0 && lane == 0) s.tile[tile & 1] = d;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.sums[tile & 1]);
+      ++tile;
+      pending = true;
+    }
   }
-  return tiles == 0 || finish(tile - 1);
 }
 
 }  // namespace few
