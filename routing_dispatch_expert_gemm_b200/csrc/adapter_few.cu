@@ -48,8 +48,8 @@ struct AdapterTables {
   int32_t nseg;
 };
 constexpr uint32_t kAdapterTableBytes = (sizeof(AdapterTables) + 15) & ~15u;
-static_assert(kCtlBytes + 2 * kRedFloats<4> * 4 + kAdapterTableBytes + kMaxSlotBytes <= kSmemBytes,
-              "the ring holds the largest slot");
+static_assert(kCtlBytes + kRedFloats<4> * 4 + kAdapterTableBytes + 2 * kMaxSlotBytes <= kSmemBytes,
+              "the ring holds two of the largest slots");
 
 __device__ __forceinline__ void build_adapter_tables(const AdapterFewParams& p,
                                                      AdapterTables& tb, int live) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
   constexpr int TILE = kTileRows / M;       // output rows of a tile
   extern __shared__ __align__(128) uint8_t smem[];
   const Shared s = carve<NT>(smem, kAdapterTableBytes, p.smem_bytes);
-  AdapterTables& tb = *reinterpret_cast<AdapterTables*>(smem + kCtlBytes + 2 * kRedFloats<NT> * 4);
+  AdapterTables& tb = *reinterpret_cast<AdapterTables*>(smem + kCtlBytes + kRedBufs<NT> * kRedFloats<NT> * 4);
   const int tid = threadIdx.x, warp = tid >> 5;
 
   init_shared(s);

@@ -66,8 +66,6 @@ struct Tables {
   uint32_t seg_mask[kMaxExperts + 1];
   int16_t seg_e[kMaxExperts + 2];
   int16_t seg_hrow[kMaxExperts + 2];
-  int32_t ids[kMaxTokens * 32];    // [T, k]
-  float gates[kMaxTokens * 32];    // [T, k]
   float gate_of_row[kMaxTokens * 33];
   int32_t cost[kMaxExperts + 2];   // per hidden row, summed over the segments before
   int32_t lo, hi;                  // this CTA's (segment, hidden row) pairs of gate/up
@@ -79,8 +77,13 @@ struct Tables {
 __device__ __forceinline__ int pair_cost(int nb) { return 32 + nb; }
 
 constexpr uint32_t kTableBytes = (sizeof(Tables) + 15) & ~15u;
-static_assert(kCtlBytes + 2 * kRedFloats<4> * 4 + kTableBytes + kMaxSlotBytes <= kSmemBytes,
-              "the ring holds the largest slot");
+// Only while the tables are built: in the ring, which is still empty.
+struct Choice {
+  int32_t ids[kMaxTokens * 32];  // [T, k]
+  float gates[kMaxTokens * 32];  // [T, k]
+};
+static_assert(kCtlBytes + kRedFloats<4> * 4 + kTableBytes + 2 * kMaxSlotBytes <= kSmemBytes,
+              "the ring holds two of the largest slots");
 
 __device__ __forceinline__ float rank_key(float z) { return isnan(z) ? -INFINITY : z; }
 // Larger logit, larger key; -0 ranks as +0.
@@ -141,7 +144,7 @@ __device__ __forceinline__ void router_logits(const FewParams& p, int live) {
 
 // Top-k and gates of token t by one warp: k rounds of (largest key, then lowest index).
 template <int NP>
-__device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, int t) {
+__device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, Choice& ch, int t) {
   const int lane = threadIdx.x & 31;
   uint32_t key[NP];
 #pragma unroll
@@ -182,21 +185,21 @@ __device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, int
     g = ej / denom;
   }
   if (lane < p.k) {
-    tb.ids[t * p.k + lane] = sel_e;
-    tb.gates[t * p.k + lane] = g;
+    ch.ids[t * p.k + lane] = sel_e;
+    ch.gates[t * p.k + lane] = g;
     atomicOr(&tb.mask[sel_e], 1u << t);
   }
 }
 
 // The tables, by the consumer threads.
-__device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int live) {
+__device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Choice& ch, int live) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e <= p.E; e += kConsumers) tb.mask[e] = 0;
   consumer_sync();
   for (int t = warp; t < live; t += kConsumerWarps) {
-    if (p.E <= 32) select_token<1>(p, tb, t);
-    else if (p.E <= 64) select_token<2>(p, tb, t);
-    else select_token<8>(p, tb, t);
+    if (p.E <= 32) select_token<1>(p, tb, ch, t);
+    else if (p.E <= 64) select_token<2>(p, tb, ch, t);
+    else select_token<8>(p, tb, ch, t);
   }
   consumer_sync();
   if (warp == 0) {
@@ -276,15 +279,15 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, int
       float g = 0.f;
 #pragma unroll 1
       for (int j = 0; j < p.k; ++j)
-        if (tb.ids[lane * p.k + j] == e) g = tb.gates[lane * p.k + j];
+        if (ch.ids[lane * p.k + j] == e) g = ch.gates[lane * p.k + j];
       tb.gate_of_row[tb.seg_hrow[s] + __popc(m & ((1u << lane) - 1u))] = g;
     }
   }
   if (blockIdx.x == 0)
 #pragma unroll 1
     for (int i = tid; i < live * p.k; i += kConsumers) {
-      if (p.ids_out != nullptr) p.ids_out[i] = tb.ids[i];
-      if (p.gates_out != nullptr) p.gates_out[i] = tb.gates[i];
+      if (p.ids_out != nullptr) p.ids_out[i] = ch.ids[i];
+      if (p.gates_out != nullptr) p.gates_out[i] = ch.gates[i];
     }
 }
 
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
   constexpr int VEC = Vec<Tin>::N;
   extern __shared__ __align__(128) uint8_t smem[];
   const Shared s = carve<NT>(smem, kTableBytes, p.smem_bytes);
-  Tables& tb = *reinterpret_cast<Tables*>(smem + kCtlBytes + 2 * kRedFloats<NT> * 4);
+  Tables& tb = *reinterpret_cast<Tables*>(smem + kCtlBytes + kRedBufs<NT> * kRedFloats<NT> * 4);
   const int tid = threadIdx.x, warp = tid >> 5;
   const Tin* X = static_cast<const Tin*>(p.x);
   Tin* H = static_cast<Tin*>(p.h);
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     }
     consumer_sync();
     ok = *s.abort_flag == 0;  // written before the barrier: the same for all
-    if (ok) build_tables(p, tb, live);
+    if (ok) build_tables(p, tb, *reinterpret_cast<Choice*>(s.ring), live);
     else if (tid == 0) tb.nseg = tb.c0 = tb.c1 = 0;
   }
   __syncthreads();

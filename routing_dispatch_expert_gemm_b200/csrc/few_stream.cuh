@@ -76,10 +76,11 @@ struct Shared {
   SlotDesc* desc;
   uint32_t* start;  // [kProducerWarps][kSlots]: each producer's record of slot positions
   uint64_t* sums;   // [2] a tile's partial sums are complete
+  uint64_t* freed;  // a tile's epilogue is done (one buffer of partial sums)
   SlotDesc* tile;   // [2] its last slot's descriptor
   volatile int* abort_flag;
   uint8_t* ring;
-  float* red;       // [2][8 warps][8 NT][kRedStride]
+  float* red;       // [kRedBufs][8 warps][8 NT][kRedStride]
   uint8_t* zeros;   // a chunk of zeros: the row of a token that a slot does not hold
   uint32_t ring_bytes;
 };
@@ -88,6 +89,9 @@ constexpr int kCtlBytes = 2 * kSlots * 8 + kSlots * 32 + kProducerWarps * kSlots
 static_assert(sizeof(SlotDesc) == 32, "descriptor size");
 static_assert(kSlots % kGroups == 0, "a slot's barriers belong to one group");
 template <int NT> constexpr int kRedFloats = kConsumerWarps * 8 * NT * kRedStride;
+// Buffers of partial sums: two for up to 8 tokens; with more tokens one (and a barrier for its
+// release), because the ring needs the room: a slot of 32 tokens takes 68 KB.
+template <int NT> constexpr int kRedBufs = NT == 1 ? 2 : 1;
 // The largest slot: a full tile and 32 token rows.
 constexpr uint32_t kMaxSlotBytes = (kTileRows + kMaxTokens) * (kChunkBytes + 64);
 
@@ -101,10 +105,11 @@ __device__ __forceinline__ Shared carve(uint8_t* smem, uint32_t table_bytes, uin
   s.start = reinterpret_cast<uint32_t*>(s.desc + kSlots);
   s.tile = reinterpret_cast<SlotDesc*>(s.start + kProducerWarps * kSlots);
   s.sums = reinterpret_cast<uint64_t*>(s.tile + 2);
-  s.abort_flag = reinterpret_cast<volatile int*>(s.sums + 2);
+  s.freed = s.sums + 2;
+  s.abort_flag = reinterpret_cast<volatile int*>(s.freed + 1);
   s.red = reinterpret_cast<float*>(smem + kCtlBytes);
   s.zeros = smem + kCtlBytes - kChunkBytes;
-  const uint32_t at = kCtlBytes + 2 * kRedFloats<NT> * 4 + table_bytes;
+  const uint32_t at = kCtlBytes + kRedBufs<NT> * kRedFloats<NT> * 4 + table_bytes;
   s.ring = smem + at;
   s.ring_bytes = (total - at) & ~15u;
   return s;
@@ -120,6 +125,7 @@ __device__ __forceinline__ void init_shared(const Shared& s) {
     }
     mbar_init(&s.sums[0], kConsumerWarps);
     mbar_init(&s.sums[1], kConsumerWarps);
+    mbar_init(s.freed, kConsumerWarps);
     *s.abort_flag = 0;
     fence_mbar_init();
   }
@@ -519,8 +525,9 @@ __device__ __forceinline__ float red_sum(const float* red, int m, int i, int n) 
 // tiles[1] of chunks[1].  epilogue(desc, red) runs on all consumer threads once per tile, with
 // the descriptor of its last slot and the 8 warps' partial sums: after the next tile's slots are
 // consumed, or, for the last tile of a phase, at once.  A buffer of partial sums is written again
-// only after its tile's epilogue: each warp arrives for a tile after its own epilogue of the tile
-// before, and waits for all arrivals of that one first.
+// only after its tile's epilogue: with two buffers because each warp arrives for a tile after its
+// own epilogue of the tile before, and waits for all arrivals of that one first; with one buffer
+// because it waits for all epilogues of the tile before.
 //   between(ok) holds barriers of the consumer threads: every warp calls it once, also one that
 // gives up before (every wait is bounded); it returns whether all are well.
 // One loop for both phases on purpose: its code is there once.
@@ -567,7 +574,11 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
     if (pending && ok) {
       const uint32_t t = tile - 1;
       ok = __all_sync(0xffffffffu, wait(&s.sums[t & 1u], (t >> 1) & 1u, s.abort_flag, status));
-      if (ok) epilogue(s.tile[t & 1u], s.red + (t & 1u) * kRedFloats<NT>);
+      if (ok) epilogue(s.tile[t & 1u], s.red + (t % kRedBufs<NT>) * kRedFloats<NT>);
+      if (kRedBufs<NT> == 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s.freed);
+      }
     }
     pending = false;
     if (!ok) {
@@ -575,7 +586,12 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
       return;
     }
     if (!flush) {
-      acc.store(s.red + (tile & 1) * kRedFloats<NT>, warp, lane);
+      if (kRedBufs<NT> == 1 && tile > 0 &&
+          !__all_sync(0xffffffffu, wait(s.freed, (tile - 1) & 1u, s.abort_flag, status))) {
+        if (!crossed) between(false);
+        return;
+      }
+      acc.store(s.red + (tile % kRedBufs<NT>) * kRedFloats<NT>, warp, lane);
       if (last && part == 0 && lane == 0) s.tile[tile & 1] = d;
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.sums[tile & 1]);
