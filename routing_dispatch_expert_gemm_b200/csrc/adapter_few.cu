@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
   AdapterTables& tb = *reinterpret_cast<AdapterTables*>(smem + kCtlBytes + kRedBufs<NT> * kRedFloats<NT> * 4);
   const int tid = threadIdx.x, warp = tid >> 5;
 
-  init_shared(s);
+  init_shared<NT>(s);
   const int live = p.n_tokens != nullptr ? min(max(__ldg(p.n_tokens), 0), p.T) : p.T;
   if (warp == 0) build_adapter_tables(p, tb, live);
   __syncthreads();

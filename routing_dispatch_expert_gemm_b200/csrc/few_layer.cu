@@ -66,15 +66,17 @@ struct Tables {
   uint32_t seg_mask[kMaxExperts + 1];
   int16_t seg_e[kMaxExperts + 2];
   int16_t seg_hrow[kMaxExperts + 2];
+  int16_t row[kMaxExperts + 2];    // first H row of each expert
   float gate_of_row[kMaxTokens * 33];
   int32_t cost[kMaxExperts + 2];   // per hidden row, summed over the segments before
   int32_t lo, hi;                  // this CTA's (segment, hidden row) pairs of gate/up
   int32_t c0, c1;                  // and its output rows of down
   int32_t nseg;
 };
-// Cost of a gate/up row pair with nb tokens: two weight rows and, per 16 pairs, nb token
-// rows through the same copies and shared memory.
-__device__ __forceinline__ int pair_cost(int nb) { return 32 + nb; }
+// Cost of a gate/up row pair with nb tokens: two weight rows and, per 16 pairs, nb token rows
+// through the same copies and shared memory, and their MMAs.  Measured on skewed experts (T=32,
+// 1 to 30 tokens each): at 32 + nb the CTAs of the fullest expert took 497 us, the others 305.
+__device__ __forceinline__ int pair_cost(int nb) { return 32 + 2 * nb; }
 
 constexpr uint32_t kTableBytes = (sizeof(Tables) + 15) & ~15u;
 // Only while the tables are built: in the ring, which is still empty.
@@ -142,52 +144,74 @@ __device__ __forceinline__ void router_logits(const FewParams& p, int live) {
   }
 }
 
-// Top-k and gates of token t by one warp: k rounds of (largest key, then lowest index).
+// Top-k and gates of token t by one warp; lane l holds experts l, l + 32, ...  k rounds of
+// (largest key, then lowest index).  (Ranking each expert against all others by 32 shuffles
+// instead took 1.7 us a token: the shuffles' dependent instructions, not the rounds, bound.)
 template <int NP>
-__device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, Choice& ch, int t) {
+__device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, Choice& ch, int t,
+                                             const float (&z)[NP]) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[NP];
+  uint32_t key[NP], most = 0;
+  int rank[NP];  // slot of each of the lane's experts, kMaxExperts: not chosen
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const int e = 32 * i + lane;
-    key[i] = 0;  // below every logit's key (-inf is 0x007fffff)
-    if (e < p.E) key[i] = order_key(rank_key(__ldcg(p.logits + t * p.E + e)));
+    key[i] = 32 * i + lane < p.E ? order_key(rank_key(z[i])) : 0;  // 0: below every logit's key
+    rank[i] = kMaxExperts;
   }
-  uint32_t taken = 0;
-  float sel_z = -INFINITY;
-  int sel_e = 0;
 #pragma unroll 1
   for (int j = 0; j < p.k; ++j) {
     uint32_t best = 0;
     int be = 0x7fffffff;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      if (!(taken & (1u << i)) && key[i] > best) { best = key[i]; be = 32 * i + lane; }
-    }
+    for (int i = 0; i < NP; ++i)
+      if (rank[i] == kMaxExperts && key[i] > best) { best = key[i]; be = 32 * i + lane; }
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const int e = __reduce_min_sync(0xffffffffu, best == top ? be : 0x7fffffff);
-    if (e % 32 == lane) taken |= 1u << (e / 32);
-    if (lane == j) { sel_z = key_value(top); sel_e = e; }
-  }
-  const float m = __shfl_sync(0xffffffffu, sel_z, 0);
-  float g = 0.f;
-  if (m > -INFINITY) {  // else every expert is masked: the token takes nothing from any
-    const float ej = (lane < p.k) ? expf(sel_z - m) : 0.f;
-    float denom = warp_sum(ej);
-    if (p.gate_mode == MOE_GATE_SOFTMAX_TOPK) {
-      float local = 0.f;
+    int e;
+    if constexpr (NP == 1) e = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+    else e = __reduce_min_sync(0xffffffffu, best == top ? be : 0x7fffffff);
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
-        if (32 * i + lane < p.E) local += expf(key_value(key[i]) - m);
-      denom = warp_sum(local);
-    }
-    // renormalising the full softmax over the selected experts cancels its denominator
-    g = ej / denom;
+    for (int i = 0; i < NP; ++i)
+      if (32 * i + lane == e) rank[i] = j;
+    if (j == 0) most = top;
   }
-  if (lane < p.k) {
-    ch.ids[t * p.k + lane] = sel_e;
-    ch.gates[t * p.k + lane] = g;
-    atomicOr(&tb.mask[sel_e], 1u << t);
+  const float m = key_value(most);
+  const bool open = m > -INFINITY;  // else every expert is masked: the token takes nothing
+  float ej[NP], local = 0.f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    ej[i] = open && 32 * i + lane < p.E ? expf(key_value(key[i]) - m) : 0.f;
+    // renormalising the full softmax over the selected experts cancels its denominator
+    if (rank[i] < p.k || p.gate_mode == MOE_GATE_SOFTMAX_TOPK) local += ej[i];
+  }
+  const float denom = warp_sum(local);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    if (rank[i] < p.k) {
+      const int e = 32 * i + lane;
+      ch.ids[t * p.k + rank[i]] = e;
+      ch.gates[t * p.k + rank[i]] = open ? ej[i] / denom : 0.f;
+      atomicOr(&tb.mask[e], 1u << t);
+    }
+  }
+}
+
+// The tokens of this warp; a token's logits are loaded while the one before is selected.
+template <int NP>
+__device__ __forceinline__ void select_tokens(const FewParams& p, Tables& tb, Choice& ch, int live) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float z[NP], next[NP] = {};
+  auto load = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      if (t < live && 32 * i + lane < p.E) next[i] = __ldcg(p.logits + t * p.E + 32 * i + lane);
+  };
+  load(warp);
+#pragma unroll 1
+  for (int t = warp; t < live; t += kConsumerWarps) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) z[i] = next[i];
+    load(t + kConsumerWarps);
+    select_token<NP>(p, tb, ch, t, z);
   }
 }
 
@@ -196,11 +220,9 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e <= p.E; e += kConsumers) tb.mask[e] = 0;
   consumer_sync();
-  for (int t = warp; t < live; t += kConsumerWarps) {
-    if (p.E <= 32) select_token<1>(p, tb, ch, t);
-    else if (p.E <= 64) select_token<2>(p, tb, ch, t);
-    else select_token<8>(p, tb, ch, t);
-  }
+  if (p.E <= 32) select_tokens<1>(p, tb, ch, live);
+  else if (p.E <= 64) select_tokens<2>(p, tb, ch, live);
+  else select_tokens<8>(p, tb, ch, live);
   consumer_sync();
   if (warp == 0) {
     int nseg = 0, rows = 0, cost = 0;
@@ -222,6 +244,7 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
       const int row = rows + incl - n;
       if (e < p.E) {
         tb.mask[e] = m;
+        tb.row[e] = static_cast<int16_t>(row);
         if (blockIdx.x == 0 && p.offsets_out != nullptr) p.offsets_out[e] = row;
       }
       if (n > 0) {
@@ -248,6 +271,8 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
       tb.nseg = nseg;
       tb.cost[nseg] = cost;
       tb.lo = tb.hi = nseg * p.F;  // the end, unless a segment has it
+      tb.c0 = static_cast<int>(share_begin(p.d, blockIdx.x));
+      tb.c1 = static_cast<int>(share_begin(p.d, blockIdx.x + 1));
       if (blockIdx.x == 0 && p.offsets_out != nullptr) {
         p.offsets_out[p.E] = rows;
         p.offsets_out[p.E + 1] = total;
@@ -256,32 +281,24 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
     for (int i = rows + lane; i < total; i += 32) tb.gate_of_row[i] = 1.f;  // shared expert
   }
   consumer_sync();
-  // equal cost for every CTA: where this one's share of the pairs begins and ends
-  const int64_t sum = static_cast<int64_t>(tb.cost[tb.nseg]) * p.F;
-  const int64_t from = share_begin(sum, blockIdx.x), to = share_begin(sum, blockIdx.x + 1);
-  if (tid == 0) {
-    tb.c0 = static_cast<int>(share_begin(p.d, blockIdx.x));
-    tb.c1 = static_cast<int>(share_begin(p.d, blockIdx.x + 1));
-  }
-  for (int s = tid; s < tb.nseg; s += kConsumers) {
-    const int64_t a = static_cast<int64_t>(tb.cost[s]) * p.F;
-    const int64_t b = static_cast<int64_t>(tb.cost[s + 1]) * p.F;
-    const int w = tb.cost[s + 1] - tb.cost[s];
-    // (from - a) / w < F fits 32 bits: (E + 1) F < 2^31
-    if (from >= a && from < b) tb.lo = s * p.F + static_cast<int>((from - a) / w);
-    if (to >= a && to < b) tb.hi = s * p.F + static_cast<int>((to - a) / w);
+  // Equal cost for every CTA: where this one's share of the pairs begins (lanes of even threads)
+  // and ends.  The share's bounds in cost, then in the segment that holds them.
+  {
+    const int end = tid & 1;
+    const int64_t at = share_begin(static_cast<int64_t>(tb.cost[tb.nseg]) * p.F, blockIdx.x + end);
+    for (int s = tid >> 1; s < tb.nseg; s += kConsumers / 2) {
+      const int64_t a = static_cast<int64_t>(tb.cost[s]) * p.F;
+      const int w = tb.cost[s + 1] - tb.cost[s];
+      if (at >= a && at < a + static_cast<int64_t>(w) * p.F)  // F <= 2^24, w < 2^7
+        (end ? tb.hi : tb.lo) = s * p.F + static_cast<int>(static_cast<uint32_t>(at - a) / w);
+    }
   }
   // gate of each kept route's H row
-  for (int s = warp; s < tb.nseg; s += kConsumerWarps) {
-    const int e = tb.seg_e[s];
-    const uint32_t m = tb.seg_mask[s];
-    if (e < p.E && ((m >> lane) & 1u)) {
-      float g = 0.f;
 #pragma unroll 1
-      for (int j = 0; j < p.k; ++j)
-        if (ch.ids[lane * p.k + j] == e) g = ch.gates[lane * p.k + j];
-      tb.gate_of_row[tb.seg_hrow[s] + __popc(m & ((1u << lane) - 1u))] = g;
-    }
+  for (int i = tid; i < live * p.k; i += kConsumers) {
+    const int t = i / p.k, e = ch.ids[i];
+    const uint32_t m = tb.mask[e];
+    if ((m >> t) & 1u) tb.gate_of_row[tb.row[e] + __popc(m & ((1u << t) - 1u))] = ch.gates[i];
   }
   if (blockIdx.x == 0)
 #pragma unroll 1
@@ -310,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
   const Tin* X = static_cast<const Tin*>(p.x);
   Tin* H = static_cast<Tin*>(p.h);
 
-  init_shared(s);
+  init_shared<NT>(s);
   const int live = p.n_tokens != nullptr ? min(max(__ldg(p.n_tokens), 0), p.T) : p.T;
   __syncthreads();
 
@@ -532,7 +549,8 @@ FewLayout few_layer_layout(const moe_config& c) {
 }
 
 bool few_layer_supported(const moe_config& c) {
-  return c.T <= kMaxTokens && (c.E + 1) * static_cast<int64_t>(c.d_ff) <= INT_MAX && !c.stats && c.layout == MOE_LAYOUT_RAGGED &&
+  return c.T <= kMaxTokens && c.d_ff <= (1 << 24) &&
+         (c.E + 1) * static_cast<int64_t>(c.d_ff) <= INT_MAX && !c.stats && c.layout == MOE_LAYOUT_RAGGED &&
          c.overflow == MOE_OVERFLOW_DROP && c.fuse == MOE_FUSE_NONE;
 }
 

@@ -13,7 +13,7 @@
 //     HBM's rate (Mixtral-shaped T=16: 890 us with one producer), so slot i belongs to
 //     producer warp i mod kProducerWarps, one lane per row; every producer follows the same
 //     sequence of slots and places them by the same arithmetic.
-//   * Warps 0-7 consume, two warps to a slot (kGroups slots at a time): a slot costs a warp
+//   * Warps 0-7 consume, two or four warps to a slot, several slots at a time: a slot costs a warp
 //     a fixed latency (its barrier, descriptor, first loads) that eight warps sharing every
 //     slot all paid (Granite-shaped T=16: 0.7 us per 11-row slot), now paid in parallel.
 //     bf16: mma.sync m16n8k16 with the weight rows on M and the tokens on N, fed by 16-byte
@@ -40,8 +40,10 @@ namespace few {
 constexpr int kMaxTokens = 32;       // one token-mask word
 constexpr int kConsumerWarps = 8;
 constexpr int kConsumers = 32 * kConsumerWarps;
-constexpr int kGroupWarps = 2;       // warps that share a slot
-constexpr int kGroups = kConsumerWarps / kGroupWarps;
+// Warps that share a slot: more of them where token rows leave the ring few slots, which are then
+// to be released sooner (16+1 experts T=32: 759 us with 2, 711 us with 4; T=1: 108.7 and 109.1).
+template <int NT> constexpr int kGroupWarps = NT == 1 ? 2 : 4;
+template <int NT> constexpr int kGroups = kConsumerWarps / kGroupWarps<NT>;
 constexpr int kProducerWarps = 4;
 constexpr int kThreads = kConsumers + 32 * kProducerWarps;
 constexpr int kSlots = 64;           // slot descriptors and barriers
@@ -87,7 +89,8 @@ struct Shared {
 
 constexpr int kCtlBytes = 2 * kSlots * 8 + kSlots * 32 + kProducerWarps * kSlots * 4 + 2 * 32 + 64 + kChunkBytes;
 static_assert(sizeof(SlotDesc) == 32, "descriptor size");
-static_assert(kSlots % kGroups == 0, "a slot's barriers belong to one group");
+static_assert(kSlots % kGroups<1> == 0 && kSlots % kGroups<4> == 0,
+              "a slot's barriers belong to one group");
 template <int NT> constexpr int kRedFloats = kConsumerWarps * 8 * NT * kRedStride;
 // Buffers of partial sums: two for up to 8 tokens; with more tokens one (and a barrier for its
 // release), because the ring needs the room: a slot of 32 tokens takes 68 KB.
@@ -115,13 +118,14 @@ __device__ __forceinline__ Shared carve(uint8_t* smem, uint32_t table_bytes, uin
   return s;
 }
 
+template <int NT>
 __device__ __forceinline__ void init_shared(const Shared& s) {
   for (int i = threadIdx.x; i < kChunkVecs; i += kThreads)
     reinterpret_cast<uint4*>(s.zeros)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], kGroupWarps);
+      mbar_init(&s.empty[i], kGroupWarps<NT>);
     }
     mbar_init(&s.sums[0], kConsumerWarps);
     mbar_init(&s.sums[1], kConsumerWarps);
@@ -385,7 +389,7 @@ template <int NT> struct Acc<false, NT> {
       b[n] = row >= 0 ? base + (d.r0 + d.r1 + row) * P + at : smem_u32(s.zeros) + at;
     }
     float part_c[2][NT][4] = {};
-    constexpr int kStep = kGroupWarps * 64;                // bytes between a warp's blocks
+    constexpr int kStep = kGroupWarps<NT> * 64;                // bytes between a warp's blocks
     constexpr int kBlocks = kChunkBytes / kStep;
     constexpr int HB = NB == 4 ? 2 : 4;  // blocks loaded together, so that latencies overlap
     if (d.kvec == kChunkVecs) {
@@ -473,7 +477,7 @@ template <int NT> struct Acc<true, NT> {
     const uint32_t b = base + (d.r0 + d.r1) * P;
     constexpr int V = 8;  // vectors of the row held together
 #pragma unroll 1
-    for (int v0 = part * V; v0 < d.kvec; v0 += V * kGroupWarps) {
+    for (int v0 = part * V; v0 < d.kvec; v0 += V * kGroupWarps<NT>) {
       float w[V][4];
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -536,8 +540,8 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
                                         const int (&chunks)[2], int32_t* status, Epi&& epilogue,
                                         Between&& between) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t group = warp / kGroupWarps;
-  const int part = warp % kGroupWarps;
+  const uint32_t group = warp / kGroupWarps<NT>;
+  const int part = warp % kGroupWarps<NT>;
   const int total = tiles[0] + tiles[1];
   uint32_t it = 0;       // slots passed
   int tile = 0;
@@ -558,7 +562,7 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
       acc.zero();
       const uint32_t end = it + chunks[crossed ? 1 : 0];
 #pragma unroll 1
-      for (it += (group - it) % kGroups; it < end; it += kGroups) {
+      for (it += (group - it) % kGroups<NT>; it < end; it += kGroups<NT>) {
         const uint32_t slot = it % kSlots;
         ok = __all_sync(0xffffffffu,
                         wait(&s.full[slot], (it / kSlots) & 1u, s.abort_flag, status));
