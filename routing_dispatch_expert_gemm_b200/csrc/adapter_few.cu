@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
           const uint32_t bytes = n * 16, o = kv * 16;
           pr.open(SlotDesc{0, static_cast<int16_t>(n0), static_cast<int16_t>(n1),
                            static_cast<int16_t>(n), i + 1 == chunks,
-                           static_cast<int8_t>(kind), mask, 0, seg, row},
+                           static_cast<int8_t>(kind), mask, 0, seg, row, kv},
                   rows * bytes);
           pr.copy_rows(pr.it, pr.head, 0, w0 + o, xs, n0, bytes);
           pr.copy_rows(pr.it, pr.head, n0, w1 + o, xs, n1, bytes);
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
         return;
       }
       if (!waited) {  // u is complete
-        if (!grid_wait_warp(p.sync, gridDim.x, s.abort_flag, p.status)) return;
+        if (!grid_wait_warps(p.sync, gridDim.x, tid < 32, s.passed, s.abort_flag, p.status)) return;
         waited = true;
       }
       const int nr = PAIR ? d.r0 : d.r0 + d.r1;

@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
           const int n = min(kChunkVecs, dv - kv);
           const uint32_t bytes = n * 16, o = kv * 16;
           pr.open(SlotDesc{0, static_cast<int16_t>(np), static_cast<int16_t>(np),
-                           static_cast<int16_t>(n), i + 1 == chunks, 0, mask, 0, seg, f0},
+                           static_cast<int16_t>(n), i + 1 == chunks, 0, mask, 0, seg, f0, kv},
                   rows * bytes);
           pr.copy_rows(pr.it, pr.head, 0, wg + o, xs, np, bytes);
           pr.copy_rows(pr.it, pr.head, np, wu + o, xs, np, bytes);
@@ -390,15 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
       at += np;
     }
     // Down: the weight rows of the slots that fit come before the barrier, their H rows
-    // after it.  `w` is the position of the next slot, `b` that of slot h_it, the first
-    // whose H rows are still to come.
+    // after it.
     const uint32_t first = pr.it;
-    uint32_t h_it = first;
     const int fch = (fv + kChunkVecs - 1) / kChunkVecs, pairs = fch * nseg;
     const int turn = static_cast<int>(static_cast<int64_t>(pairs) * blockIdx.x / gridDim.x);
     DownPos w{c0, min(kTileRows, c1 - c0),
               turn / fch, turn % fch * kChunkVecs, pairs};
-    DownPos b = w;
     auto next = [&](DownPos& q) {
       q.kv += kChunkVecs;
       if (q.kv >= fv) {
@@ -410,19 +407,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
       q.row += q.nrows;
       q.nrows = min(kTileRows, c1 - q.row);
     };
-    auto load_h = [&](const DownPos& q, uint32_t it) {
-      const int nb = __popc(tb.seg_mask[q.seg]);
-      pr.copy_rows(it, s.desc[it % kSlots].off, q.nrows,
-                   reinterpret_cast<const uint8_t*>(H) + tb.seg_hrow[q.seg] * hs + q.kv * 16,
-                   hs, nb, min(kChunkVecs, fv - q.kv) * 16);
+    auto load_h = [&](uint32_t it) {  // the H rows of slot `it`, one of this warp's
+      const SlotDesc& d = s.desc[it % kSlots];
+      pr.copy_rows(it, d.off, d.r0 + d.r1,
+                   reinterpret_cast<const uint8_t*>(H) + tb.seg_hrow[d.seg] * hs + d.kv * 16, hs,
+                   __popc(d.mask), d.kvec * 16);
     };
     auto load_late_h = [&] {
-      for (; h_it < pr.it; ++h_it, next(b))
-        if (h_it % kProducerWarps == pr.me) load_h(b, h_it);
+      uint32_t it = first + (pr.me - first) % kProducerWarps;
+#pragma unroll 1
+      for (; it < pr.it; it += kProducerWarps) load_h(it);
     };
     bool passed = false;
     auto pass_barrier = [&] {  // H is complete; bulk copies may read it
-      go = grid_wait_warp(p.sync, 2 * gridDim.x, s.abort_flag, p.status);
+      go = grid_wait_warps(p.sync, 2 * gridDim.x, pr.me == 0, s.passed, s.abort_flag, p.status);
       passed = true;
       fence_proxy_async_all();
       load_late_h();
@@ -445,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
                             ((sh ? 0 : static_cast<size_t>(e) * p.d) + w.row) * hs + w.kv * 16;
         const int r0 = min(16, w.nrows);
         pr.open(SlotDesc{0, static_cast<int16_t>(r0), static_cast<int16_t>(w.nrows - r0),
-                         static_cast<int16_t>(n), w.left == 1, 1, mask, 1, w.seg, w.row},
+                         static_cast<int16_t>(n), w.left == 1, 1, mask, 1, w.seg, w.row, w.kv},
                 rows * n * 16);
         pr.copy_rows(pr.it, pr.head, 0, wd, hs, w.nrows, n * 16);
-        if (passed) load_h(w, pr.it);
+        if (passed) load_h(pr.it);
       }
       pr.pass(rows * P);
       next(w);

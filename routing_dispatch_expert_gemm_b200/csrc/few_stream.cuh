@@ -70,6 +70,7 @@ struct alignas(16) SlotDesc {
   int32_t scatter; // 1: the token of mask bit t is column t; 0: columns are 0..popc(mask)-1
   int32_t seg;     // caller's: what the tile belongs to
   int32_t row;     // caller's: first output row of the tile
+  int32_t kv;      // caller's: first vector of the chunk along the contraction
 };
 
 struct Shared {
@@ -79,6 +80,7 @@ struct Shared {
   uint32_t* start;  // [kProducerWarps][kSlots]: each producer's record of slot positions
   uint64_t* sums;   // [2] a tile's partial sums are complete
   uint64_t* freed;  // a tile's epilogue is done (one buffer of partial sums)
+  uint64_t* passed; // this CTA knows that all CTAs have arrived
   SlotDesc* tile;   // [2] its last slot's descriptor
   volatile int* abort_flag;
   uint8_t* ring;
@@ -109,7 +111,8 @@ __device__ __forceinline__ Shared carve(uint8_t* smem, uint32_t table_bytes, uin
   s.tile = reinterpret_cast<SlotDesc*>(s.start + kProducerWarps * kSlots);
   s.sums = reinterpret_cast<uint64_t*>(s.tile + 2);
   s.freed = s.sums + 2;
-  s.abort_flag = reinterpret_cast<volatile int*>(s.freed + 1);
+  s.passed = s.freed + 1;
+  s.abort_flag = reinterpret_cast<volatile int*>(s.passed + 1);
   s.red = reinterpret_cast<float*>(smem + kCtlBytes);
   s.zeros = smem + kCtlBytes - kChunkBytes;
   const uint32_t at = kCtlBytes + kRedBufs<NT> * kRedFloats<NT> * 4 + table_bytes;
@@ -130,6 +133,7 @@ __device__ __forceinline__ void init_shared(const Shared& s) {
     mbar_init(&s.sums[0], kConsumerWarps);
     mbar_init(&s.sums[1], kConsumerWarps);
     mbar_init(s.freed, kConsumerWarps);
+    mbar_init(s.passed, 1);
     *s.abort_flag = 0;
     fence_mbar_init();
   }
@@ -198,12 +202,14 @@ static __device__ __noinline__ bool grid_wait(const GridSync& g, unsigned int ta
     }
   }
 }
-// The same by a whole warp: one lane polls.
-__device__ __forceinline__ bool grid_wait_warp(const GridSync& g, unsigned int target,
-                                               volatile int* abort_flag, int32_t* status) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = grid_wait(g, target, abort_flag, status);
-  return __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+// The same by several whole warps of a CTA, once per launch: one lane of the `poller` warp polls,
+// the others wait in shared memory (polls of all warps would crowd the arrivals).
+__device__ __forceinline__ bool grid_wait_warps(const GridSync& g, unsigned int target,
+                                                bool poller, uint64_t* passed,
+                                                volatile int* abort_flag, int32_t* status) {
+  if (poller && (threadIdx.x & 31) == 0 && grid_wait(g, target, abort_flag, status))
+    mbar_arrive(passed);
+  return __all_sync(0xffffffffu, wait(passed, 0, abort_flag, status));
 }
 __device__ __forceinline__ void grid_leave(const GridSync& g) {  // one thread, waits all passed
   __threadfence();
