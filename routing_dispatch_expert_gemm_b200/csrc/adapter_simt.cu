@@ -3,11 +3,12 @@
 //   p[t] = W x_t + s_a B_a (A_a x_t);  y[t] = p[t] (+ addend[t])  or  SiLU(p_gate) * p_up
 // CUDA cores, as the fp32 expert FFN: tf32 cannot meet its tolerance.  Two launches:
 //   shrink  u[t] = s_a A_a x_t, one warp per token and four ranks.
-//   GEMM    tiles of BT tokens x BC rows of W, staged 32 columns at a time in shared memory
+//   GEMM    tiles of BT tokens x BC rows of W, staged BKF columns at a time in shared memory
 //           with the next stage's loads in registers; the epilogue adds B_a u.  Bound by FMA
 //           (128 per SM and clock).  Two tile sizes: 64 x 64 (4 x 4 outputs per thread, one
 //           shared float4 load per 8 FMA) when its tiles cover the SMs, else 16 x 32 (1 x 2),
-//           which reads shared memory more often but keeps small batches on all SMs.
+//           which reads shared memory more often but keeps small batches on all SMs, and
+//           whose stages are longer, because the loads' latency bounds it.
 #include <algorithm>
 
 #include "gemm_common.cuh"
@@ -17,7 +18,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int BKF = 32;  // contraction columns per stage
 
 struct SimtParams {
   const float* x;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const Simt
   }
 }
 
-template <bool PAIR, int BT, int BC, int RT, int RC>
+template <bool PAIR, int BT, int BC, int RT, int RC, int BKF>
 __global__ void __launch_bounds__(kThreads) adapter_gemm_f32_kernel(const SimtParams p) {
   constexpr int M = PAIR ? 2 : 1;
   constexpr int TX = BC / RC;                 // threads across the rows of W
@@ -179,24 +179,24 @@ __global__ void __launch_bounds__(kThreads) adapter_gemm_f32_kernel(const SimtPa
   }
 }
 
-template <bool PAIR, int BT, int BC, int RT, int RC>
+template <bool PAIR, int BT, int BC, int RT, int RC, int BKF>
 cudaError_t launch_tile(const SimtParams& p, cudaStream_t s) {
   static DeviceOnce once;
   cudaError_t e =
-      once.run([] { return prefer_max_shared(adapter_gemm_f32_kernel<PAIR, BT, BC, RT, RC>); });
+      once.run([] { return prefer_max_shared(adapter_gemm_f32_kernel<PAIR, BT, BC, RT, RC, BKF>); });
   if (e != cudaSuccess) return e;
   // tokens on grid.x: grid.y ends at 65535 blocks
   const int rows = (p.d_out + BC - 1) / BC;
   if (rows > 65535) return cudaErrorInvalidValue;
-  return launch_pdl(adapter_gemm_f32_kernel<PAIR, BT, BC, RT, RC>,
+  return launch_pdl(adapter_gemm_f32_kernel<PAIR, BT, BC, RT, RC, BKF>,
                     dim3((p.T + BT - 1) / BT, rows), dim3(kThreads), 0, s, p);
 }
 
 template <bool PAIR>
 cudaError_t launch_gemm_f32(const SimtParams& p, cudaStream_t s) {
   const int64_t big = static_cast<int64_t>((p.d_out + 63) / 64) * ((p.T + 63) / 64);
-  return big >= sm_count() ? launch_tile<PAIR, 64, 64, 4, 4>(p, s)
-                           : launch_tile<PAIR, 16, 32, 1, 2>(p, s);
+  return big >= sm_count() ? launch_tile<PAIR, 64, 64, 4, 4, 32>(p, s)
+                           : launch_tile<PAIR, 16, 32, 1, 2, PAIR ? 64 : 128>(p, s);
 }
 
 }  // namespace

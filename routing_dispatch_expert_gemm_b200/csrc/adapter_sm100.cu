@@ -39,6 +39,7 @@ constexpr int kShrinkWarps = 8;
 constexpr int kShrinkTokens = 16;  // MMA rows
 constexpr int kShrinkRanks = 32;   // ranks per pass: 4 MMA column blocks
 constexpr int kMaxBlockAdapters = 64;
+constexpr int kMaxParts = 8;         // pieces of the contraction, in the split form
 
 struct ShrinkParams {
   const __nv_bfloat16* x;
@@ -47,6 +48,8 @@ struct ShrinkParams {
   const int32_t* ids;
   const int32_t* n_tokens;
   uint4* u;         // [2, T, rank / 8]: 8 ranks as 8 high and 8 low bf16 halves (2 vectors)
+  float* u_parts;   // else [parts, 2, T, rank]: fp32 sums of `parts` pieces of the contraction
+  int parts;        // 0: u
   int32_t* blocks;  // [token blocks][1 + kMaxBlockAdapters]: adapters of each GEMM token block
   int32_t* status;
   int T, d_in, n, rank, block_tokens;
@@ -92,18 +95,18 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Partial product of one warp: its share of the contraction of 16 tokens with 8 NB ranks.
+// Partial product of one warp: its share of vectors v_lo .. dv - 1 of the contraction of 16
+// tokens with 8 NB ranks.
 // U 32-wide blocks are loaded before the first MMA (one at a time the loads' latency bounds).
 template <int NB>
 __device__ __forceinline__ void shrink_partial(float (&c)[4][4], const __nv_bfloat16* x0,
                                                const __nv_bfloat16* x1, const __nv_bfloat16* ar,
-                                               int d_in, int warp, int q) {
+                                               int d_in, int v_lo, int dv, int warp, int q) {
   constexpr int U = NB == 4 ? 2 : 4;
   constexpr int kStep = 4 * kShrinkWarps;  // vectors between a warp's blocks
-  const int dv = d_in / 8;
   const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-  for (int v0 = warp * 4; v0 < dv; v0 += U * kStep) {
+  for (int v0 = v_lo + warp * 4; v0 < dv; v0 += U * kStep) {
     uint4 a[U][2], b[U][NB];
 #pragma unroll
     for (int h = 0; h < U; ++h) {
@@ -132,19 +135,22 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
   pdl_trigger();  // the GEMM may start; it waits for this grid before it reads u
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int t0 = blockIdx.x * kShrinkTokens, m = blockIdx.z;
+  const int parts = max(p.parts, 1), m = blockIdx.z / parts, part = blockIdx.z % parts;
+  const int t0 = blockIdx.x * kShrinkTokens;
+  const int dv = p.d_in / 8, blocks = (dv + 3) / 4;  // whole 32-wide blocks to a part
+  const int v_lo = blocks * part / parts * 4, v_hi = min(dv, blocks * (part + 1) / parts * 4);
   const int live = live_tokens(p.n_tokens, p.T);
   const int tiles = (p.T + kShrinkTokens - 1) / kShrinkTokens;
   if (blockIdx.x >= tiles) {  // the CTAs behind the token tiles list the blocks' adapters
     const int tb = blockIdx.x - tiles;
-    if (blockIdx.y == 0 && m == 0 && tb * p.block_tokens < live) list_block_adapters(p, tb, live);
+    if (blockIdx.y == 0 && blockIdx.z == 0 && tb * p.block_tokens < live) list_block_adapters(p, tb, live);
     return;
   }
   if (t0 >= live) return;
   const int nt = min(kShrinkTokens, live - t0);
   int id = lane < nt ? __ldg(p.ids + t0 + lane) : -1;
   if (id < -1 || id >= p.n) {
-    if (blockIdx.y == 0 && m == 0 && warp == 0) record_status(p.status, MOE_ERR_BAD_ADAPTER_ID);
+    if (blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) record_status(p.status, MOE_ERR_BAD_ADAPTER_ID);
     id = -1;
   }
   const uint32_t same = __match_any_sync(0xffffffffu, id);
@@ -164,10 +170,10 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
       const int nb = min(4, (p.rank - j0) / 8);  // rank is a multiple of 8
       const __nv_bfloat16* ar = A + static_cast<size_t>(j0 + g) * p.d_in;
       float c[4][4] = {};
-      if (nb == 1) shrink_partial<1>(c, x0, x1, ar, p.d_in, warp, q);
-      else if (nb == 2) shrink_partial<2>(c, x0, x1, ar, p.d_in, warp, q);
-      else if (nb == 3) shrink_partial<3>(c, x0, x1, ar, p.d_in, warp, q);
-      else shrink_partial<4>(c, x0, x1, ar, p.d_in, warp, q);
+      if (nb == 1) shrink_partial<1>(c, x0, x1, ar, p.d_in, v_lo, v_hi, warp, q);
+      else if (nb == 2) shrink_partial<2>(c, x0, x1, ar, p.d_in, v_lo, v_hi, warp, q);
+      else if (nb == 3) shrink_partial<3>(c, x0, x1, ar, p.d_in, v_lo, v_hi, warp, q);
+      else shrink_partial<4>(c, x0, x1, ar, p.d_in, v_lo, v_hi, warp, q);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         red[warp][g][8 * n + 2 * q] = c[n][0];
@@ -187,14 +193,20 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
         }
         v[0] *= sc;
         v[1] *= sc;
-        const uint32_t hi = gemm::pack_bf16(v[0], v[1]);
-        const uint32_t lo = gemm::pack_bf16(v[0] - __uint_as_float(hi << 16),
-                                            v[1] - __uint_as_float(hi & 0xffff0000u));
-        uint32_t* u = reinterpret_cast<uint32_t*>(
-            p.u + ((static_cast<size_t>(m) * p.T + t0 + t) * p.rank + j0) / 4) + (j / 8) * 8 +
-            (j % 8) / 2;
-        u[0] = hi;
-        u[4] = lo;
+        if (p.parts > 0) {
+          *reinterpret_cast<float2*>(
+              p.u_parts + ((static_cast<size_t>(part) * 2 + m) * p.T + t0 + t) * p.rank + j0 + j) =
+              make_float2(v[0], v[1]);
+        } else {
+          const uint32_t hi = gemm::pack_bf16(v[0], v[1]);
+          const uint32_t lo = gemm::pack_bf16(v[0] - __uint_as_float(hi << 16),
+                                              v[1] - __uint_as_float(hi & 0xffff0000u));
+          uint32_t* u = reinterpret_cast<uint32_t*>(
+              p.u + ((static_cast<size_t>(m) * p.T + t0 + t) * p.rank + j0) / 4) + (j / 8) * 8 +
+              (j % 8) / 2;
+          u[0] = hi;
+          u[4] = lo;
+        }
       }
       __syncthreads();
     }
@@ -233,6 +245,8 @@ struct GemmMaps {
 struct GemmParams {
   const __nv_bfloat16* b[2];
   const uint4* u;
+  const float* u_parts;  // with `parts` > 0 instead of u
+  int parts;
   const int32_t* blocks;
   const int32_t* ids;
   const __nv_bfloat16* addend;
@@ -277,7 +291,16 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
       for (int at = lane; at < kChunk * eights; at += 32) {
         const int t = at / eights;
         float h[8] = {}, l[8] = {};
-        if ((with >> t) & 1u) {
+        if (((with >> t) & 1u) && p.parts > 0) {
+          const float4* f = reinterpret_cast<const float4*>(
+              p.u_parts + (static_cast<size_t>(m) * p.T + t0) * p.rank) + 2 * at;
+#pragma unroll 4
+          for (int k = 0; k < p.parts; ++k, f += static_cast<size_t>(p.T) * p.rank / 2) {
+            const float4 a = __ldcg(f), b = __ldcg(f + 1);
+            h[0] += a.x; h[1] += a.y; h[2] += a.z; h[3] += a.w;
+            h[4] += b.x; h[5] += b.y; h[6] += b.z; h[7] += b.w;
+          }
+        } else if ((with >> t) & 1u) {
           Vec<__nv_bfloat16>::to_f32(__ldcg(u + 2 * at), h);
           Vec<__nv_bfloat16>::to_f32(__ldcg(u + 2 * at + 1), l);
         }
@@ -703,26 +726,53 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem_base, 2 * ACC_COLS);
 }
 
+// Clusters of `size` CTAs of the GEMM that the current device holds at once: fewer than its SMs
+// suggest, since a cluster stays within one GPC (B200: 74 of 2, 33 of 4, 15 of 8).  A second wave
+// of clusters doubled a 2048x2048 call.
 template <bool PAIR>
-cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, cudaStream_t s) {
+int resident_clusters(int size) {
+  static std::atomic<int> known[64][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int>& slot = known[dev][size == 2 ? 1 : size == 4 ? 2 : 3];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = kGemmSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, adapter_gemm_kernel<PAIR>, &cfg) != cudaSuccess) n = -1;
+    slot.store(n > 0 ? n : -1, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <bool PAIR>
+cudaError_t set_up_gemm() {
   static DeviceOnce once;
-  cudaError_t e = once.run([] {
+  return once.run([] {
     cudaError_t r = cudaFuncSetAttribute(adapter_gemm_kernel<PAIR>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
     return r != cudaSuccess ? r : prefer_max_shared(adapter_gemm_kernel<PAIR>);
   });
-  if (e != cudaSuccess) return e;
+}
+
+template <bool PAIR>
+cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, cudaStream_t s) {
   constexpr int NT = kTileTokens<PAIR>;
   const int sms = sm_count();
   p.row_blocks = (p.d_out + BW - 1) / BW;
   p.tok_blocks = (p.T + NT - 1) / NT;
   p.boxes = std::min(NT / kTokBox, (p.T + kTokBox - 1) / kTokBox);
   p.stages = std::min(kMaxStages, kRingBytes / ((PAIR ? 2 : 1) * W_BYTES + p.boxes * kBoxBytes));
-  // Few tiles: a cluster per tile, as many CTAs as fit the SMs, each with a K block at least.
   const int64_t tiles = static_cast<int64_t>(p.row_blocks) * p.tok_blocks;
-  const int k_blocks = (p.d_in + BK - 1) / BK;
-  p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= sms && p.split * 2 <= k_blocks) p.split *= 2;
   if (p.split == 1)
     return launch_pdl(adapter_gemm_kernel<PAIR>, dim3(static_cast<unsigned>(std::min<int64_t>(
                                                      tiles, sms))),
@@ -733,6 +783,27 @@ cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, cudaStream_t s) {
 }
 
 }  // namespace
+
+// CTAs that may split the contraction of a tile.  Few tiles: a cluster per tile, as many CTAs as
+// fit the SMs, each with a K block at least.  (The launch takes fewer where the clusters would not
+// all be resident at once.)
+static int gemm_split(const moe_adapter_config& c, bool pair, int sms) {
+  const int nt = pair ? kTileTokens<true> : kTileTokens<false>;
+  const int64_t tiles =
+      static_cast<int64_t>((c.d_out + BW - 1) / BW) * ((static_cast<int64_t>(c.T) + nt - 1) / nt);
+  const int k_blocks = (c.d_in + BK - 1) / BK;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= sms && split * 2 <= k_blocks) split *= 2;
+  return split;
+}
+
+size_t adapter_u_bytes(const moe_adapter_config& c) {
+  // the split form keeps up to kMaxParts pieces; either projection count
+  const size_t one = 2 * static_cast<size_t>(c.T) * c.rank * 4;
+  const bool split = c.dtype == MOE_BF16 && (gemm_split(c, false, sm_count()) > 1 ||
+                                             gemm_split(c, true, sm_count()) > 1);
+  return split ? kMaxParts * one : one;
+}
 
 size_t adapter_block_table_bytes(int T) {
   const size_t blocks = (static_cast<size_t>(T) + kTileTokens<true> - 1) / kTileTokens<true>;
@@ -753,23 +824,40 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   else maps.w[1] = maps.w[0];
   if (!ok) return cudaErrorInvalidValue;
 
+  const int sms = sm_count();
   const int tiles = (c.T + kShrinkTokens - 1) / kShrinkTokens, m = a.pair ? 2 : 1;
-  // deal a tile's adapters over grid.y until the grid covers the SMs twice
-  const int deal = std::max(1, std::min(kShrinkTokens, 2 * sm_count() / (tiles * m)));
+  cudaError_t e = a.pair ? set_up_gemm<true>() : set_up_gemm<false>();
+  if (e != cudaSuccess) return e;
+  int split = gemm_split(c, a.pair, sms);
+  {
+    const int nt = a.pair ? kTileTokens<true> : kTileTokens<false>;
+    const int64_t gemm_tiles = static_cast<int64_t>((c.d_out + BW - 1) / BW) * ((c.T + nt - 1) / nt);
+    while (split > 1 && gemm_tiles > (a.pair ? resident_clusters<true>(split)
+                                             : resident_clusters<false>(split)))
+      split /= 2;
+  }
+  // deal a tile's adapters over grid.y until the grid covers the SMs twice; in the split form,
+  // whose epilogue adds the pieces up, also cut the contraction (blocks of 32 for every warp)
+  const int deal = std::max(1, std::min(kShrinkTokens, 2 * sms / (tiles * m)));
+  const int parts = split == 1 ? 0
+                               : std::max(1, std::min({kMaxParts, 2 * sms / (tiles * m * deal),
+                                                       c.d_in / (32 * kShrinkWarps)}));
   const ShrinkParams sp{static_cast<const bf16*>(a.x),
                         {static_cast<const bf16*>(a.a[0]), static_cast<const bf16*>(a.a[1])},
-                        a.scale, a.ids, a.n_tokens, u, blocks, status, c.T, c.d_in, c.n_adapters, c.rank,
+                        a.scale, a.ids, a.n_tokens, u, reinterpret_cast<float*>(w + L.u), parts,
+                        blocks, status, c.T, c.d_in, c.n_adapters, c.rank,
                         a.pair ? kTileTokens<true> : kTileTokens<false>};
   static DeviceOnce once;
-  cudaError_t e = once.run([] { return prefer_max_shared(adapter_shrink_kernel); });
+  e = once.run([] { return prefer_max_shared(adapter_shrink_kernel); });
   if (e != cudaSuccess) return e;
   const int blocks_n = (c.T + sp.block_tokens - 1) / sp.block_tokens;
-  adapter_shrink_kernel<<<dim3(tiles + blocks_n, deal, m), 32 * kShrinkWarps, 0, s>>>(sp);
+  adapter_shrink_kernel<<<dim3(tiles + blocks_n, deal, m * std::max(parts, 1)), 32 * kShrinkWarps, 0, s>>>(sp);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
-  GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u, blocks, a.ids,
+  GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u,
+               reinterpret_cast<const float*>(w + L.u), parts, blocks, a.ids,
                static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y), a.n_tokens, status,
-               c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, 1};
+               c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, split};
   return a.pair ? launch_gemm<true>(maps, p, s) : launch_gemm<false>(maps, p, s);
 }
 

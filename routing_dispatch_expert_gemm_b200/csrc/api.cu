@@ -163,13 +163,23 @@ moe_status validate_adapter(const moe_adapter_config* c) {
   return MOE_OK;
 }
 
-// Tokens up to which the streaming kernel runs a projection.
-constexpr int kAdapterFewTokens = 32;
+// Whether the streaming kernel runs a call of at most 32 tokens.  It reads the token rows once per
+// CTA, so many tokens beside a large W are better off on tcgen05, whose fixed costs (a second
+// launch, the cluster) are 5 to 20 us.  Measured, rank 16, us streaming / tcgen05:
+//   linear  2048x2048 T=32 17 / 28;   4096x4096 T=16 20 / 20, T=24 25 / 21;
+//   linear  4096x8192 T=12 26 / 25;   14336x4096 T=8 36 / 37, T=24 61 / 39;
+//   gate/up 4096x4096 T=16 31 / 33, T=24 41 / 33;   4096x8192 T=8 40 / 43, T=16 53 / 45.
+bool adapter_streams(const moe_adapter_config& c, bool pair) {
+  if (c.T > 32) return false;
+  if (c.T <= 8 || c.dtype == MOE_F32) return true;
+  const int64_t weights = static_cast<int64_t>(c.d_in) * c.d_out * (pair ? 2 : 1);
+  return weights <= (int64_t{12} << 20) || (c.T <= 16 && weights <= (int64_t{32} << 20));
+}
 
 AdapterLayout adapter_layout(const moe_adapter_config& c) {
   AdapterLayout L{};
   L.u = kWsHeaderBytes;
-  L.blocks = align256(L.u + 2 * static_cast<size_t>(c.T) * c.rank * 4);
+  L.blocks = align256(L.u + adapter_u_bytes(c));
   L.total = align256(L.blocks + adapter_block_table_bytes(c.T));
   return L;
 }
@@ -182,7 +192,8 @@ moe_status adapter_impl(const moe_adapter_config* cfg, const AdapterArgs& a, voi
   if (a.pair && (!a.w[1] || !a.a[1] || !a.b[1])) return MOE_ERR_INVALID;
   if (!aligned16({a.x, a.w[0], a.w[1], a.a[0], a.a[1], a.b[0], a.b[1]})) return MOE_ERR_INVALID;
   const AdapterLayout L = adapter_layout(*cfg);
-  if (cfg->T <= kAdapterFewTokens) return cuda_status(launch_adapter_few(*cfg, a, L, ws, stream));
+  if (adapter_streams(*cfg, a.pair))
+    return cuda_status(launch_adapter_few(*cfg, a, L, ws, stream));
   return cuda_status(cfg->dtype == MOE_BF16 ? launch_adapter_sm100(*cfg, a, L, ws, stream)
                                             : launch_adapter_simt(*cfg, a, L, ws, stream));
 }

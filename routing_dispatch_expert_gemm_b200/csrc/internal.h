@@ -207,12 +207,13 @@ struct AdapterArgs {
   bool pair;           // SwiGLU of the two projections
 };
 struct AdapterLayout {
-  size_t u;       // byte offset of u: [2, T, rank], 4 bytes each
+  size_t u;       // byte offset of u: [2, T, rank], 4 bytes each (or several such pieces)
   size_t blocks;  // of the adapters per GEMM token block (adapter_sm100.cu)
   size_t total;   // bytes in all
 };
 // bf16, any T: shrink launch + tcgen05 GEMM.
-// Bytes of its table of adapters per token block.
+// Bytes of its u, and of its table of adapters per token block.
+size_t adapter_u_bytes(const moe_adapter_config& c);
 size_t adapter_block_table_bytes(int T);
 cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs& a,
                                  const AdapterLayout& L, void* ws, cudaStream_t s);
