@@ -3,12 +3,12 @@
 //   p[t] = W x_t + s_a B_a (A_a x_t);  y[t] = p[t] (+ addend[t])  or  SiLU(p_gate) * p_up
 // CUDA cores, as the fp32 expert FFN: tf32 cannot meet its tolerance.  Two launches:
 //   shrink  u[t] = s_a A_a x_t, one warp per token and four ranks.
-//   GEMM    tiles of BT tokens x BC rows of W, staged BKF columns at a time in shared memory
-//           with the next stage's loads in registers; the epilogue adds B_a u.  Bound by FMA
-//           (128 per SM and clock).  Two tile sizes: 64 x 64 (4 x 4 outputs per thread, one
-//           shared float4 load per 8 FMA) when its tiles cover the SMs, else 16 x 32 (1 x 2),
-//           which reads shared memory more often but keeps small batches on all SMs, and
-//           whose stages are longer, because the loads' latency bounds it.
+//   GEMM    with enough tiles for the SMs, tiles of 64 tokens x 64 rows of W staged 32 columns
+//           at a time in shared memory, the next stage's loads in registers, 4 x 4 outputs per
+//           thread (bound by FMA, 128 per SM and clock); else a warp per 4 tokens x 4 rows,
+//           its lanes splitting the contraction, straight from L1 (T=77, 1000x516: 33 us with
+//           small shared-memory tiles, whose latencies follow one another).  The epilogue adds
+//           B_a u.
 #include <algorithm>
 
 #include "gemm_common.cuh"
@@ -74,6 +74,35 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const Simt
     *reinterpret_cast<float4*>(p.u + (static_cast<size_t>(m) * p.T + t) * p.rank + j0) =
         make_float4(sc * s[0], sc * s[1], sc * s[2], sc * s[3]);
   }
+}
+
+// Adds B_a u to output (t, c) of each projection, finishes and stores it.
+template <bool PAIR>
+__device__ __forceinline__ void finish_f32(const SimtParams& p, float (&v)[PAIR ? 2 : 1], int t,
+                                           int c) {
+  constexpr int M = PAIR ? 2 : 1;
+  const int id = __ldg(p.ids + t);
+  if (id >= 0 && id < p.n) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const float4* u =
+          reinterpret_cast<const float4*>(p.u + (static_cast<size_t>(m) * p.T + t) * p.rank);
+      const float4* b = reinterpret_cast<const float4*>(
+          p.b[m] + (static_cast<size_t>(id) * p.d_out + c) * p.rank);
+      float s = 0.f;
+#pragma unroll 4
+      for (int r = 0; r < p.rank / 4; ++r) {
+        const float4 uv = __ldcg(u + r), bv = __ldg(b + r);
+        s = fmaf(uv.x, bv.x, fmaf(uv.y, bv.y, fmaf(uv.z, bv.z, fmaf(uv.w, bv.w, s))));
+      }
+      v[m] += s;
+    }
+  }
+  const size_t o = static_cast<size_t>(t) * p.d_out + c;
+  float out = v[0];
+  if constexpr (PAIR) out = out / (1.f + expf(-out)) * v[M - 1];
+  else if (p.addend != nullptr) out += p.addend[o];
+  p.y[o] = out;
 }
 
 template <bool PAIR, int BT, int BC, int RT, int RC, int BKF>
@@ -145,38 +174,87 @@ __global__ void __launch_bounds__(kThreads) adapter_gemm_f32_kernel(const SimtPa
     }
   }
   pdl_wait();  // u is complete; what read y before this call is done
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < RT; ++i) {
     const int t = t0 + ty * RT + i;
     if (t >= live) continue;
-    int id = __ldg(p.ids + t);
-    if (id < 0 || id >= p.n) id = -1;
 #pragma unroll
     for (int j = 0; j < RC; ++j) {
-      const int c = c0 + tx * RC + j;
-      if (c >= p.d_out) continue;
+      float v[M];
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        if (id < 0) continue;
-        const float4* u = reinterpret_cast<const float4*>(
-            p.u + (static_cast<size_t>(m) * p.T + t) * p.rank);
-        const float4* b = reinterpret_cast<const float4*>(
-            p.b[m] + (static_cast<size_t>(id) * p.d_out + c) * p.rank);
-        float v = 0.f;
-#pragma unroll 4
-        for (int r = 0; r < p.rank / 4; ++r) {
-          const float4 uv = __ldcg(u + r), bv = __ldg(b + r);
-          v = fmaf(uv.x, bv.x, fmaf(uv.y, bv.y, fmaf(uv.z, bv.z, fmaf(uv.w, bv.w, v))));
-        }
-        acc[m][i][j] += v;
+        v[m] = acc[m][0][j];
+#pragma unroll
+        for (int q = 1; q < RT; ++q) v[m] = i == q ? acc[m][q][j] : v[m];
       }
-      const size_t o = static_cast<size_t>(t) * p.d_out + c;
-      float out = acc[0][i][j];
-      if constexpr (PAIR) out = out / (1.f + expf(-out)) * acc[M - 1][i][j];
-      else if (p.addend != nullptr) out += p.addend[o];
-      p.y[o] = out;
+      if (c0 + tx * RC + j < p.d_out) finish_f32<PAIR>(p, v, t, c0 + tx * RC + j);
     }
   }
+}
+
+// A warp per kWT tokens x kWC rows of W.
+constexpr int kWT = 4, kWC = 4;
+template <bool PAIR>
+__global__ void __launch_bounds__(kThreads) adapter_warp_f32_kernel(const SimtParams p) {
+  constexpr int M = PAIR ? 2 : 1;
+  const int live = live_tokens(p);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // 2 x 4 warps of a CTA share token and weight rows through L1
+  const int t0 = (blockIdx.x * 2 + warp / 4) * kWT, c0 = (blockIdx.y * 4 + warp % 4) * kWC;
+  if (t0 >= live || c0 >= p.d_out) return;
+  const int dv = p.d_in / 4;
+  const float4* x[kWT];
+  const float4* w[M][kWC];
+#pragma unroll
+  for (int i = 0; i < kWT; ++i)  // rows past the last one: the last one's, not stored
+    x[i] = reinterpret_cast<const float4*>(p.x + static_cast<size_t>(min(t0 + i, live - 1)) * p.d_in);
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int j = 0; j < kWC; ++j)
+      w[m][j] = reinterpret_cast<const float4*>(
+          p.w[m] + static_cast<size_t>(min(c0 + j, p.d_out - 1)) * p.d_in);
+  float acc[M][kWT][kWC] = {};
+#pragma unroll 2
+  for (int v = lane; v < dv; v += 32) {
+    float4 xv[kWT], wv[M][kWC];
+#pragma unroll
+    for (int i = 0; i < kWT; ++i) xv[i] = __ldg(x[i] + v);
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int j = 0; j < kWC; ++j) wv[m][j] = __ldg(w[m][j] + v);
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int i = 0; i < kWT; ++i)
+#pragma unroll
+        for (int j = 0; j < kWC; ++j) {
+          float& s = acc[m][i][j];
+          s = fmaf(xv[i].x, wv[m][j].x, s);
+          s = fmaf(xv[i].y, wv[m][j].y, s);
+          s = fmaf(xv[i].z, wv[m][j].z, s);
+          s = fmaf(xv[i].w, wv[m][j].w, s);
+        }
+  }
+  // lane l < 16 gets the total of output (l / 4, l % 4)
+  float v[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    v[m] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWT; ++i)
+#pragma unroll
+      for (int j = 0; j < kWC; ++j) {
+        float s = acc[m][i][j];
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == i * kWC + j) v[m] = s;
+      }
+  }
+  pdl_wait();  // u is complete; what read y before this call is done
+  const int t = t0 + lane / kWC, c = c0 + lane % kWC;
+  if (lane < kWT * kWC && t < live && c < p.d_out) finish_f32<PAIR>(p, v, t, c);
 }
 
 template <bool PAIR, int BT, int BC, int RT, int RC, int BKF>
@@ -195,8 +273,13 @@ cudaError_t launch_tile(const SimtParams& p, cudaStream_t s) {
 template <bool PAIR>
 cudaError_t launch_gemm_f32(const SimtParams& p, cudaStream_t s) {
   const int64_t big = static_cast<int64_t>((p.d_out + 63) / 64) * ((p.T + 63) / 64);
-  return big >= sm_count() ? launch_tile<PAIR, 64, 64, 4, 4, 32>(p, s)
-                           : launch_tile<PAIR, 16, 32, 1, 2, PAIR ? 64 : 128>(p, s);
+  const int rows = (p.d_out + 4 * kWC - 1) / (4 * kWC);
+  if (big * 2 >= sm_count() || rows > 65535) return launch_tile<PAIR, 64, 64, 4, 4, 32>(p, s);
+  static DeviceOnce once;
+  const cudaError_t e = once.run([] { return prefer_max_shared(adapter_warp_f32_kernel<PAIR>); });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(adapter_warp_f32_kernel<PAIR>, dim3((p.T + 2 * kWT - 1) / (2 * kWT), rows),
+                    dim3(kThreads), 0, s, p);
 }
 
 }  // namespace
