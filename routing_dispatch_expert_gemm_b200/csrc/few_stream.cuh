@@ -22,7 +22,7 @@
 //     the pipe needs 2 * 8 FLOP per weight (about 53 TFLOP/s at the full HBM rate), far
 //     below even the warp-level MMA rate, and there is no tensor-memory round trip at the
 //     end of a 7-row tile; that is why this is not tcgen05, whose M is at least 64 rows.
-//     fp32: FMA, one weight row per lane.
+//     fp32: FMA, a weight row per lane.
 //   * The 8 partial sums per output meet in shared memory in warp order (which slots a warp
 //     takes depends on the shape alone, so runs give the same bits); the caller's epilogue
 //     consumes a tile's total while the next tile's slots are already being consumed.
@@ -467,29 +467,38 @@ template <int NT> struct Acc<false, NT> {
     }
   }
 };
+// fp32: lane = row, and where the tile has fewer than 32 rows the lanes behind the rows (a power
+// of two) take other parts of the contraction: with one row per lane alone, a 5-row tile left 27
+// lanes to repeat it and the FMAs bound it.
 template <int NT> struct Acc<true, NT> {
   float c[8 * NT];
+  int rows, r0;  // lanes per part of the contraction; rows of the first row block
   __device__ __forceinline__ void zero() {
+    rows = 32;
+    r0 = 16;
 #pragma unroll
     for (int n = 0; n < 8 * NT; ++n) c[n] = 0.f;
   }
   __device__ __forceinline__ void chunk(const SlotDesc& d, const Shared& s, int part, int lane) {
     constexpr int P = kPitch<true>;
+    constexpr int V = 8;  // vectors of the row held together
+    const int n_rows = d.r0 + d.r1;
+    rows = n_rows > 16 ? 32 : n_rows > 8 ? 16 : n_rows > 4 ? 8 : 4;
+    r0 = d.r0;
+    const int ks = 32 / rows, k = lane / rows;  // parts of the contraction, this lane's
     const uint32_t base = smem_u32(s.ring) + d.off;
     const int nb = __popc(d.mask);
-    const int row = lane < 16 || d.r1 == 0 ? min(lane, d.r0 - 1)
-                                           : d.r0 + min(lane - 16, d.r1 - 1);
-    const uint32_t a = base + row * P;
-    const uint32_t b = base + (d.r0 + d.r1) * P;
-    constexpr int V = 8;  // vectors of the row held together
+    const uint32_t a = base + min(lane & (rows - 1), n_rows - 1) * P + k * 16;
+    const uint32_t b = base + n_rows * P + k * 16;
 #pragma unroll 1
-    for (int v0 = part * V; v0 < d.kvec; v0 += V * kGroupWarps<NT>) {
+    for (int v0 = part * V * ks; v0 < d.kvec; v0 += V * ks * kGroupWarps<NT>) {
+      const int left = d.kvec - v0 - k;  // this lane's vectors: 0, ks, 2 ks, ...
       float w[V][4];
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        Vec<float>::to_f32(v0 + i < d.kvec ? lds_vec(a + (v0 + i) * 16) : make_uint4(0, 0, 0, 0),
+        Vec<float>::to_f32(i * ks < left ? lds_vec(a + (v0 + i * ks) * 16) : make_uint4(0, 0, 0, 0),
                            w[i]);
-      const int left = d.kvec - v0;
+      const bool full = v0 + V * ks <= d.kvec;
 #pragma unroll
       for (int n = 0; n < 8 * NT; ++n) {
         int slot = n;
@@ -501,23 +510,33 @@ template <int NT> struct Acc<true, NT> {
         }
         const uint32_t xb = b + slot * P + v0 * 16;
         float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        float x[V][4];
+        if (full) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (i < left) {
-            float x[4];
-            Vec<float>::to_f32(lds_vec(xb + i * 16), x);
+          for (int i = 0; i < V; ++i) Vec<float>::to_f32(lds_vec(xb + i * ks * 16), x[i]);
+        } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s4[j] = fmaf(w[i][j], x[j], s4[j]);
-          }
+          for (int i = 0; i < V; ++i)
+            Vec<float>::to_f32(i * ks < left ? lds_vec(xb + i * ks * 16) : make_uint4(0, 0, 0, 0),
+                               x[i]);
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s4[j] = fmaf(w[i][j], x[i][j], s4[j]);
         c[n] += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       }
     }
   }
   __device__ __forceinline__ void store(float* red, int warp, int lane) const {
     float* w = red + warp * (8 * NT * kRedStride);
+    const int at = lane < r0 ? lane : 16 + lane - r0;  // the second row block begins at 16
 #pragma unroll
-    for (int n = 0; n < 8 * NT; ++n) w[n * kRedStride + lane] = c[n];
+    for (int n = 0; n < 8 * NT; ++n) {
+      float v = c[n];
+      for (int o = rows; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane < rows && at < 32) w[n * kRedStride + at] = v;
+    }
   }
 };
 
