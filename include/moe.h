@@ -266,10 +266,13 @@ moe_status moe_forward(const moe_config* cfg, const void* x, const void* w_route
  *               gate 0, and a token with no other logit has only zero gates, so its routed
  *               part is zero.
  *   y           may be x itself.
- * cfg->tiles is ignored.  MOE_ERR_UNSUPPORTED: T > 32, stats, the padded layout, the reroute
- * policy, fused steps.  MOE_ERR_INVALID also for x or weights that are not 16-byte aligned.
+ * cfg->tiles is ignored.  MOE_ERR_UNSUPPORTED: T > 32, d or d_ff above 2^24, (E + 1) * d_ff of
+ * 2^31 or more, stats, the padded layout, the reroute policy, fused steps.  MOE_ERR_INVALID also for x or weights that are not 16-byte aligned.
  * The kernel occupies every SM (a cooperative launch) and can be captured into a graph.  If
- * it ever reports MOE_ERR_TIMEOUT, call moe_workspace_init before the workspace's next use.
+ * it ever reports MOE_ERR_TIMEOUT, clear the status (moe_get_device_status) or call
+ * moe_workspace_init before the workspace's next use.  Up to 8 tokens it is faster than
+ * moe_forward, up to 16 as fast or faster, beyond that slower on large experts: it reads the
+ * token rows once per CTA.
  * Source: "271,104 Routes...", section 5 (with small batches the cost is moving weights). */
 moe_status moe_forward_few(const moe_config* cfg, const void* x, const void* w_router,
                            const float* logit_bias, const void* w_gate, const void* w_up,
@@ -288,7 +291,8 @@ typedef struct {
   int32_t dtype;       /* moe_dtype                                                       */
 } moe_adapter_config;
 /* Supported shapes (else MOE_ERR_UNSUPPORTED): d_in, d_out and rank are multiples of 8 (bf16)
- * or 4 (fp32); rank <= 128; T <= 2^24; d_out <= 2^20; T * d_in, T * d_out and d_in * d_out below 2^40.  */
+ * or 4 (fp32); rank <= 128; T, d_in <= 2^24; d_out <= 2^20; T * d_in, T * d_out and
+ * d_in * d_out below 2^40.                                                              */
 
 /* Bytes of workspace of the two calls below; 0 for an invalid config.                     */
 size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg);
@@ -336,7 +340,8 @@ moe_status moe_forward_profiled(const moe_config* cfg, const void* x, const void
                                 void* ws, moe_stream_t stream);
 
 /* Synchronise `stream`, copy the device status word of `ws` to *status_out (a moe_status)
- * and, if clear != 0, reset it to MOE_OK.  Returns MOE_ERR_CUDA if the copy fails.      */
+ * and, if clear != 0, reset it to MOE_OK (after MOE_ERR_TIMEOUT the whole header, as
+ * moe_workspace_init does).  Returns MOE_ERR_CUDA if the copy fails.                    */
 moe_status moe_get_device_status(void* ws, moe_stream_t stream, int32_t clear,
                                  int32_t* status_out);
 

@@ -158,7 +158,7 @@ moe_status validate_adapter(const moe_adapter_config* c) {
   const int64_t limit = int64_t{1} << 40;
   if (c->T > (1 << 24) || static_cast<int64_t>(c->T) * c->d_in >= limit ||
       static_cast<int64_t>(c->T) * c->d_out >= limit ||
-      static_cast<int64_t>(c->d_in) * c->d_out >= limit || c->d_out > (1 << 20))
+      static_cast<int64_t>(c->d_in) * c->d_out >= limit || c->d_out > (1 << 20) || c->d_in > (1 << 24))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -477,7 +477,9 @@ moe_status moe_get_device_status(void* ws, moe_stream_t stream, int32_t clear,
   if (cudaStreamSynchronize(stream) != cudaSuccess) return MOE_ERR_CUDA;
   int32_t v = 0;
   if (cudaMemcpy(&v, ws, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  if (clear && cudaMemset(ws, 0, sizeof(int32_t)) != cudaSuccess) return MOE_ERR_CUDA;
+  // after a timeout the header's tickets and barrier counts may stand anywhere: all start again
+  const size_t bytes = v == MOE_ERR_TIMEOUT ? kWsHeaderBytes : sizeof(int32_t);
+  if (clear && cudaMemset(ws, 0, bytes) != cudaSuccess) return MOE_ERR_CUDA;
   *status_out = v;
   return MOE_OK;
 }

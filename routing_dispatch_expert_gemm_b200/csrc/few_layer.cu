@@ -547,7 +547,7 @@ FewLayout few_layer_layout(const moe_config& c) {
 }
 
 bool few_layer_supported(const moe_config& c) {
-  return c.T <= kMaxTokens && c.d_ff <= (1 << 24) &&
+  return c.T <= kMaxTokens && c.d <= (1 << 24) && c.d_ff <= (1 << 24) &&
          (c.E + 1) * static_cast<int64_t>(c.d_ff) <= INT_MAX && !c.stats && c.layout == MOE_LAYOUT_RAGGED &&
          c.overflow == MOE_OVERFLOW_DROP && c.fuse == MOE_FUSE_NONE;
 }

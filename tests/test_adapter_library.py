@@ -39,6 +39,7 @@ SHAPE = dict(T=8, d_in=64, d_out=32, n_adapters=2, rank=8)
     (dict(rank=0), 1), (dict(d_in=60), 2), (dict(d_out=36), 2), (dict(rank=12), 2),
     (dict(rank=136), 2), (dict(d_in=62, dtype="f32"), 2), (dict(rank=6, dtype="f32"), 2),
     (dict(rank=132, dtype="f32"), 2), (dict(T=(1 << 24) + 1), 2),
+    (dict(d_in=(1 << 24) + 8), 2), (dict(d_out=(1 << 20) + 8), 2),
     (dict(d_in=1 << 20, d_out=1 << 20), 2), (dict(T=1 << 20, d_in=1 << 20), 2)])
 def test_shapes(native, kw, code):
     cfg = native.make_adapter_config(**dict(SHAPE, **kw))

@@ -27,7 +27,8 @@ def few(native, cfg, x=FAKE, w_router=FAKE, w_gate=FAKE, w_up=FAKE, w_down=FAKE,
 @pytest.mark.parametrize("kw", [
     dict(T=33), dict(stats=True), dict(layout="padded", capacity=4),
     dict(layout="padded", capacity=4, overflow="reroute"), dict(fuse="gather"),
-    dict(fuse="combine"), dict(d=96), dict(d_ff=130), dict(d=66, dtype="f32"), dict(E=257)])
+    dict(fuse="combine"), dict(d=96), dict(d_ff=130), dict(d=66, dtype="f32"), dict(E=257),
+    dict(d=(1 << 24) + 128), dict(d_ff=(1 << 24) + 128), dict(E=255, d_ff=1 << 23)])
 def test_unsupported(native, kw):
     shape = dict(T=8, d=128, E=4, k=2, d_ff=128)
     shape.update(kw)
