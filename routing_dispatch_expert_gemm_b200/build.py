@@ -24,7 +24,8 @@ SOURCES = ["api.cu", "route.cu", "route_sm100.cu", "dispatch.cu", "reroute.cu", 
            "gemm_sm100.cu", "gemm_cols_sm100.cu", "gemm_pair_sm100.cu",
            "gemm_rowpair_sm100.cu", "combine.cu", "stats.cu",
            "noalloc.cu", "few_layer.cu", "adapter_few.cu",
-           "adapter_sm100.cu", "adapter_simt.cu"]
+           "adapter_sm100.cu", "adapter_pair_sm100.cu",
+           "adapter_simt.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -26,6 +26,7 @@
 // the same bits every run).
 #include <algorithm>
 
+#include "adapter_gemm.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
 
@@ -38,7 +39,6 @@ using gemm::BK;
 constexpr int kShrinkWarps = 8;
 constexpr int kShrinkTokens = 16;  // MMA rows
 constexpr int kShrinkRanks = 32;   // ranks per pass: 4 MMA column blocks
-constexpr int kMaxBlockAdapters = 64;
 constexpr int kMaxParts = 8;         // pieces of the contraction, in the split form
 
 struct ShrinkParams {
@@ -57,7 +57,8 @@ struct ShrinkParams {
 
 // Adapters of token block `tb`, by the whole CTA: their number, then the adapters in the order
 // of their first token; or kMaxBlockAdapters + 1 when the epilogue is to expand them: more than
-// the table holds, or fewer than 16 tokens each (a K block costs about 1.5 us to fill).
+// the table holds, or fewer than 16 tokens each, unless four K blocks hold them (a K block costs
+// up to 1.5 us to fill; the last tokens of a prompt, expanded, cost T=4099 28 us).
 __device__ __forceinline__ void list_block_adapters(const ShrinkParams& p, int tb, int live) {
   __shared__ int s_ids[32 * kShrinkWarps], s_count[kShrinkWarps];
   const int tid = threadIdx.x, t = tb * p.block_tokens + tid;
@@ -77,13 +78,11 @@ __device__ __forceinline__ void list_block_adapters(const ShrinkParams& p, int t
     all += s_count[w];
   }
   int32_t* out = p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters);
-  const bool few = all <= kMaxBlockAdapters && all * 16 <= min(p.block_tokens, live - tb * p.block_tokens);
+  const bool few = all <= kMaxBlockAdapters &&
+                   (all * 16 <= min(p.block_tokens, live - tb * p.block_tokens) ||
+                    all * (p.rank / 8) * 2 <= 4 * 8);
   if (tid == 0) out[0] = few || all == 0 ? all : kMaxBlockAdapters + 1;
   if (first && before < kMaxBlockAdapters) out[1 + before] = id;
-}
-
-__device__ __forceinline__ int live_tokens(const int32_t* n_tokens, int T) {
-  return n_tokens != nullptr ? min(max(__ldg(n_tokens), 0), T) : T;
 }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -220,7 +219,6 @@ constexpr int kEpiWarps = 8;
 constexpr int kProducerWarp = kEpiWarps;
 constexpr int kMmaWarp = kEpiWarps + 1;
 constexpr int kExtWarp0 = kEpiWarps + 2;  // two warps fill the adapters' K blocks
-constexpr int kExtThreads = 64;
 constexpr int kGemmThreads = 32 * (kEpiWarps + 2) + kExtThreads;
 constexpr int W_BYTES = BW * BK * 2;
 constexpr int kBoxBytes = kTokBox * BK * 2;
@@ -346,33 +344,6 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
       if (i < cnt) y[static_cast<size_t>(i) * p.d_out] = __float2bfloat16_rn(o);
     }
   }
-}
-
-// Barrier of the ext warps; whether `v` held on all of their threads.
-__device__ __forceinline__ bool ext_all(bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 2, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "n"(kExtThreads)
-      : "memory");
-  return r != 0;
-}
-// Zeros the infinities and NaNs among 8 bf16 of shared memory; whether there were any.
-__device__ __forceinline__ bool zero_nonfinite(uint8_t* p) {
-  uint4 v = *reinterpret_cast<const uint4*>(p);
-  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if ((w[i] & 0x7f800000u) == 0x7f800000u) { w[i] &= 0x0000ffffu; any = true; }
-    if ((w[i] & 0x7f80u) == 0x7f80u) { w[i] &= 0xffff0000u; any = true; }
-  }
-  if (any) *reinterpret_cast<uint4*>(p) = v;
-  return any;
 }
 
 // Totals of `cnt` tokens of one weight row over the cluster's S partial tiles, in rank order,
@@ -824,6 +795,7 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   else maps.w[1] = maps.w[0];
   if (!ok) return cudaErrorInvalidValue;
 
+  const bool pairs = adapter_pair_fits(c, a.pair);
   const int sms = sm_count();
   const int tiles = (c.T + kShrinkTokens - 1) / kShrinkTokens, m = a.pair ? 2 : 1;
   cudaError_t e = a.pair ? set_up_gemm<true>() : set_up_gemm<false>();
@@ -846,7 +818,7 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
                         {static_cast<const bf16*>(a.a[0]), static_cast<const bf16*>(a.a[1])},
                         a.scale, a.ids, a.n_tokens, u, reinterpret_cast<float*>(w + L.u), parts,
                         blocks, status, c.T, c.d_in, c.n_adapters, c.rank,
-                        a.pair ? kTileTokens<true> : kTileTokens<false>};
+                        pairs ? kPairBlockTokens : a.pair ? kTileTokens<true> : kTileTokens<false>};
   static DeviceOnce once;
   e = once.run([] { return prefer_max_shared(adapter_shrink_kernel); });
   if (e != cudaSuccess) return e;
@@ -854,6 +826,7 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   adapter_shrink_kernel<<<dim3(tiles + blocks_n, deal, m * std::max(parts, 1)), 32 * kShrinkWarps, 0, s>>>(sp);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
+  if (pairs) return launch_adapter_pair(c, a, u, blocks, status, s);
   GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u,
                reinterpret_cast<const float*>(w + L.u), parts, blocks, a.ids,
                static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y), a.n_tokens, status,

@@ -135,6 +135,10 @@ CASES = [
     (300, 648, 392, 3, 24, "bf16", "none", None),
     (777, 512, 2048, 6, 32, "bf16", "requests", 700),
     (1031, 264, 5000, 9, 16, "bf16", "tokens", None),
+    (1024, 136, 4872, 3, 8, "bf16", "requests", None),
+    (1500, 264, 4104, 200, 16, "bf16", "tokens", None),
+    (2047, 72, 2056, 5, 128, "bf16", "requests", 1900),
+    (2500, 1032, 1944, 40, 24, "bf16", "one", 2305),
     (33, 68, 36, 5, 4, "f32", "tokens", 33),
     (77, 1000, 516, 5, 12, "f32", "tokens", 70),
     (300, 132, 260, 3, 64, "f32", "requests", None),
@@ -169,7 +173,7 @@ def test_padding_ids_and_scale(N, T, dtype):
     assert bool((call(N, bad, False, n_tokens=2)[2:] == 7.0).all())
 
 
-@pytest.mark.parametrize("T", [12, 150])
+@pytest.mark.parametrize("T", [12, 150, 5000])
 def test_in_place_repeat_and_graph(N, T):
     p = make(T, 1024, 512, 6, 16)
     want = call(N, p, False, True)
@@ -253,7 +257,7 @@ def test_layer_with_adapted_shared_expert(N, T):
     assert N.moe_get_device_status(ws) == 0 and N.moe_get_device_status(aws) == 0
 
 
-@pytest.mark.parametrize("T,d_out", [(6, 64), (90, 64), (700, 5000), (700, 64)])
+@pytest.mark.parametrize("T,d_out", [(6, 64), (90, 64), (700, 5000), (700, 64), (1000, 5000)])
 def test_broken_adapter_reaches_its_own_tokens_only(N, T, d_out):
     """Infinities and NaNs in one request's adapter, also in matrices that no token uses."""
     for dtype in ("bf16", "f32"):
