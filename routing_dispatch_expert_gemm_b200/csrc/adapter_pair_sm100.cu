@@ -211,7 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-      int e = 0;  // the adapters' blocks so far: block e comes after (e + 1) / (ext + 1) of W's
+      // The adapters' blocks follow evenly spread ones of W.  Only a compare per K block: this
+      // thread issues one every 512 cycles, and 64-bit products here cost 10 us at T=4099.
+      int e = 0;
+      const int ext_step = ext > 0 ? max(1, k_blocks / (ext + 1)) : k_blocks;
+      int ext_at = ext > 0 ? min(ext_step, k_blocks) : k_blocks;
       for (int kb = 0; kb < k_blocks && ok; ++kb) {
         if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs, p.status)) {
           ok = false;
@@ -225,9 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_mma_bf16_pair(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
         tc_commit_pair_mc(&empty[stage], 0x3);  // frees the stage in both SMs
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
-        while (e < ext && (kb + 1 == k_blocks ||
-                           static_cast<int64_t>(kb + 1) * (ext + 1) >=
-                               static_cast<int64_t>(e + 1) * k_blocks)) {
+        if (kb + 1 != ext_at) continue;
+        ext_at = min(ext_at + ext_step, k_blocks);
+        // one block, after W's last block all that are left
+        for (const int upto = kb + 1 == k_blocks ? ext : min(e + 1, ext); e < upto; ++e) {
           if (!mbar_wait_bounded(ext_full, ext_phase, abort_flag, kWaitLimitNs, p.status)) {
             ok = false;
             break;
@@ -239,7 +244,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < BK / 16; ++kk)
             tc_mma_bf16_pair(d_tmem, ea + 2 * kk, eb + 2 * kk, idesc, 1u);
           tc_commit_pair_mc(ext_empty, 0x3);
-          ++e;
         }
       }
       if (!ok) break;
