@@ -126,14 +126,16 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
   const int c0 = static_cast<int>(share_begin(rows_w, blockIdx.x));
   const int c1 = static_cast<int>(share_begin(rows_w, blockIdx.x + 1));
   const int dv = p.d_in / VEC;
-  const int chunks = (dv + kChunkVecs - 1) / kChunkVecs;
+  // chunks of the two phases
+  const int vecs[2] = {chunk_vecs(min(kTileRows, a1 - a0) + live, dv),
+                       chunk_vecs(M * min(TILE, c1 - c0) + live, dv)};
+  const int chunks[2] = {(dv + vecs[0] - 1) / vecs[0], (dv + vecs[1] - 1) / vecs[1]};
   auto shrink_rows = [&](int at) {  // rows of the shrink tile at `at`: within one matrix
     return min(min(kTileRows, a1 - at), p.rank - at % p.rank);
   };
 
   if (warp >= kConsumerWarps) {
     // ------------------------------------------------------------------ producers
-    constexpr uint32_t P = kPitch<F32>;
     const size_t xs = static_cast<size_t>(p.d_in) * sizeof(Tin);
     const uint8_t* xb = static_cast<const uint8_t*>(p.x);
     Producer<F32> pr(s, p.status);
@@ -142,21 +144,23 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
     auto tile = [&](const uint8_t* w0, int n0, const uint8_t* w1, int n1, uint32_t mask, int seg,
                     int row, int kind) {
       const uint32_t rows = n0 + n1 + __popc(mask);
-      int c = blockIdx.x % chunks;  // not all CTAs read the same token chunk at once
-      for (int i = 0; i < chunks; ++i, c = c + 1 == chunks ? 0 : c + 1) {
-        const int kv = c * kChunkVecs;
+      const int cv = kind == 0 ? vecs[0] : vecs[1], nc = kind == 0 ? chunks[0] : chunks[1];
+      const uint32_t P = pitch_of<F32>(cv);
+      int c = blockIdx.x % nc;  // not all CTAs read the same token chunk at once
+      for (int i = 0; i < nc; ++i, c = c + 1 == nc ? 0 : c + 1) {
+        const int kv = c * cv;
         pr.reserve(rows * P);
         if (pr.mine()) {
           if (pr.ready(rows * P, 0xffffffffu) != 1) { go = false; return; }
-          const int n = min(kChunkVecs, dv - kv);
+          const int n = min(cv, dv - kv);
           const uint32_t bytes = n * 16, o = kv * 16;
           pr.open(SlotDesc{0, static_cast<int16_t>(n0), static_cast<int16_t>(n1),
-                           static_cast<int16_t>(n), i + 1 == chunks,
-                           static_cast<int8_t>(kind), mask, 0, seg, row, kv},
+                           static_cast<int16_t>(n), static_cast<int16_t>(P), i + 1 == nc,
+                           static_cast<int8_t>(kind), 0, 0, mask, seg, row, kv},
                   rows * bytes);
-          pr.copy_rows(pr.it, pr.head, 0, w0 + o, xs, n0, bytes);
-          pr.copy_rows(pr.it, pr.head, n0, w1 + o, xs, n1, bytes);
-          pr.copy_tokens(pr.it, pr.head, n0 + n1, xb + o, xs, mask, bytes);
+          pr.copy_rows(pr.it, pr.head, P, 0, w0 + o, xs, n0, bytes);
+          pr.copy_rows(pr.it, pr.head, P, n0, w1 + o, xs, n1, bytes);
+          pr.copy_tokens(pr.it, pr.head, P, n0 + n1, xb + o, xs, mask, bytes);
         }
         pr.pass(rows * P);
       }
@@ -213,7 +217,6 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
 #pragma unroll 1
     for (int at = a0; at < a1; ++a_tiles) at += shrink_rows(at);
     const int tiles[2] = {a_tiles, (c1 - c0 + TILE - 1) / TILE};
-    const int n_chunks[2] = {chunks, chunks};
     bool waited = nseg == 0;
     auto epilogue = [&](const SlotDesc& d, const float* red) {
       if (d.kind == 0) {
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
       if (tid == 0) grid_arrive(p.sync);
       return well;
     };
-    consume<F32, NT>(s, tiles, n_chunks, p.status, epilogue, between);
+    consume<F32, NT>(s, tiles, chunks, p.status, epilogue, between);
   }
   __syncthreads();
   if (tid == 0 && *s.abort_flag == 0) grid_leave(p.sync);

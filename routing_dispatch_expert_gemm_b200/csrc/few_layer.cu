@@ -350,10 +350,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
   const int g0 = nseg > 0 ? tb.lo : 0, g1 = nseg > 0 ? tb.hi : 0;
   const int c0 = tb.c0, c1 = tb.c1;
   const int dv = p.d / VEC, fv = p.F / VEC;  // 16-byte vectors of a row
+  // chunks of the two phases
+  const int gu_vecs = chunk_vecs(2 * min(16, g1 - g0) + live, dv);
+  const int dn_vecs = chunk_vecs(min(kTileRows, c1 - c0) + live, fv);
 
   if (warp >= kConsumerWarps) {
     // ------------------------------------------------------------------ producers
-    constexpr uint32_t P = kPitch<F32>;
+    const uint32_t P = pitch_of<F32>(gu_vecs);
     const size_t xs = static_cast<size_t>(p.d) * sizeof(Tin);  // bytes of a row of d
     const size_t hs = static_cast<size_t>(p.F) * sizeof(Tin);  // bytes of a row of F
     Producer<F32> pr(s, p.status);
@@ -369,21 +372,22 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
       const uint8_t* wg = static_cast<const uint8_t*>(sh ? p.s_gate : p.w_gate) + base;
       const uint8_t* wu = static_cast<const uint8_t*>(sh ? p.s_up : p.w_up) + base;
       const uint8_t* xb = static_cast<const uint8_t*>(p.x);
-      const int chunks = (dv + kChunkVecs - 1) / kChunkVecs;
+      const int chunks = (dv + gu_vecs - 1) / gu_vecs;
       int c = blockIdx.x % chunks;  // see DownPos: not all CTAs read the same token chunk
       for (int i = 0; i < chunks; ++i, c = c + 1 == chunks ? 0 : c + 1) {
-        const int kv = c * kChunkVecs;
+        const int kv = c * gu_vecs;
         pr.reserve(rows * P);
         if (pr.mine()) {
           if (pr.ready(rows * P, 0xffffffffu) != 1) { go = false; break; }
-          const int n = min(kChunkVecs, dv - kv);
+          const int n = min(gu_vecs, dv - kv);
           const uint32_t bytes = n * 16, o = kv * 16;
           pr.open(SlotDesc{0, static_cast<int16_t>(np), static_cast<int16_t>(np),
-                           static_cast<int16_t>(n), i + 1 == chunks, 0, mask, 0, seg, f0, kv},
+                           static_cast<int16_t>(n), static_cast<int16_t>(P), i + 1 == chunks, 0, 0, 0,
+                           mask, seg, f0, kv},
                   rows * bytes);
-          pr.copy_rows(pr.it, pr.head, 0, wg + o, xs, np, bytes);
-          pr.copy_rows(pr.it, pr.head, np, wu + o, xs, np, bytes);
-          pr.copy_tokens(pr.it, pr.head, 2 * np, xb + o, xs, mask, bytes);
+          pr.copy_rows(pr.it, pr.head, P, 0, wg + o, xs, np, bytes);
+          pr.copy_rows(pr.it, pr.head, P, np, wu + o, xs, np, bytes);
+          pr.copy_tokens(pr.it, pr.head, P, 2 * np, xb + o, xs, mask, bytes);
         }
         pr.pass(rows * P);
       }
@@ -392,12 +396,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     // Down: the weight rows of the slots that fit come before the barrier, their H rows
     // after it.
     const uint32_t first = pr.it;
-    const int fch = (fv + kChunkVecs - 1) / kChunkVecs, pairs = fch * nseg;
+    const uint32_t PD = pitch_of<F32>(dn_vecs);
+    const int fch = (fv + dn_vecs - 1) / dn_vecs, pairs = fch * nseg;
     const int turn = static_cast<int>(static_cast<int64_t>(pairs) * blockIdx.x / gridDim.x);
     DownPos w{c0, min(kTileRows, c1 - c0),
-              turn / fch, turn % fch * kChunkVecs, pairs};
+              turn / fch, turn % fch * dn_vecs, pairs};
     auto next = [&](DownPos& q) {
-      q.kv += kChunkVecs;
+      q.kv += dn_vecs;
       if (q.kv >= fv) {
         q.kv = 0;
         if (++q.seg == nseg) q.seg = 0;
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     };
     auto load_h = [&](uint32_t it) {  // the H rows of slot `it`, one of this warp's
       const SlotDesc& d = s.desc[it % kSlots];
-      pr.copy_rows(it, d.off, d.r0 + d.r1,
+      pr.copy_rows(it, d.off, d.pitch, d.r0 + d.r1,
                    reinterpret_cast<const uint8_t*>(H) + tb.seg_hrow[d.seg] * hs + d.kv * 16, hs,
                    __popc(d.mask), d.kvec * 16);
     };
@@ -429,26 +434,27 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
       const int e = tb.seg_e[w.seg];
       const uint32_t mask = tb.seg_mask[w.seg];
       const uint32_t rows = w.nrows + __popc(mask);
-      pr.reserve(rows * P);
+      pr.reserve(rows * PD);
       if (pr.mine()) {
-        int r = pr.ready(rows * P, passed ? 0xffffffffu : first);
+        int r = pr.ready(rows * PD, passed ? 0xffffffffu : first);
         if (r == 0) {  // the ring is full of slots that wait for H
           pass_barrier();
-          r = go ? pr.ready(rows * P, 0xffffffffu) : -1;
+          r = go ? pr.ready(rows * PD, 0xffffffffu) : -1;
         }
         if (r < 0) { go = false; break; }
-        const int n = min(kChunkVecs, fv - w.kv);
+        const int n = min(dn_vecs, fv - w.kv);
         const bool sh = e == p.E;
         const uint8_t* wd = static_cast<const uint8_t*>(sh ? p.s_down : p.w_down) +
                             ((sh ? 0 : static_cast<size_t>(e) * p.d) + w.row) * hs + w.kv * 16;
         const int r0 = min(16, w.nrows);
         pr.open(SlotDesc{0, static_cast<int16_t>(r0), static_cast<int16_t>(w.nrows - r0),
-                         static_cast<int16_t>(n), w.left == 1, 1, mask, 1, w.seg, w.row, w.kv},
+                         static_cast<int16_t>(n), static_cast<int16_t>(PD), w.left == 1, 1, 1, 0, mask,
+                         w.seg, w.row, w.kv},
                 rows * n * 16);
-        pr.copy_rows(pr.it, pr.head, 0, wd, hs, w.nrows, n * 16);
+        pr.copy_rows(pr.it, pr.head, PD, 0, wd, hs, w.nrows, n * 16);
         if (passed) load_h(pr.it);
       }
-      pr.pass(rows * P);
+      pr.pass(rows * PD);
       next(w);
     }
     if (go && !passed && pr.it > first) pass_barrier();  // everything fitted
@@ -464,8 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     for (int at = g0; at < g1; ++gu_tiles) at += min(min(16, g1 - at), p.F - at % p.F);
     const int tiles[2] = {ok ? gu_tiles : 0,
                           ok && nseg > 0 ? (rows + kTileRows - 1) / kTileRows : 0};
-    const int chunks[2] = {(dv + kChunkVecs - 1) / kChunkVecs,
-                           (fv + kChunkVecs - 1) / kChunkVecs * nseg};
+    const int chunks[2] = {(dv + gu_vecs - 1) / gu_vecs, (fv + dn_vecs - 1) / dn_vecs * nseg};
     auto put = [&](int t, int c, float v) {
       const size_t o = static_cast<size_t>(t) * p.d + c;
       Tin* yo = static_cast<Tin*>(p.y) + o;

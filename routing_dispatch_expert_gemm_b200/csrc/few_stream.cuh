@@ -5,7 +5,7 @@
 //   * One CTA per SM, all resident (cooperative launch).  Every phase cuts its output rows
 //     (weight rows) evenly over the CTAs, at single-row granularity, whatever the expert.
 //   * Warps 8.. produce: the CTA's rows are cut into tiles of up to 32 weight rows and the
-//     contraction into chunks of 1 KB per row; a slot of the ring holds one chunk of a
+//     contraction into chunks of 1 KB per row (2 or 4 KB in thin tiles, chunk_vecs); a slot of the ring holds one chunk of a
 //     tile's weight rows and of its token rows, copied with one bulk copy per row.  Slots
 //     are sized by the rows they hold, so thin tiles (a phase that leaves a CTA 7 rows)
 //     still keep the whole ring in flight; the stream does not stop between tiles or phases.
@@ -47,8 +47,9 @@ template <int NT> constexpr int kGroups = kConsumerWarps / kGroupWarps<NT>;
 constexpr int kProducerWarps = 4;
 constexpr int kThreads = kConsumers + 32 * kProducerWarps;
 constexpr int kSlots = 64;           // slot descriptors and barriers
-constexpr int kChunkBytes = 1024;    // contraction bytes per row and chunk
+constexpr int kChunkBytes = 1024;    // contraction bytes per row of the smallest chunk
 constexpr int kChunkVecs = kChunkBytes / 16;
+constexpr int kMaxChunkVecs = 4 * kChunkVecs;
 constexpr uint32_t kSmemBytes = 227 * 1024;
 constexpr int kTileRows = 32;        // weight rows per tile at most (two MMA row blocks)
 constexpr int kRedStride = 36;       // floats per token column of the partial sums: the MMA
@@ -56,7 +57,18 @@ constexpr int kRedStride = 36;       // floats per token column of the partial s
 
 // Row pitch of a slot.  bf16 fragments read 64 bytes of two rows per 8-lane phase (pitch
 // 64 mod 128), fp32 lanes read 16 bytes of 8 rows (pitch 16 mod 128).
-template <bool F32> constexpr int kPitch = F32 ? kChunkBytes + 16 : kChunkBytes + 64;
+template <bool F32>
+__host__ __device__ constexpr uint32_t pitch_of(int chunk_vecs) {
+  return chunk_vecs * 16 + (F32 ? 16 : 64);
+}
+// 16-byte vectors along the contraction of a phase's chunks, for tiles of at most `rows` rows
+// (token rows too) of `vecs` vectors.  A slot costs its warps a fixed latency whatever it holds,
+// so thin tiles take longer chunks, while the slot stays within 20 KB (of a ring of about 170).
+__device__ __forceinline__ int chunk_vecs(int rows, int vecs) {
+  int v = kChunkVecs;
+  while (v < kMaxChunkVecs && v < vecs && rows * (2 * v * 16 + 64) <= 20 * 1024) v *= 2;
+  return v;
+}
 
 // One slot of the ring, written by the producer before the slot's barrier completes.
 struct alignas(16) SlotDesc {
@@ -64,10 +76,12 @@ struct alignas(16) SlotDesc {
   int16_t r0, r1;  // weight rows of the first and second row block (the second follows the
                    // first in the slot; in a pair tile they are the gate and the up rows)
   int16_t kvec;    // valid 16-byte vectors along the contraction
+  int16_t pitch;   // bytes between rows
   int8_t last;     // last chunk of the tile
   int8_t kind;     // caller's: which phase
+  int8_t scatter;  // 1: the token of mask bit t is column t; 0: columns are 0..popc(mask)-1
+  int8_t unused;
   uint32_t mask;   // tokens whose rows the slot holds, ascending
-  int32_t scatter; // 1: the token of mask bit t is column t; 0: columns are 0..popc(mask)-1
   int32_t seg;     // caller's: what the tile belongs to
   int32_t row;     // caller's: first output row of the tile
   int32_t kv;      // caller's: first vector of the chunk along the contraction
@@ -293,23 +307,23 @@ struct Producer {
   }
   // Copy `rows` (at most 32) rows of `bytes` bytes, `stride` bytes apart, to rows row.. of the
   // slot at `off`.
-  __device__ __forceinline__ void copy_rows(uint32_t slot, uint32_t off, int row,
+  __device__ __forceinline__ void copy_rows(uint32_t slot, uint32_t off, uint32_t pitch, int row,
                                             const uint8_t* src, size_t stride, int rows,
                                             uint32_t bytes) {
     const int r = threadIdx.x & 31;
     if (r < rows)
-      bulk_load(s.ring + off + static_cast<uint32_t>(row + r) * kPitch<F32>, src + r * stride,
+      bulk_load(s.ring + off + static_cast<uint32_t>(row + r) * pitch, src + r * stride,
                 bytes, &s.full[slot % kSlots]);
     __syncwarp();
   }
   // The same for the rows of a token mask.
-  __device__ __forceinline__ void copy_tokens(uint32_t slot, uint32_t off, int row,
-                                              const uint8_t* src, size_t stride, uint32_t mask,
+  __device__ __forceinline__ void copy_tokens(uint32_t slot, uint32_t off, uint32_t pitch,
+                                              int row, const uint8_t* src, size_t stride, uint32_t mask,
                                               uint32_t bytes) {
     const int t = threadIdx.x & 31;
     if ((mask >> t) & 1u)
       bulk_load(s.ring + off +
-                    static_cast<uint32_t>(row + __popc(mask & ((1u << t) - 1u))) * kPitch<F32>,
+                    static_cast<uint32_t>(row + __popc(mask & ((1u << t) - 1u))) * pitch,
                 src + t * stride, bytes, &s.full[slot % kSlots]);
     __syncwarp();
   }
@@ -377,54 +391,63 @@ template <int NT> struct Acc<false, NT> {
   template <bool TWO, int NB>
   __device__ __forceinline__ void chunk_of(const SlotDesc& d, const Shared& s, int part,
                                            int lane) {
-    constexpr int P = kPitch<false>;
+    const int P = d.pitch;
     const uint32_t base = smem_u32(s.ring) + d.off;
     const int g = lane >> 2, q = lane & 3;
     const uint32_t at = (part * 4 + q) * 16;
     // 16-row blocks: rows past a block's last one are clamped to it
-    const uint32_t a[4] = {base + min(g, d.r0 - 1) * P + at, base + min(g + 8, d.r0 - 1) * P + at,
+    uint32_t a[4] = {base + min(g, d.r0 - 1) * P + at, base + min(g + 8, d.r0 - 1) * P + at,
                            base + (d.r0 + min(g, d.r1 - 1)) * P + at,
                            base + (d.r0 + min(g + 8, d.r1 - 1)) * P + at};
     const int nb = __popc(d.mask);
-    uint32_t b[NB];
+    uint32_t b[NB], step[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const int t = 8 * n + g;
       int row = t < nb ? t : -1;  // the token row of this lane's column, or none
       if (d.scatter) row = ((d.mask >> t) & 1u) ? __popc(d.mask & ((1u << t) - 1u)) : -1;
       b[n] = row >= 0 ? base + (d.r0 + d.r1 + row) * P + at : smem_u32(s.zeros) + at;
+      step[n] = row >= 0 ? kChunkBytes : 0;
     }
     float part_c[2][NT][4] = {};
     constexpr int kStep = kGroupWarps<NT> * 64;                // bytes between a warp's blocks
     constexpr int kBlocks = kChunkBytes / kStep;
     constexpr int HB = NB == 4 ? 2 : 4;  // blocks loaded together, so that latencies overlap
-    if (d.kvec == kChunkVecs) {
-#pragma unroll
-      for (int i = 0; i < kBlocks; i += HB) {
-        uint4 w[HB][4], x[HB][NB];
-#pragma unroll
-        for (int h = 0; h < HB; ++h) {
-          const int o = (i + h) * kStep;
-#pragma unroll
-          for (int j = 0; j < (TWO ? 4 : 2); ++j) w[h][j] = lds_vec(a[j] + o);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) x[h][n] = lds_vec(b[n] + o);
-        }
-#pragma unroll
-        for (int h = 0; h < HB; ++h) block<TWO, NB>(part_c, w[h], x[h]);
-      }
-    } else {
 #pragma unroll 1
-      for (int o = 0; (part * 4 + o / 16) < d.kvec; o += kStep) {
-        const bool in = part * 4 + q + o / 16 < d.kvec;  // the end inside a block: zeros
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        uint4 w[4], x[NB];
+    for (int left = d.kvec;; left -= kChunkVecs) {  // 1 KB of every row at a time
+      if (left >= kChunkVecs) {
 #pragma unroll
-        for (int j = 0; j < (TWO ? 4 : 2); ++j) w[j] = in ? lds_vec(a[j] + o) : z;
+        for (int i = 0; i < kBlocks; i += HB) {
+          uint4 w[HB][4], x[HB][NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) x[n] = in ? lds_vec(b[n] + o) : z;
-        block<TWO, NB>(part_c, w, x);
+          for (int h = 0; h < HB; ++h) {
+            const int o = (i + h) * kStep;
+#pragma unroll
+            for (int j = 0; j < (TWO ? 4 : 2); ++j) w[h][j] = lds_vec(a[j] + o);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) x[h][n] = lds_vec(b[n] + o);
+          }
+#pragma unroll
+          for (int h = 0; h < HB; ++h) block<TWO, NB>(part_c, w[h], x[h]);
+        }
+      } else {
+#pragma unroll 1
+        for (int o = 0; (part * 4 + o / 16) < left; o += kStep) {
+          const bool in = part * 4 + q + o / 16 < left;  // the end inside a block: zeros
+          const uint4 z = make_uint4(0, 0, 0, 0);
+          uint4 w[4], x[NB];
+#pragma unroll
+          for (int j = 0; j < (TWO ? 4 : 2); ++j) w[j] = in ? lds_vec(a[j] + o) : z;
+#pragma unroll
+          for (int n = 0; n < NB; ++n) x[n] = in ? lds_vec(b[n] + o) : z;
+          block<TWO, NB>(part_c, w, x);
+        }
       }
+      if (left <= kChunkVecs) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] += kChunkBytes;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) b[n] += step[n];
     }
     // A token column that the slot does not hold stays as it is, whatever zero times the
     // weights gave (infinities and NaNs of an expert's weights reach its own tokens only).
@@ -480,7 +503,7 @@ template <int NT> struct Acc<true, NT> {
     for (int n = 0; n < 8 * NT; ++n) c[n] = 0.f;
   }
   __device__ __forceinline__ void chunk(const SlotDesc& d, const Shared& s, int part, int lane) {
-    constexpr int P = kPitch<true>;
+    const int P = d.pitch;
     constexpr int V = 8;  // vectors of the row held together
     const int n_rows = d.r0 + d.r1;
     rows = n_rows > 16 ? 32 : n_rows > 8 ? 16 : n_rows > 4 ? 8 : 4;
