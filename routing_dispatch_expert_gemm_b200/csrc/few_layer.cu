@@ -72,6 +72,7 @@ struct Tables {
   int32_t lo, hi;                  // this CTA's (segment, hidden row) pairs of gate/up
   int32_t c0, c1;                  // and its output rows of down
   int32_t nseg;
+  int32_t most;                    // tokens of the fullest segment
 };
 // Cost of a gate/up row pair with nb tokens: two weight rows and, per 16 pairs, nb token rows
 // through the same copies and shared memory, and their MMAs.  Measured on skewed experts (T=32,
@@ -225,7 +226,7 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
   else select_tokens<8>(p, tb, ch, live);
   consumer_sync();
   if (warp == 0) {
-    int nseg = 0, rows = 0, cost = 0;
+    int nseg = 0, rows = 0, cost = 0, most = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       uint32_t m = e < p.E ? tb.mask[e] : 0;
@@ -254,6 +255,7 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
         tb.seg_hrow[i] = static_cast<int16_t>(row);
         tb.cost[i] = cost + cincl - w;
       }
+      most = max(most, __reduce_max_sync(0xffffffffu, n));
       nseg += __popc(has);
       rows += __shfl_sync(0xffffffffu, incl, 31);
       cost += __shfl_sync(0xffffffffu, cincl, 31);
@@ -266,9 +268,11 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
         tb.seg_hrow[nseg] = static_cast<int16_t>(rows);
         tb.cost[nseg] = cost;
         cost += pair_cost(live);
+        most = live;
         ++nseg;
       }
       tb.nseg = nseg;
+      tb.most = most;
       tb.cost[nseg] = cost;
       tb.lo = tb.hi = nseg * p.F;  // the end, unless a segment has it
       tb.c0 = static_cast<int>(share_begin(p.d, blockIdx.x));
@@ -351,8 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
   const int c0 = tb.c0, c1 = tb.c1;
   const int dv = p.d / VEC, fv = p.F / VEC;  // 16-byte vectors of a row
   // chunks of the two phases
-  const int gu_vecs = chunk_vecs(2 * min(16, g1 - g0) + live, dv);
-  const int dn_vecs = chunk_vecs(min(kTileRows, c1 - c0) + live, fv);
+  const int most = nseg > 0 ? tb.most : 0;
+  const int gu_vecs = chunk_vecs(2 * min(16, g1 - g0) + most, dv);
+  const int dn_vecs = chunk_vecs(min(kTileRows, c1 - c0) + most, fv);
 
   if (warp >= kConsumerWarps) {
     // ------------------------------------------------------------------ producers

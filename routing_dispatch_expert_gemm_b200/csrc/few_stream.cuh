@@ -63,10 +63,10 @@ __host__ __device__ constexpr uint32_t pitch_of(int chunk_vecs) {
 }
 // 16-byte vectors along the contraction of a phase's chunks, for tiles of at most `rows` rows
 // (token rows too) of `vecs` vectors.  A slot costs its warps a fixed latency whatever it holds,
-// so thin tiles take longer chunks, while the slot stays within 20 KB (of a ring of about 170).
+// so thin tiles take longer chunks, while the slot stays within 24 KB (of a ring of about 170).
 __device__ __forceinline__ int chunk_vecs(int rows, int vecs) {
   int v = kChunkVecs;
-  while (v < kMaxChunkVecs && v < vecs && rows * (2 * v * 16 + 64) <= 20 * 1024) v *= 2;
+  while (v < kMaxChunkVecs && v < vecs && rows * (2 * v * 16 + 64) <= 24 * 1024) v *= 2;
   return v;
 }
 
