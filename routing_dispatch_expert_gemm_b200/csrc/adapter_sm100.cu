@@ -808,9 +808,10 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
                                              : resident_clusters<false>(split)))
       split /= 2;
   }
-  // deal a tile's adapters over grid.y until the grid covers the SMs twice; in the split form,
-  // whose epilogue adds the pieces up, also cut the contraction (blocks of 32 for every warp)
-  const int deal = std::max(1, std::min(kShrinkTokens, 2 * sms / (tiles * m)));
+  // Deal a tile's adapters over grid.y until the grid covers the SMs twice, and at least over
+  // two: the tile where two requests meet would take twice as long as the others.  In the split
+  // form, whose epilogue adds the pieces up, also cut the contraction (blocks of 32 for every warp).
+  const int deal = std::max(2, std::min(kShrinkTokens, 2 * sms / (tiles * m)));
   const int parts = split == 1 ? 0
                                : std::max(1, std::min({kMaxParts, 2 * sms / (tiles * m * deal),
                                                        c.d_in / (32 * kShrinkWarps)}));
