@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 16; ++i) {
           float a0 = v[0][2 * i], a1 = v[0][2 * i + 1];
           if constexpr (PAIR) {
-            a0 = a0 / (1.f + __expf(-a0)) * v[M - 1][2 * i];
-            a1 = a1 / (1.f + __expf(-a1)) * v[M - 1][2 * i + 1];
+            a0 = gemm::silu_f(a0) * v[M - 1][2 * i];
+            a1 = gemm::silu_f(a1) * v[M - 1][2 * i + 1];
           }
           o[i] = pack_bf16(a0, a1);
         }

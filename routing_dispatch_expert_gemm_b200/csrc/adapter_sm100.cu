@@ -340,7 +340,7 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
       float o = v[0][i];
-      if constexpr (PAIR) o = o / (1.f + __expf(-o)) * v[M - 1][i];
+      if constexpr (PAIR) o = gemm::silu_f(o) * v[M - 1][i];
       if (i < cnt) y[static_cast<size_t>(i) * p.d_out] = __float2bfloat16_rn(o);
     }
   }
@@ -365,7 +365,8 @@ __device__ __forceinline__ void gather_partials(const float* part, int cnt, floa
   }
 }
 
-template <bool PAIR>
+// SPLIT (a cluster per tile) is a template argument for the code's size: see kChunk.
+template <bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     adapter_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams p) {
   constexpr int M = PAIR ? 2 : 1;
@@ -391,8 +392,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   int* s_ids = reinterpret_cast<int*>(ctl + 512);  // the ext warps': adapters of their tile's tokens
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int first_tile = blockIdx.x / p.split, tile_step = gridDim.x / p.split;
+  const int split = SPLIT ? p.split : 1;
+  const int rank = SPLIT ? static_cast<int>(cluster_rank()) : 0;
+  const int first_tile = blockIdx.x / split, tile_step = gridDim.x / split;
   const int stages = p.stages;
   const int stage_bytes = M * W_BYTES + p.boxes * kBoxBytes;
 
@@ -426,12 +428,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int tok_blocks = (live + NT - 1) / NT;
   const int total = p.row_blocks * tok_blocks;
   const int k_all = (p.d_in + BK - 1) / BK;
-  const int k_lo = k_all * rank / p.split, k_hi = k_all * (rank + 1) / p.split;
+  const int k_lo = k_all * rank / split, k_hi = k_all * (rank + 1) / split;
   // K blocks that the adapters of a token block add per projection; 0: the epilogue adds them,
   // or there are none (then it has nothing to add).  Written by the shrink kernel: after pdl_wait only.
   const int units_per = p.rank / 8 * 2;  // 8-rank units of an adapter, high and low
   auto ext_blocks = [&](int tb) {
-    if (p.split > 1) return 0;
+    if (SPLIT) return 0;
     const int n = __ldcg(p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters));
     return n > kMaxBlockAdapters ? 0 : (n * units_per + 7) / 8;
   };
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_commit(drain);
       mbar_wait_bounded(drain, 0, nullptr, kWaitLimitNs, p.status);
     }
-  } else if (warp >= kExtWarp0 && p.split == 1) {
+  } else if (!SPLIT && warp >= kExtWarp0) {
     // ------------------------------------------------------------ the adapters' K blocks
     const int et = threadIdx.x - kExtWarp0 * 32;
     // The TMA producer, which follows every use of a stage, hands a stage over (ext_go): these
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int quarter = warp & 3, half = warp >> 2;
     int acc = 0;
     uint32_t acc_phase = 0;
-    if (p.split > 1 && first_tile < total) {
+    if (SPLIT && first_tile < total) {
       // bring the rows of B that this CTA's share of the tokens needs into L2 meanwhile
       const int rb = first_tile / tok_blocks, tb = first_tile - rb * tok_blocks;
       const int ntok = min(NT, live - tb * NT), c = rb * BW + quarter * 32 + lane;
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int i = 0; i < kChunk; ++i) v[m][i] = __uint_as_float(r[i]);
         }
-        if (p.split == 1) {
+        if constexpr (!SPLIT) {
           finish_tokens<PAIR>(p, v, tb * NT + c0, min(kChunk, ntok - c0),
                               rb * BW + quarter * 32 + lane, expand, su_all + warp * (kUBytes / 4));
         } else {  // this CTA's partial tile, token-major, over the drained ring
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
   }
-  if (p.split > 1) {  // one tile per cluster
+  if constexpr (SPLIT) {  // one tile per cluster
     __syncwarp();
     cluster_sync_all();
     if (warp < kEpiWarps && first_tile < total && *abort_flag == 0) {
@@ -702,6 +704,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // of clusters doubled a 2048x2048 call.
 template <bool PAIR>
 int resident_clusters(int size) {
+  constexpr bool SPLIT = true;
   static std::atomic<int> known[64][4];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -719,19 +722,19 @@ int resident_clusters(int size) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, adapter_gemm_kernel<PAIR>, &cfg) != cudaSuccess) n = -1;
+    if (cudaOccupancyMaxActiveClusters(&n, adapter_gemm_kernel<PAIR, SPLIT>, &cfg) != cudaSuccess) n = -1;
     slot.store(n > 0 ? n : -1, std::memory_order_relaxed);
   }
   return n;
 }
 
-template <bool PAIR>
+template <bool PAIR, bool SPLIT>
 cudaError_t set_up_gemm() {
   static DeviceOnce once;
   return once.run([] {
-    cudaError_t r = cudaFuncSetAttribute(adapter_gemm_kernel<PAIR>,
+    cudaError_t r = cudaFuncSetAttribute(adapter_gemm_kernel<PAIR, SPLIT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-    return r != cudaSuccess ? r : prefer_max_shared(adapter_gemm_kernel<PAIR>);
+    return r != cudaSuccess ? r : prefer_max_shared(adapter_gemm_kernel<PAIR, SPLIT>);
   });
 }
 
@@ -745,10 +748,10 @@ cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, cudaStream_t s) {
   p.stages = std::min(kMaxStages, kRingBytes / ((PAIR ? 2 : 1) * W_BYTES + p.boxes * kBoxBytes));
   const int64_t tiles = static_cast<int64_t>(p.row_blocks) * p.tok_blocks;
   if (p.split == 1)
-    return launch_pdl(adapter_gemm_kernel<PAIR>, dim3(static_cast<unsigned>(std::min<int64_t>(
+    return launch_pdl(adapter_gemm_kernel<PAIR, false>, dim3(static_cast<unsigned>(std::min<int64_t>(
                                                      tiles, sms))),
                       dim3(kGemmThreads), kGemmSmem, s, maps, p);
-  return launch_pdl_cluster(adapter_gemm_kernel<PAIR>,
+  return launch_pdl_cluster(adapter_gemm_kernel<PAIR, true>,
                             dim3(static_cast<unsigned>(tiles * p.split)), dim3(kGemmThreads),
                             kGemmSmem, static_cast<unsigned>(p.split), s, maps, p);
 }
@@ -798,7 +801,8 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   const bool pairs = adapter_pair_fits(c, a.pair);
   const int sms = sm_count();
   const int tiles = (c.T + kShrinkTokens - 1) / kShrinkTokens, m = a.pair ? 2 : 1;
-  cudaError_t e = a.pair ? set_up_gemm<true>() : set_up_gemm<false>();
+  cudaError_t e = a.pair ? set_up_gemm<true, true>() : set_up_gemm<false, true>();
+  if (e == cudaSuccess) e = a.pair ? set_up_gemm<true, false>() : set_up_gemm<false, false>();
   if (e != cudaSuccess) return e;
   int split = gemm_split(c, a.pair, sms);
   {
