@@ -157,18 +157,23 @@ def _ptr(t):
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a torch Stream object takes 3 us, as long as a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on_device(t):
     """Make a tensor's device the current one for the call (its stream is the default)."""
-    if hasattr(t, "is_cuda") and t.is_cuda:
+    if getattr(t, "is_cuda", False):
         import torch
-        return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+        if t.get_device() != torch.cuda.current_device():
+            return torch.cuda.device(t.get_device())
+    return _HERE
 
 
 def _check(code: int, where: str):
