@@ -133,6 +133,7 @@ CASES = [
     (200, 4096, 512, 64, 16, "bf16", "tokens", None),
     (257, 128, 4096, 7, 16, "bf16", "requests", 256),
     (300, 648, 392, 3, 24, "bf16", "none", None),
+    (400, 264, 9000, 100, 16, "bf16", "tokens", 390),
     (777, 512, 2048, 6, 32, "bf16", "requests", 700),
     (1031, 264, 5000, 9, 16, "bf16", "tokens", None),
     (1024, 136, 4872, 3, 8, "bf16", "requests", None),
@@ -288,3 +289,37 @@ def test_broken_adapter_reaches_its_own_tokens_only(N, T, d_out):
                 rest = [c for c in range(d_out) if c not in (7, d_out - 1)]
                 assert bool(err[own][:, rest].all())
             del clean
+
+
+@pytest.mark.parametrize("T,d_out", [(20, 64), (200, 512), (777, 2048), (5000, 2048)])
+def test_few_live_tokens_and_unaligned_outputs(N, T, d_out):
+    """A batch padded to many times its tokens; y and the addend at addresses that are not
+    16-byte aligned."""
+    p = make(T, 64, d_out, 4, 8, mix="requests", seed=2)
+    for live in (0, 1, T // 3):
+        for pair in (False, True):
+            check(call(N, p, pair, n_tokens=live), reference(p, pair), live)
+    flat = torch.full((T * d_out + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    add = torch.empty_like(flat)
+    add[3:3 + T * d_out] = p["addend"].flatten()
+    y = flat[1:1 + T * d_out].view(T, d_out)
+    q = dict(p, addend=add[3:3 + T * d_out].view(T, d_out))
+    check(call(N, q, False, True, n_tokens=T - 1, y=y), reference(p, False, True), T - 1)
+    assert bool((flat[1 + T * d_out:] == 7.0).all()) and float(flat[0]) == 7.0
+    check(call(N, p, True, y=y), reference(p, True), T)
+
+
+def test_adapters_of_another_stream_and_order(N):
+    """The tensors of one stream used on another, after an event: the call runs on the stream it
+    is given."""
+    p = make(50, 512, 256, 3, 16)
+    want = call(N, p, False)
+    cfg = N.make_adapter_config(50, 512, 256, 3, 16)
+    ws = N.adapter_workspace(cfg)
+    y = torch.zeros_like(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    N.moe_adapter_linear(cfg, p["x"], p["w"][0], p["a"][0], p["b"][0], p["scale"], p["ids"], None,
+                         y, None, ws, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)

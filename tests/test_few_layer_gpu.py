@@ -300,3 +300,16 @@ def test_broken_expert_reaches_its_own_tokens_only(N, T, dtype):
     assert torch.equal(before["ids"][rest], after["ids"][rest])
     assert bool(((after["y"].double() - ref["y"]).abs() <= ref["by"])[rest].all())
     assert bool(torch.isnan(after["y"][1]).all())
+
+
+def test_unaligned_output_and_wide_shapes(N):
+    """y at an address that is not 16-byte aligned; a hidden width of many chunks beside a narrow
+    model width, and the other way round."""
+    for d, F, E, T in ((128, 8192, 6, 5), (6144, 128, 3, 9), (256, 2048, 250, 31)):
+        p = make(T, d, E, 3, F, shared=True, seed=d)
+        cfg = N.make_config(T, d, E, 3, F, has_shared=True, add_residual=True)
+        flat = torch.full((T * d + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = flat[3:3 + T * d].view(T, d)
+        out = call(N, cfg, p, n_tokens=T - 1, y=y)
+        check(out, reference(p, out, 3, "topk_softmax", -1, True, T - 1), T - 1)
+        assert bool((flat[:3] == 7.0).all()) and bool((flat[3 + T * d:] == 7.0).all())
