@@ -91,7 +91,7 @@ __device__ __forceinline__ void expand_row(const PairParams& p, int m, int t, in
       Vec<__nv_bfloat16>::to_f32(ld_vec(b + static_cast<size_t>(c) * p.rank), f);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[c] = fmaf(only_nonfinite && isfinite(f[i]) ? 0.f : f[i], h[i], v[c]);
+        if (!only_nonfinite || !isfinite(f[i])) v[c] = fmaf(f[i], h[i], v[c]);
     }
   }
 }
@@ -119,7 +119,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = ext_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // per tile of this pair, modulo kFlags: its K blocks met a non-finite element of B, [SM]
+  // per tile of this pair that has K blocks of adapters, modulo kFlags: they met a non-finite
+  // element of B, [SM].  Only such tiles count: the ext warps may pass any number of others, but
+  // fill a block only after the last one's MMAs, which wait for the epilogue two tiles before.
   volatile int* nonfinite = abort_flag + 1;
   int* s_ids = reinterpret_cast<int*>(ctl + 512);     // the ext warps': adapters of their tokens
 
@@ -261,10 +263,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t uses = 0;  // blocks filled so far
     bool ok = true;
     pdl_wait();
-    for (int tile = pair, iter = 0; tile < total && ok; tile += npairs, ++iter) {
+    for (int tile = pair, iter = -1; tile < total && ok; tile += npairs) {
       const int cb = tile / tok_blocks, tb = tile - cb * tok_blocks;
       const int n = ext_blocks(tb);
       if (n == 0) continue;
+      ++iter;
       const int32_t* list = p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters);
       const int units = __ldcg(list) * units_per;
       const int t0 = tb * 2 * BM + static_cast<int>(rank) * BM;
@@ -321,9 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     pdl_wait();  // what read y before this call is done
-    for (int tile = pair, iter = 0; tile < total; tile += npairs, ++iter) {
+    for (int tile = pair, iter = -1; tile < total; tile += npairs) {
       const int cb = tile / tok_blocks, tb = tile - cb * tok_blocks;
       const bool blocks = ext_blocks(tb) != 0;
+      iter += blocks;
       int ok = 1;
       if (lane == 0)
         ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs, p.status);

@@ -198,8 +198,10 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
               make_float2(v[0], v[1]);
         } else {
           const uint32_t hi = gemm::pack_bf16(v[0], v[1]);
-          const uint32_t lo = gemm::pack_bf16(v[0] - __uint_as_float(hi << 16),
-                                              v[1] - __uint_as_float(hi & 0xffff0000u));
+          // an infinity has no low half (inf - inf is NaN)
+          const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
+          const uint32_t lo = gemm::pack_bf16(isfinite(h0) ? v[0] - h0 : 0.f,
+                                              isfinite(h1) ? v[1] - h1 : 0.f);
           uint32_t* u = reinterpret_cast<uint32_t*>(
               p.u + ((static_cast<size_t>(m) * p.T + t0 + t) * p.rank + j0) / 4) + (j / 8) * 8 +
               (j % 8) / 2;

@@ -323,3 +323,39 @@ def test_adapters_of_another_stream_and_order(N):
                          y, None, ws, stream=side)
     side.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,d_out", [(6, 64), (90, 64), (700, 5000), (700, 64), (1000, 5000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_shrink(N, T, d_out, dtype):
+    """A x of one adapter is +inf in one rank and its B is positive there: the formula gives
+    +inf in every output of its tokens, and the others know nothing of it."""
+    p = make(T, 128, d_out, 4, 16, dtype, "requests", seed=3)
+    p["ids"][T // 2] = 2
+    p["a"][0][2, 5, 9] = float("inf")
+    p["x"][:, 9] = 1.0
+    p["b"][0][2, :, 5] = 0.5
+    own = p["ids"] == 2
+    y = call(N, p, False)
+    assert bool((y[own] == float("inf")).all())
+    q = dict(p, a=[p["a"][0].clone()])
+    q["a"][0][2, 5, 9] = 0.0
+    want, bound = reference(q, False)
+    assert bool(((y.double() - want).abs() <= bound)[~own].all())
+
+
+def test_broken_rows_of_rare_adapters(N):
+    """Adapters in the first token block alone: the tiles between two of its tiles have none.
+    Infinities in B in the rows of its first tiles, which the later ones do not meet."""
+    T, d_out = 8192, 10240
+    p = make(T, 64, d_out, 3, 8, mix="none", seed=4)
+    p["ids"][:100] = 1
+    p["b"][0][1, :256, 2] = float("inf")
+    y = call(N, p, False)
+    v = (p["x"][:100].double() @ p["a"][0][1].double().t())[:, 2]
+    sign = torch.where(v > 0, float("inf"), float("-inf"))  # v is no zero: 64 random products
+    assert bool((y[:100, :256].double() == sign[:, None]).all())
+    q = dict(p, w=[p["w"][0][256:]], b=[p["b"][0][:, 256:].contiguous()])
+    want, bound = reference(q, False)
+    assert bool(((y[:, 256:].double() - want).abs() <= bound).all())
+    assert bool(torch.isfinite(y[100:]).all())
