@@ -265,9 +265,10 @@ moe_status moe_forward(const moe_config* cfg, const void* x, const void* w_route
  *               left; a route chosen at a logit of -inf (or NaN, which ranks as -inf) has
  *               gate 0, and a token with no other logit has only zero gates, so its routed
  *               part is zero.
- *   y           may be x itself.
+ *   y           may be x itself; must not overlap it otherwise (MOE_ERR_INVALID).
  * cfg->tiles is ignored.  MOE_ERR_UNSUPPORTED: T > 32, d or d_ff above 2^24, (E + 1) * d_ff of
- * 2^31 or more, stats, the padded layout, the reroute policy, fused steps.  MOE_ERR_INVALID also for x or weights that are not 16-byte aligned.
+ * 2^31 or more, stats, the padded layout, the reroute policy, fused steps.  MOE_ERR_INVALID
+ * also for x or weights that are not 16-byte aligned.
  * The kernel occupies every SM (a cooperative launch) and can be captured into a graph.  If
  * it ever reports MOE_ERR_TIMEOUT, clear the status (moe_get_device_status) or call
  * moe_workspace_init before the workspace's next use.  Up to 8 tokens it is faster than
@@ -281,8 +282,8 @@ moe_status moe_forward_few(const moe_config* cfg, const void* x, const void* w_r
                            int32_t* demand_out, int32_t* offsets_out, const int32_t* n_tokens,
                            void* ws, moe_stream_t stream);
 
-/* A projection that all tokens share (a shared expert's, or the router of a dense block) with
- * each token's own low-rank adapter beside it, for the tokens of many requests at once.     */
+/* A projection that all tokens share (a shared expert's) with each token's own low-rank
+ * adapter beside it, for the tokens of many requests at once.                              */
 typedef struct {
   int32_t T;           /* tokens in this call (>= 1)                                     */
   int32_t d_in, d_out; /* the projection W is [d_out, d_in]                               */
@@ -304,7 +305,8 @@ size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg);
  *   adapter_ids [T] int32; -1: the projection alone.  Any other id outside [0, n_adapters)
  *               counts as -1 and records MOE_ERR_BAD_ADAPTER_ID in the status word.
  *   addend      [T, d_out] or NULL; may be y itself (the layer's output, added to in place)
- *   y           [T, d_out] (out); must not overlap x
+ *   y           [T, d_out] (out); must not overlap x, nor the addend but as a whole
+ *               (MOE_ERR_INVALID)
  *   n_tokens    device int32 or NULL: rows 0 .. *n_tokens - 1 hold tokens (clamped to 0..T;
  *               NULL: all T); y's rows behind them are left as they were.
  * A_a x is summed and kept in fp32 or better than 16 bits of it, sums are fp32, y is rounded
@@ -340,7 +342,7 @@ moe_status moe_forward_profiled(const moe_config* cfg, const void* x, const void
                                 void* ws, moe_stream_t stream);
 
 /* Synchronise `stream`, copy the device status word of `ws` to *status_out (a moe_status)
- * and, if clear != 0, reset it to MOE_OK (after MOE_ERR_TIMEOUT the whole header, as
+ * and, if clear != 0, reset it to MOE_OK (after any error the whole header, as
  * moe_workspace_init does).  Returns MOE_ERR_CUDA if the copy fails.                    */
 moe_status moe_get_device_status(void* ws, moe_stream_t stream, int32_t clear,
                                  int32_t* status_out);

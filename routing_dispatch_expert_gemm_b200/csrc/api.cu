@@ -134,6 +134,12 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+// Whether a of `an` bytes and b of `bn` share any.
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
+}
+
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 #define MOE_TRY(expr)                 \
@@ -191,6 +197,12 @@ moe_status adapter_impl(const moe_adapter_config* cfg, const AdapterArgs& a, voi
   if (!a.x || !a.w[0] || !a.a[0] || !a.b[0] || !a.ids || !a.y) return MOE_ERR_INVALID;
   if (a.pair && (!a.w[1] || !a.a[1] || !a.b[1])) return MOE_ERR_INVALID;
   if (!aligned16({a.x, a.w[0], a.w[1], a.a[0], a.a[1], a.b[0], a.b[1]})) return MOE_ERR_INVALID;
+  // x is read for other rows and columns after y's first are written; the addend is read where y
+  // is written
+  const int64_t esz = cfg->dtype == MOE_BF16 ? 2 : 4, yb = int64_t{1} * cfg->T * cfg->d_out * esz;
+  if (overlap(a.x, int64_t{1} * cfg->T * cfg->d_in * esz, a.y, yb)) return MOE_ERR_INVALID;
+  if (a.addend != nullptr && a.addend != a.y && overlap(a.addend, yb, a.y, yb))
+    return MOE_ERR_INVALID;
   const AdapterLayout L = adapter_layout(*cfg);
   if (adapter_streams(*cfg, a.pair))
     return cuda_status(launch_adapter_few(*cfg, a, L, ws, stream));
@@ -409,6 +421,8 @@ moe_status moe_forward_few(const moe_config* cfg, const void* x, const void* w_r
   if (cfg->has_shared && (!shared_gate || !shared_up || !shared_down)) return MOE_ERR_INVALID;
   if (!aligned16({x, w_router, w_gate, w_up, w_down, shared_gate, shared_up, shared_down}))
     return MOE_ERR_INVALID;
+  const int64_t bytes = int64_t{1} * cfg->T * cfg->d * (cfg->dtype == MOE_BF16 ? 2 : 4);
+  if (y != x && overlap(x, bytes, y, bytes)) return MOE_ERR_INVALID;
   const FewArgs a{x, w_router, logit_bias, w_gate, w_up, w_down, shared_gate, shared_up,
                   shared_down, y, ids_out, gates_out, demand_out, offsets_out, n_tokens};
   return cuda_status(launch_few_layer(*cfg, a, ws, stream));
@@ -477,8 +491,9 @@ moe_status moe_get_device_status(void* ws, moe_stream_t stream, int32_t clear,
   if (cudaStreamSynchronize(stream) != cudaSuccess) return MOE_ERR_CUDA;
   int32_t v = 0;
   if (cudaMemcpy(&v, ws, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  // after a timeout the header's tickets and barrier counts may stand anywhere: all start again
-  const size_t bytes = v == MOE_ERR_TIMEOUT ? kWsHeaderBytes : sizeof(int32_t);
+  // After a timeout the header's tickets and barrier counts may stand anywhere: all start again.
+  // Whatever the word says: it keeps the first error, and a timeout may have followed another.
+  const size_t bytes = v != MOE_OK ? kWsHeaderBytes : sizeof(int32_t);
   if (clear && cudaMemset(ws, 0, bytes) != cudaSuccess) return MOE_ERR_CUDA;
   *status_out = v;
   return MOE_OK;

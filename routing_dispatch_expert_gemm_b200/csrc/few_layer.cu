@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     ok = *s.abort_flag == 0;  // written before the barrier: the same for all
     if (ok) build_tables(p, tb, *reinterpret_cast<Choice*>(s.ring), live);
     else if (tid == 0) tb.nseg = tb.c0 = tb.c1 = 0;
+    fence_proxy_async_smem();  // Choice lies where bulk copies now write
   }
   __syncthreads();
   const int nseg = tb.nseg;

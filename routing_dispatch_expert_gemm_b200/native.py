@@ -154,6 +154,12 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _ptr_i32(t):
+    if t is not None and not isinstance(t, int) and t.element_size() != 4:
+        raise ValueError("ids and token counts passed to libmoe must be int32")
+    return _ptr(t)
+
+
 def _stream(s):
     if s is None:
         import torch
@@ -268,7 +274,7 @@ def moe_forward_few(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, shared_g
                                      _ptr(logit_bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                                      _ptr(shared_gate), _ptr(shared_up), _ptr(shared_down),
                                      _ptr(y), _ptr(ids_out), _ptr(gates_out), _ptr(demand_out),
-                                     _ptr(offsets_out), _ptr(n_tokens), _ptr(ws),
+                                     _ptr(offsets_out), _ptr_i32(n_tokens), _ptr(ws),
                                      _stream(stream)), "moe_forward_few")
 
 
@@ -281,8 +287,8 @@ def moe_adapter_linear(cfg, x, w, a, b, scale, adapter_ids, addend, y, n_tokens,
     see moe_adapter_linear in include/moe.h.  ``scale``, ``addend``, ``n_tokens`` may be None."""
     with _on_device(x):
         _check(lib().moe_adapter_linear(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(a), _ptr(b),
-                                        _ptr(scale), _ptr(adapter_ids), _ptr(addend), _ptr(y),
-                                        _ptr(n_tokens), _ptr(ws), _stream(stream)),
+                                        _ptr(scale), _ptr_i32(adapter_ids), _ptr(addend), _ptr(y),
+                                        _ptr_i32(n_tokens), _ptr(ws), _stream(stream)),
                "moe_adapter_linear")
 
 
@@ -292,8 +298,8 @@ def moe_adapter_gate_up(cfg, x, w_gate, w_up, a_gate, b_gate, a_up, b_up, scale,
     with _on_device(x):
         _check(lib().moe_adapter_gate_up(ctypes.byref(cfg), _ptr(x), _ptr(w_gate), _ptr(w_up),
                                          _ptr(a_gate), _ptr(b_gate), _ptr(a_up), _ptr(b_up),
-                                         _ptr(scale), _ptr(adapter_ids), _ptr(h),
-                                         _ptr(n_tokens), _ptr(ws), _stream(stream)),
+                                         _ptr(scale), _ptr_i32(adapter_ids), _ptr(h),
+                                         _ptr_i32(n_tokens), _ptr(ws), _stream(stream)),
                "moe_adapter_gate_up")
 
 
@@ -316,8 +322,9 @@ def moe_forward_profiled(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, sha
 
 def moe_get_device_status(ws, stream=None, clear=False) -> int:
     out = _I32(0)
-    _check(lib().moe_get_device_status(_ptr(ws), _stream(stream), int(bool(clear)),
-                                       ctypes.byref(out)), "moe_get_device_status")
+    with _on_device(ws):
+        _check(lib().moe_get_device_status(_ptr(ws), _stream(stream), int(bool(clear)),
+                                           ctypes.byref(out)), "moe_get_device_status")
     return out.value
 
 
@@ -350,7 +357,8 @@ def workspace(cfg: MoeConfig, device="cuda"):
     if n == 0:
         raise MoeError(1, "moe_workspace_bytes")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    moe_workspace_init(ws)
+    with _on_device(ws):
+        moe_workspace_init(ws)
     return ws
 
 

@@ -14,11 +14,12 @@ def native():
 
 
 FAKE = 1 << 20  # 16-byte aligned, never dereferenced
+OUT = 1 << 50   # behind the largest input
 WS = 1 << 12
-LINEAR = dict(x=FAKE, w=FAKE, a=FAKE, b=FAKE, scale=None, ids=FAKE, addend=None, y=FAKE,
+LINEAR = dict(x=FAKE, w=FAKE, a=FAKE, b=FAKE, scale=None, ids=FAKE, addend=None, y=OUT,
               n_tokens=None, ws=WS)
 PAIR = dict(x=FAKE, w_gate=FAKE, w_up=FAKE, a_gate=FAKE, b_gate=FAKE, a_up=FAKE, b_up=FAKE,
-            scale=None, ids=FAKE, h=FAKE, n_tokens=None, ws=WS)
+            scale=None, ids=FAKE, h=OUT, n_tokens=None, ws=WS)
 
 
 def linear(native, cfg, **kw):
@@ -75,3 +76,33 @@ def test_workspace_holds_the_shrunk_tokens(native):
         cfg = native.make_adapter_config(T, 64, 32, 2, rank)
         assert native.moe_adapter_workspace_bytes(cfg) >= 256 + 2 * T * rank * 4
         assert native.moe_adapter_workspace_bytes(cfg) % 256 == 0
+
+
+def test_overlapping_outputs(native):
+    """y reaches into x, from either side; y and the addend overlap without being the same."""
+    for dtype, esz in (("bf16", 2), ("f32", 4)):
+        cfg = native.make_adapter_config(**SHAPE, dtype=dtype)
+        x_bytes, y_bytes = 8 * 64 * esz, 8 * 32 * esz
+        for y in (FAKE, FAKE + x_bytes - esz, FAKE - y_bytes + esz):
+            assert linear(native, cfg, y=y) == 1 and gate_up(native, cfg, h=y) == 1
+        for ad in (OUT + esz, OUT + y_bytes - esz, OUT - y_bytes + esz):
+            assert linear(native, cfg, addend=ad) == 1
+
+
+def test_types_of_ids_and_counts(native):
+    """64-bit ids, torch's default, would be read as pairs of 32-bit ones."""
+    torch = pytest.importorskip("torch")
+    cfg = native.make_adapter_config(**SHAPE)
+    ids, count = torch.zeros(8, dtype=torch.int64), torch.ones(1, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        native.moe_adapter_linear(cfg, FAKE, FAKE, FAKE, FAKE, None, ids, None, OUT, None, WS, 0)
+    with pytest.raises(ValueError):
+        native.moe_adapter_linear(cfg, FAKE, FAKE, FAKE, FAKE, None, FAKE, None, OUT, count, WS,
+                                  0)
+    with pytest.raises(ValueError):
+        native.moe_adapter_gate_up(cfg, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, ids, OUT,
+                                   None, WS, 0)
+    layer = native.make_config(8, 128, 4, 2, 128)
+    with pytest.raises(ValueError):
+        native.moe_forward_few(layer, FAKE, FAKE, None, FAKE, FAKE, FAKE, None, None, None, FAKE,
+                               None, None, None, None, count, WS, 0)

@@ -41,6 +41,8 @@ def test_invalid(native):
         assert few(native, cfg, **{name: None}) == 1
     for name in ("x", "w_router", "w_gate", "w_up", "w_down"):
         assert few(native, cfg, **{name: FAKE + 8}) == 1     # rows are copied in 16 bytes
+    for y in (FAKE + 2, FAKE + 8 * 128 * 2 - 2, FAKE - 8 * 128 * 2 + 2):  # inside x, not x
+        assert few(native, cfg, y=y) == 1
     assert few(native, cfg, ws=None) == 3 and few(native, cfg, ws=WS + 16) == 3
     shared = native.make_config(8, 128, 4, 2, 128, has_shared=True)
     full = dict(s_gate=FAKE, s_up=FAKE, s_down=FAKE)
