@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
     for (int at = a0; at < a1; ++a_tiles) at += shrink_rows(at);
     const int tiles[2] = {a_tiles, (c1 - c0 + TILE - 1) / TILE};
     bool waited = nseg == 0;
-    auto epilogue = [&](const SlotDesc& d, const float* red) {
+    auto epilogue = [&](const SlotDesc& d, const float* red, const Crew&) {
       if (d.kind == 0) {
         const int m = PAIR && d.seg >= nseg ? 1 : 0, seg = d.seg - m * nseg;
         const int nr = d.r0 + d.r1, nb = __popc(d.mask);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
           const int r = i & 31, n = i >> 5;
           if (r < nr)
             p.u[(static_cast<size_t>(m) * p.T + tb.tok[tb.seg_tok[seg] + n]) * p.rank + d.row +
-                r] = sc * red_sum<NT>(red, 0, r, n);
+                r] = sc * red_sum<NT>(red, kConsumerWarps, 0, r, n);
         }
         return;
       }
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
         float v[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-          v[m] = red_sum<NT>(red, m, r, t);
+          v[m] = red_sum<NT>(red, kConsumerWarps, m, r, t);
           if (id >= 0)
             v[m] += expand(static_cast<const Tin*>(p.b[m]) +
                                (static_cast<size_t>(id) * p.d_out + c) * p.rank,
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
       if (tid == 0) grid_arrive(p.sync);
       return well;
     };
-    consume<F32, NT>(s, tiles, chunks, p.status, epilogue, between);
+    consume<F32, NT>(s, tiles, chunks, false, p.status, epilogue, between);
   }
   __syncthreads();
   if (tid == 0 && *s.abort_flag == 0) grid_leave(p.sync);

@@ -486,14 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
         *yo = __float2bfloat16_rn(p.residual ? v + __bfloat162float(X[o]) : v);
       }
     };
-    auto epilogue = [&](const SlotDesc& d, const float* red) {
+    auto epilogue = [&](const SlotDesc& d, const float* red, const Crew& crew) {
       if (d.kind == 0) {
         const int nb = __popc(d.mask), hrow = tb.seg_hrow[d.seg];
 #pragma unroll 1
-        for (int i = tid; i < 16 * nb; i += kConsumers) {
+        for (int i = crew.index; i < 16 * nb; i += crew.count) {
           const int r = i & 15, n = i >> 4;
           if (r >= d.r0) continue;
-          const float g = red_sum<NT>(red, 0, r, n), u = red_sum<NT>(red, 1, r, n);
+          const float g = red_sum<NT>(red, crew.warps, 0, r, n);
+          const float u = red_sum<NT>(red, crew.warps, 1, r, n);
           const float v = g / (1.f + expf(-g)) * u * tb.gate_of_row[hrow + n];
           Tin* o = H + static_cast<size_t>(hrow + n) * p.F + d.row + r;
           if constexpr (F32) *o = v;
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
 #pragma unroll 1
         for (int i = tid; i < kTileRows * live; i += kConsumers) {
           const int r = i & 31, t = i >> 5;
-          if (r < nr) put(t, d.row + r, red_sum<NT>(red, 0, r, t));
+          if (r < nr) put(t, d.row + r, red_sum<NT>(red, kConsumerWarps, 0, r, t));
         }
       }
     };
@@ -514,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
       if (tid == 0) grid_arrive(p.sync);
       return well;
     };
-    consume<F32, NT>(s, tiles, chunks, p.status, epilogue, between);
+    consume<F32, NT>(s, tiles, chunks, solo_tiles<NT>(tiles[0], chunks[0]), p.status, epilogue,
+                     between);
     if (nseg == 0 && ok) {  // capacity 0 and no shared expert: only the residual is left
 #pragma unroll 1
       for (int i = tid; i < rows * live; i += kConsumers) put(i / rows, c0 + i % rows, 0.f);

@@ -182,6 +182,21 @@ __device__ __forceinline__ bool consumer_all(bool v) {
   return r != 0;
 }
 
+// The barrier of one group's warps; returns whether `v` held on all of its threads.
+template <int NT>
+__device__ __forceinline__ bool group_all(uint32_t group, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(2 + group), "n"(32 * kGroupWarps<NT>)
+      : "memory");
+  return r != 0;
+}
+
 // Where CTA i's share of n rows begins.
 static __device__ __noinline__ int64_t share_begin(int64_t n, uint32_t i) { return n * i / gridDim.x; }
 
@@ -563,19 +578,42 @@ template <int NT> struct Acc<true, NT> {
   }
 };
 
-// The total of output (row block m, row i of it, column n): the 8 warps in order.
+// The total of output (row block m, row i of it, column n): the partial sums of `warps` warps (of
+// a group, or all) in order.
 template <int NT>
-__device__ __forceinline__ float red_sum(const float* red, int m, int i, int n) {
+__device__ __forceinline__ float red_sum(const float* red, int warps, int m, int i, int n) {
   float v = 0.f;
   const float* p = red + n * kRedStride + 16 * m + i;
 #pragma unroll
-  for (int w = 0; w < kConsumerWarps; ++w) v += p[w * (8 * NT * kRedStride)];
+  for (int w = 0; w < kConsumerWarps; ++w)
+    if (w < warps) v += p[w * (8 * NT * kRedStride)];
   return v;
 }
 
+// Who runs a tile's epilogue: `count` threads, this one the `index`-th of them, on the partial
+// sums of `warps` warps.
+struct Crew {
+  int index, count, warps;
+};
+
+// A phase whose tiles have few slots gives a tile to one group, which sums up and finishes it by
+// itself while the others are at other tiles: shared by all groups, a tile of two slots costs the
+// latency of both barriers and of the epilogue each time (Granite-shaped T=16: XX us instead of
+// YY).  With more slots to a tile the ring would hold slots of one group's tile only.
+//   No group waits for use n + 1 of a slot's barrier before use n has completed: when it
+// waits for slots of its next tile, at most kGroups tiles on, the slots up to kInFlight before
+// the tile it finished have been filled.
+constexpr int kSoloChunks = 4;
+static_assert(kGroups<1> * kSoloChunks + kInFlight <= kSlots, "no parity of a slot is ambiguous");
+template <int NT>
+__device__ __forceinline__ bool solo_tiles(int tiles, int chunks) {
+  return chunks <= kSoloChunks && tiles >= kGroups<NT>;
+}
+
 // Consume the tiles of two phases: tiles[0] of chunks[0] slots each, then `between`, then
-// tiles[1] of chunks[1].  epilogue(desc, red) runs on all consumer threads once per tile, with
-// the descriptor of its last slot and the 8 warps' partial sums: after the next tile's slots are
+// tiles[1] of chunks[1].  epilogue(desc, red, crew) runs once per tile, with the descriptor of
+// its last slot and the partial sums.  `solo`: the first phase's tiles go to one group each (see
+// solo_tiles).  Else all consumer threads run it: after the next tile's slots are
 // consumed, or, for the last tile of a phase, at once.  A buffer of partial sums is written again
 // only after its tile's epilogue: with two buffers because each warp arrives for a tile after its
 // own epilogue of the tile before, and waits for all arrivals of that one first; with one buffer
@@ -585,15 +623,17 @@ __device__ __forceinline__ float red_sum(const float* red, int m, int i, int n) 
 // One loop for both phases on purpose: its code is there once.
 template <bool F32, int NT, typename Epi, typename Between>
 __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
-                                        const int (&chunks)[2], int32_t* status, Epi&& epilogue,
-                                        Between&& between) {
+                                        const int (&chunks)[2], bool solo, int32_t* status,
+                                        Epi&& epilogue, Between&& between) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t group = warp / kGroupWarps<NT>;
   const int part = warp % kGroupWarps<NT>;
   const int total = tiles[0] + tiles[1];
+  constexpr int kWarpFloats = 8 * NT * kRedStride;
   uint32_t it = 0;       // slots passed
-  int tile = 0;
-  bool pending = false;  // tile - 1 awaits its epilogue
+  int tile = solo ? group : 0;
+  uint32_t n = 0;        // tiles of all groups stored
+  bool pending = false;  // tile n - 1 of them awaits its epilogue
   bool crossed = false, ok = true;
   Acc<F32, NT> acc;
 #pragma unroll 1
@@ -602,15 +642,21 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
     bool last = false;
     SlotDesc d;
     if (!flush) {
-      if (tile == tiles[0] && !crossed) {
+      if (tile >= tiles[0] && !crossed) {
         crossed = true;
         if (!between(ok)) return;
+        if (solo) {
+          solo = false;
+          tile = tiles[0];
+          it = tiles[0] * chunks[0];
+        }
       }
       if (tile == total) return;
       acc.zero();
-      const uint32_t end = it + chunks[crossed ? 1 : 0];
+      if (solo) it = tile * chunks[0];
+      const uint32_t end = it + chunks[crossed ? 1 : 0], step = solo ? 1 : kGroups<NT>;
 #pragma unroll 1
-      for (it += (group - it) % kGroups<NT>; it < end; it += kGroups<NT>) {
+      for (it += solo ? 0 : (group - it) % kGroups<NT>; it < end; it += step) {
         const uint32_t slot = it % kSlots;
         ok = __all_sync(0xffffffffu,
                         wait(&s.full[slot], (it / kSlots) & 1u, s.abort_flag, status));
@@ -622,11 +668,27 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
         last = d.last != 0;
       }
       it = end;
+      if (solo) {
+        ok = group_all<NT>(group, ok);  // and the tile before is finished
+        acc.store(s.red, warp, lane);
+        ok = group_all<NT>(group, ok);
+        if (!ok) {
+          between(false);
+          return;
+        }
+        constexpr int kCrew = 32 * kGroupWarps<NT>;
+        epilogue(d, s.red + group * kGroupWarps<NT> * kWarpFloats,
+                 Crew{static_cast<int>(threadIdx.x) % kCrew, kCrew, kGroupWarps<NT>});
+        tile += kGroups<NT>;
+        continue;
+      }
     }
     if (pending && ok) {
-      const uint32_t t = tile - 1;
+      const uint32_t t = n - 1;
       ok = __all_sync(0xffffffffu, wait(&s.sums[t & 1u], (t >> 1) & 1u, s.abort_flag, status));
-      if (ok) epilogue(s.tile[t & 1u], s.red + (t % kRedBufs<NT>) * kRedFloats<NT>);
+      if (ok)
+        epilogue(s.tile[t & 1u], s.red + (t % kRedBufs<NT>) * kRedFloats<NT>,
+                 Crew{static_cast<int>(threadIdx.x), kConsumers, kConsumerWarps});
       if (kRedBufs<NT> == 1) {
         __syncwarp();
         if (lane == 0) mbar_arrive(s.freed);
@@ -638,15 +700,16 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
       return;
     }
     if (!flush) {
-      if (kRedBufs<NT> == 1 && tile > 0 &&
-          !__all_sync(0xffffffffu, wait(s.freed, (tile - 1) & 1u, s.abort_flag, status))) {
+      if (kRedBufs<NT> == 1 && n > 0 &&
+          !__all_sync(0xffffffffu, wait(s.freed, (n - 1) & 1u, s.abort_flag, status))) {
         if (!crossed) between(false);
         return;
       }
-      acc.store(s.red + (tile % kRedBufs<NT>) * kRedFloats<NT>, warp, lane);
-      if (last && part == 0 && lane == 0) s.tile[tile & 1] = d;
+      acc.store(s.red + (n % kRedBufs<NT>) * kRedFloats<NT>, warp, lane);
+      if (last && part == 0 && lane == 0) s.tile[n & 1] = d;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.sums[tile & 1]);
+      if (lane == 0) mbar_arrive(&s.sums[n & 1]);
+      ++n;
       ++tile;
       pending = true;
     }
