@@ -103,7 +103,7 @@ __device__ __forceinline__ float expand(const Tin* b, const float* u, int rank) 
 }
 
 template <typename Tin, int NT, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterFewParams p) {
+__global__ void __launch_bounds__(kThreads<sizeof(Tin) == 4, NT>, 1) adapter_few_kernel(const AdapterFewParams p) {
   constexpr bool F32 = sizeof(Tin) == 4;
   constexpr int VEC = Vec<Tin>::N;
   constexpr int M = PAIR ? 2 : 1;           // projections
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
   AdapterTables& tb = *reinterpret_cast<AdapterTables*>(smem + kCtlBytes + kRedBufs<NT> * kRedFloats<NT> * 4);
   const int tid = threadIdx.x, warp = tid >> 5;
 
-  init_shared<NT>(s);
+  init_shared<F32, NT>(s);
   const int live = p.n_tokens != nullptr ? min(max(__ldg(p.n_tokens), 0), p.T) : p.T;
   if (warp == 0) build_adapter_tables(p, tb, live);
   __syncthreads();
@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
   const int c1 = static_cast<int>(share_begin(rows_w, blockIdx.x + 1));
   const int dv = p.d_in / VEC;
   // chunks of the two phases
-  const int vecs[2] = {chunk_vecs(min(kTileRows, a1 - a0) + live, dv),
-                       chunk_vecs(M * min(TILE, c1 - c0) + live, dv)};
+  const int vecs[2] = {chunk_vecs(min(kTileRows, a1 - a0) + live, dv, kThinSlot),
+                       chunk_vecs(M * min(TILE, c1 - c0) + live, dv, kThinSlot)};
   const int chunks[2] = {(dv + vecs[0] - 1) / vecs[0], (dv + vecs[1] - 1) / vecs[1]};
   auto shrink_rows = [&](int at) {  // rows of the shrink tile at `at`: within one matrix
     return min(min(kTileRows, a1 - at), p.rank - at % p.rank);
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
     // ------------------------------------------------------------------ producers
     const size_t xs = static_cast<size_t>(p.d_in) * sizeof(Tin);
     const uint8_t* xb = static_cast<const uint8_t*>(p.x);
-    Producer<F32> pr(s, p.status);
+    Producer<kTeamWarps<F32, NT>> pr(s, p.status);
     bool go = true;
     // a tile: n0 rows from w0, then n1 rows from w1, against the tokens of `mask`
     auto tile = [&](const uint8_t* w0, int n0, const uint8_t* w1, int n1, uint32_t mask, int seg,
@@ -157,10 +157,9 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
           pr.open(SlotDesc{0, static_cast<int16_t>(n0), static_cast<int16_t>(n1),
                            static_cast<int16_t>(n), static_cast<int16_t>(P), i + 1 == nc,
                            static_cast<int8_t>(kind), 0, 0, mask, seg, row, kv},
-                  rows * bytes);
-          pr.copy_rows(pr.it, pr.head, P, 0, w0 + o, xs, n0, bytes);
-          pr.copy_rows(pr.it, pr.head, P, n0, w1 + o, xs, n1, bytes);
-          pr.copy_tokens(pr.it, pr.head, P, n0 + n1, xb + o, xs, mask, bytes);
+                  rows, bytes);
+          pr.copy_weights(P, w0 + o, n0, w1 + o, n1, xs, bytes);
+          pr.copy_tokens(P, n0 + n1, xb + o, xs, mask, bytes);
         }
         pr.pass(rows * P);
       }
@@ -245,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_few_kernel(const AdapterF
         float v[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-          v[m] = red_sum<NT>(red, kConsumerWarps, m, r, t);
+          v[m] = m == 0 ? red_sum<NT>(red, kConsumerWarps, 0, r, t)
+                        : red_sum_second<F32, NT>(d, red, kConsumerWarps, r, t);
           if (id >= 0)
             v[m] += expand(static_cast<const Tin*>(p.b[m]) +
                                (static_cast<size_t>(id) * p.d_out + c) * p.rank,
@@ -285,7 +285,7 @@ cudaError_t launch_pair(AdapterFewParams p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   p.smem_bytes = kSmemBytes;
-  return launch_cooperative(adapter_few_kernel<Tin, NT, PAIR>, dim3(sm_count()), dim3(kThreads),
+  return launch_cooperative(adapter_few_kernel<Tin, NT, PAIR>, dim3(sm_count()), dim3(kThreads<sizeof(Tin) == 4, NT>),
                             kSmemBytes, s, p);
 }
 

@@ -14,7 +14,7 @@
 //   -- barrier --  every CTA selects the top-k for all tokens itself (T * k <= 1024 routes)
 //                  and builds the same tables: per expert a 32-bit mask of its tokens.
 //   gate/up  (touched experts x F) row pairs, cut over the CTAs at equal cost; a tile is up to 16 gate
-//            rows with their 16 up rows, against the expert's own tokens only.
+//            rows with their 16 up rows (8 with few tokens), against the expert's own tokens only.
 //   -- barrier --  meanwhile the producer already streams W_down into the ring; only the
 //                  H rows of those slots wait for the barrier.
 //   down     d output rows, cut evenly over the CTAs; each CTA runs all touched experts'
@@ -321,7 +321,7 @@ struct DownPos {
 };
 
 template <typename Tin, int NT>
-__global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kThreads<sizeof(Tin) == 4, NT>, 1) few_layer_kernel(const FewParams p) {
   constexpr bool F32 = sizeof(Tin) == 4;
   constexpr int VEC = Vec<Tin>::N;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
   const Tin* X = static_cast<const Tin*>(p.x);
   Tin* H = static_cast<Tin*>(p.h);
 
-  init_shared<NT>(s);
+  init_shared<F32, NT>(s);
   const int live = p.n_tokens != nullptr ? min(max(__ldg(p.n_tokens), 0), p.T) : p.T;
   __syncthreads();
 
@@ -357,19 +357,24 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
   const int dv = p.d / VEC, fv = p.F / VEC;  // 16-byte vectors of a row
   // chunks of the two phases
   const int most = nseg > 0 ? tb.most : 0;
-  const int gu_vecs = chunk_vecs(2 * min(16, g1 - g0) + most, dv);
-  const int dn_vecs = chunk_vecs(min(kTileRows, c1 - c0) + most, fv);
+  // Row pairs of a gate/up tile.  With few tokens 8, and chunks twice as long: half the copies for
+  // the same bytes, one MMA row block instead of two, but twice the token rows.  us with 8 / 16:
+  // Granite-shaped T=1 18.5 / 19.2; Mixtral-shaped T=1 120 / 124, T=8 398 / 324.
+  const int pairs = !F32 && most <= 4 && dv >= 2 * kChunkVecs ? 8 : 16;
+  const int gu_vecs = chunk_vecs(2 * min(pairs, g1 - g0) + most, dv,
+                                 pairs == 8 ? 44 * 1024 : kThinSlot);
+  const int dn_vecs = chunk_vecs(min(kTileRows, c1 - c0) + most, fv, kThinSlot);
 
   if (warp >= kConsumerWarps) {
     // ------------------------------------------------------------------ producers
     const uint32_t P = pitch_of<F32>(gu_vecs);
     const size_t xs = static_cast<size_t>(p.d) * sizeof(Tin);  // bytes of a row of d
     const size_t hs = static_cast<size_t>(p.F) * sizeof(Tin);  // bytes of a row of F
-    Producer<F32> pr(s, p.status);
+    Producer<kTeamWarps<F32, NT>> pr(s, p.status);
     bool go = *s.abort_flag == 0;
     for (int at = g0; at < g1 && go;) {
       const int seg = at / p.F, f0 = at - seg * p.F;
-      const int np = min(min(16, g1 - at), p.F - f0);
+      const int np = min(min(pairs, g1 - at), p.F - f0);
       const int e = tb.seg_e[seg];
       const uint32_t mask = tb.seg_mask[seg];
       const uint32_t rows = 2 * np + __popc(mask);
@@ -390,10 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
           pr.open(SlotDesc{0, static_cast<int16_t>(np), static_cast<int16_t>(np),
                            static_cast<int16_t>(n), static_cast<int16_t>(P), i + 1 == chunks, 0, 0, 0,
                            mask, seg, f0, kv},
-                  rows * bytes);
-          pr.copy_rows(pr.it, pr.head, P, 0, wg + o, xs, np, bytes);
-          pr.copy_rows(pr.it, pr.head, P, np, wu + o, xs, np, bytes);
-          pr.copy_tokens(pr.it, pr.head, P, 2 * np, xb + o, xs, mask, bytes);
+                  rows, bytes);
+          pr.copy_weights(P, wg + o, np, wu + o, np, xs, bytes);
+          pr.copy_tokens(P, 2 * np, xb + o, xs, mask, bytes);
         }
         pr.pass(rows * P);
       }
@@ -403,10 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     // after it.
     const uint32_t first = pr.it;
     const uint32_t PD = pitch_of<F32>(dn_vecs);
-    const int fch = (fv + dn_vecs - 1) / dn_vecs, pairs = fch * nseg;
-    const int turn = static_cast<int>(static_cast<int64_t>(pairs) * blockIdx.x / gridDim.x);
+    const int fch = (fv + dn_vecs - 1) / dn_vecs, turns = fch * nseg;
+    const int turn = static_cast<int>(static_cast<int64_t>(turns) * blockIdx.x / gridDim.x);
     DownPos w{c0, min(kTileRows, c1 - c0),
-              turn / fch, turn % fch * dn_vecs, pairs};
+              turn / fch, turn % fch * dn_vecs, turns};
     auto next = [&](DownPos& q) {
       q.kv += dn_vecs;
       if (q.kv >= fv) {
@@ -414,20 +418,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
         if (++q.seg == nseg) q.seg = 0;
       }
       if (--q.left > 0) return;
-      q.left = pairs;  // back at the turn: the next tile
+      q.left = turns;  // back at the turn: the next tile
       q.row += q.nrows;
       q.nrows = min(kTileRows, c1 - q.row);
     };
-    auto load_h = [&](uint32_t it) {  // the H rows of slot `it`, one of this warp's
+    auto load_h = [&](uint32_t it) {  // the H rows of slot `it`, one of this team's
       const SlotDesc& d = s.desc[it % kSlots];
       pr.copy_rows(it, d.off, d.pitch, d.r0 + d.r1,
                    reinterpret_cast<const uint8_t*>(H) + tb.seg_hrow[d.seg] * hs + d.kv * 16, hs,
                    __popc(d.mask), d.kvec * 16);
     };
     auto load_late_h = [&] {
-      uint32_t it = first + (pr.me - first) % kProducerWarps;
+      uint32_t it = first + (pr.team() - first) % kTeams;
 #pragma unroll 1
-      for (; it < pr.it; it += kProducerWarps) load_h(it);
+      for (; it < pr.it; it += kTeams) load_h(it);
     };
     bool passed = false;
     auto pass_barrier = [&] {  // H is complete; bulk copies may read it
@@ -456,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
         pr.open(SlotDesc{0, static_cast<int16_t>(r0), static_cast<int16_t>(w.nrows - r0),
                          static_cast<int16_t>(n), static_cast<int16_t>(PD), w.left == 1, 1, 1, 0, mask,
                          w.seg, w.row, w.kv},
-                rows * n * 16);
-        pr.copy_rows(pr.it, pr.head, PD, 0, wd, hs, w.nrows, n * 16);
+                rows, n * 16);
+        pr.copy_weights(PD, wd, w.nrows, wd, 0, hs, n * 16);
         if (passed) load_h(pr.it);
       }
       pr.pass(rows * PD);
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
     const int rows = c1 - c0;
     int gu_tiles = 0;
 #pragma unroll 1
-    for (int at = g0; at < g1; ++gu_tiles) at += min(min(16, g1 - at), p.F - at % p.F);
+    for (int at = g0; at < g1; ++gu_tiles) at += min(min(pairs, g1 - at), p.F - at % p.F);
     const int tiles[2] = {ok ? gu_tiles : 0,
                           ok && nseg > 0 ? (rows + kTileRows - 1) / kTileRows : 0};
     const int chunks[2] = {(dv + gu_vecs - 1) / gu_vecs, (fv + dn_vecs - 1) / dn_vecs * nseg};
@@ -494,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
           const int r = i & 15, n = i >> 4;
           if (r >= d.r0) continue;
           const float g = red_sum<NT>(red, crew.warps, 0, r, n);
-          const float u = red_sum<NT>(red, crew.warps, 1, r, n);
+          const float u = red_sum_second<F32, NT>(d, red, crew.warps, r, n);
           const float v = g / (1.f + expf(-g)) * u * tb.gate_of_row[hrow + n];
           Tin* o = H + static_cast<size_t>(hrow + n) * p.F + d.row + r;
           if constexpr (F32) *o = v;
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_layer_kernel(const FewParams 
       if (tid == 0) grid_arrive(p.sync);
       return well;
     };
-    consume<F32, NT>(s, tiles, chunks, solo_tiles<NT>(tiles[0], chunks[0]), p.status, epilogue,
+    consume<F32, NT>(s, tiles, chunks, solo_tiles<F32, NT>(tiles[0], chunks[0]), p.status, epilogue,
                      between);
     if (nseg == 0 && ok) {  // capacity 0 and no shared expert: only the residual is left
 #pragma unroll 1
@@ -536,7 +540,7 @@ cudaError_t launch_nt(FewParams p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   p.smem_bytes = kSmemBytes;
-  return launch_cooperative(few_layer_kernel<Tin, NT>, dim3(sm_count()), dim3(kThreads), kSmemBytes,
+  return launch_cooperative(few_layer_kernel<Tin, NT>, dim3(sm_count()), dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes,
                             s, p);
 }
 

@@ -5,14 +5,17 @@
 //   * One CTA per SM, all resident (cooperative launch).  Every phase cuts its output rows
 //     (weight rows) evenly over the CTAs, at single-row granularity, whatever the expert.
 //   * Warps 8.. produce: the CTA's rows are cut into tiles of up to 32 weight rows and the
-//     contraction into chunks of 1 KB per row (2 or 4 KB in thin tiles, chunk_vecs); a slot of the ring holds one chunk of a
-//     tile's weight rows and of its token rows, copied with one bulk copy per row.  Slots
+//     contraction into chunks of 1 KB per row (2 or 4 KB in thin tiles, chunk_vecs); a slot of
+//     the ring holds one chunk of a tile's weight rows and of its token rows, copied with one
+//     bulk copy per row.  Slots
 //     are sized by the rows they hold, so thin tiles (a phase that leaves a CTA 7 rows)
 //     still keep the whole ring in flight; the stream does not stop between tiles or phases.
-//     One warp issues a bulk copy about every 45 ns, which would cap the stream at half of
-//     HBM's rate (Mixtral-shaped T=16: 890 us with one producer), so slot i belongs to
-//     producer warp i mod kProducerWarps, one lane per row; every producer follows the same
-//     sequence of slots and places them by the same arithmetic.
+//     One warp issues a bulk copy about every 28 to 45 ns, which would cap the stream at half
+//     of HBM's rate (Mixtral-shaped T=16: 890 us with one producer), so slot i belongs to
+//     producer team i mod kTeams, one lane per row; every producer follows the same
+//     sequence of slots and places them by the same arithmetic.  The rate is the ring's bytes
+//     over a slot's time in it (4 us; the copies alone, in a ring a third as long, reach
+//     6.6 TB/s), not HBM's latency: weights that are in L2 already stream as fast.
 //   * Warps 0-7 consume, two or four warps to a slot, several slots at a time: a slot costs a warp
 //     a fixed latency (its barrier, descriptor, first loads) that eight warps sharing every
 //     slot all paid (Granite-shaped T=16: 0.7 us per 11-row slot), now paid in parallel.
@@ -41,15 +44,24 @@ constexpr int kMaxTokens = 32;       // one token-mask word
 constexpr int kConsumerWarps = 8;
 constexpr int kConsumers = 32 * kConsumerWarps;
 // Warps that share a slot: more of them where token rows leave the ring few slots, which are then
-// to be released sooner (16+1 experts T=32: 759 us with 2, 711 us with 4; T=1: 108.7 and 109.1).
-template <int NT> constexpr int kGroupWarps = NT == 1 ? 2 : 4;
-template <int NT> constexpr int kGroups = kConsumerWarps / kGroupWarps<NT>;
-constexpr int kProducerWarps = 4;
-constexpr int kThreads = kConsumers + 32 * kProducerWarps;
+// to be released sooner.  us with 2 / 4: 16+1 experts T=32 643 / 606, T=16 467 / 472,
+// Granite-shaped T=16 38.9 / 40.0; fp32, 12+1 experts T=16 373 / 342.
+template <bool F32, int NT> constexpr int kGroupWarps = NT == 1 || (NT == 2 && !F32) ? 2 : 4;
+template <bool F32, int NT> constexpr int kGroups = kConsumerWarps / kGroupWarps<F32, NT>;
+// Producers: teams of warps, a slot's copies dealt over the warps of its team.  A slot takes one warp
+// 0.4 us plus 28 ns per copy, 1.5 us for 36 rows, which is a third of its time in the ring.
+// Measured, us with 4 x 1 / 4 x 2 / 2 x 4 / 8 x 1 warps: Mixtral-shaped T=16 363 / 338 / 357 / 353,
+// T=8 341 / 325 / 340 / 334, 16+1 experts T=16 508 / 474 / 507 / 484.  fp32 and more than 16 tokens
+// need more than the 128 registers a thread of 8 producer warps (fp32 T=16: 312 / 465).
+constexpr int kTeams = 4;
+template <bool F32, int NT> constexpr int kTeamWarps = F32 || NT == 4 ? 1 : 2;
+template <bool F32, int NT>
+constexpr int kThreads = kConsumers + 32 * kTeams * kTeamWarps<F32, NT>;
 constexpr int kSlots = 64;           // slot descriptors and barriers
 constexpr int kChunkBytes = 1024;    // contraction bytes per row of the smallest chunk
 constexpr int kChunkVecs = kChunkBytes / 16;
 constexpr int kMaxChunkVecs = 4 * kChunkVecs;
+constexpr int kThinSlot = 24 * 1024;  // limit of chunk_vecs
 constexpr uint32_t kSmemBytes = 227 * 1024;
 constexpr int kTileRows = 32;        // weight rows per tile at most (two MMA row blocks)
 constexpr int kRedStride = 36;       // floats per token column of the partial sums: the MMA
@@ -63,10 +75,10 @@ __host__ __device__ constexpr uint32_t pitch_of(int chunk_vecs) {
 }
 // 16-byte vectors along the contraction of a phase's chunks, for tiles of at most `rows` rows
 // (token rows too) of `vecs` vectors.  A slot costs its warps a fixed latency whatever it holds,
-// so thin tiles take longer chunks, while the slot stays within 24 KB (of a ring of about 170).
-__device__ __forceinline__ int chunk_vecs(int rows, int vecs) {
+// so thin tiles take longer chunks, while the slot stays within `limit` (of a ring of about 190 KB).
+__device__ __forceinline__ int chunk_vecs(int rows, int vecs, int limit) {
   int v = kChunkVecs;
-  while (v < kMaxChunkVecs && v < vecs && rows * (2 * v * 16 + 64) <= 24 * 1024) v *= 2;
+  while (v < kMaxChunkVecs && v < vecs && rows * (2 * v * 16 + 64) <= limit) v *= 2;
   return v;
 }
 
@@ -91,7 +103,6 @@ struct Shared {
   uint64_t* full;
   uint64_t* empty;
   SlotDesc* desc;
-  uint32_t* start;  // [kProducerWarps][kSlots]: each producer's record of slot positions
   uint64_t* sums;   // [2] a tile's partial sums are complete
   uint64_t* freed;  // a tile's epilogue is done (one buffer of partial sums)
   uint64_t* passed; // this CTA knows that all CTAs have arrived
@@ -103,9 +114,9 @@ struct Shared {
   uint32_t ring_bytes;
 };
 
-constexpr int kCtlBytes = 2 * kSlots * 8 + kSlots * 32 + kProducerWarps * kSlots * 4 + 2 * 32 + 64 + kChunkBytes;
+constexpr int kCtlBytes = 2 * kSlots * 8 + kSlots * 32 + 2 * 32 + 64 + kChunkBytes;
 static_assert(sizeof(SlotDesc) == 32, "descriptor size");
-static_assert(kSlots % kGroups<1> == 0 && kSlots % kGroups<4> == 0,
+static_assert(kSlots % kGroups<false, 1> == 0 && kSlots % kGroups<true, 4> == 0,
               "a slot's barriers belong to one group");
 template <int NT> constexpr int kRedFloats = kConsumerWarps * 8 * NT * kRedStride;
 // Buffers of partial sums: two for up to 8 tokens; with more tokens one (and a barrier for its
@@ -121,8 +132,7 @@ __device__ __forceinline__ Shared carve(uint8_t* smem, uint32_t table_bytes, uin
   s.full = reinterpret_cast<uint64_t*>(smem);
   s.empty = s.full + kSlots;
   s.desc = reinterpret_cast<SlotDesc*>(s.empty + kSlots);
-  s.start = reinterpret_cast<uint32_t*>(s.desc + kSlots);
-  s.tile = reinterpret_cast<SlotDesc*>(s.start + kProducerWarps * kSlots);
+  s.tile = s.desc + kSlots;
   s.sums = reinterpret_cast<uint64_t*>(s.tile + 2);
   s.freed = s.sums + 2;
   s.passed = s.freed + 1;
@@ -135,14 +145,14 @@ __device__ __forceinline__ Shared carve(uint8_t* smem, uint32_t table_bytes, uin
   return s;
 }
 
-template <int NT>
+template <bool F32, int NT>
 __device__ __forceinline__ void init_shared(const Shared& s) {
-  for (int i = threadIdx.x; i < kChunkVecs; i += kThreads)
+  for (int i = threadIdx.x; i < kChunkVecs; i += kThreads<F32, NT>)
     reinterpret_cast<uint4*>(s.zeros)[i] = make_uint4(0, 0, 0, 0);
   // one slot's barriers per thread: 128 initialisations in a row took 0.5 us
   if (threadIdx.x < kSlots) {
-    mbar_init(&s.full[threadIdx.x], 1);
-    mbar_init(&s.empty[threadIdx.x], kGroupWarps<NT>);
+    mbar_init(&s.full[threadIdx.x], kTeamWarps<F32, NT>);
+    mbar_init(&s.empty[threadIdx.x], kGroupWarps<F32, NT>);
   } else if (threadIdx.x == kSlots) {
     mbar_init(&s.sums[0], kConsumerWarps);
     mbar_init(&s.sums[1], kConsumerWarps);
@@ -183,7 +193,7 @@ __device__ __forceinline__ bool consumer_all(bool v) {
 }
 
 // The barrier of one group's warps; returns whether `v` held on all of its threads.
-template <int NT>
+template <bool F32, int NT>
 __device__ __forceinline__ bool group_all(uint32_t group, bool v) {
   uint32_t r;
   asm volatile(
@@ -192,7 +202,7 @@ __device__ __forceinline__ bool group_all(uint32_t group, bool v) {
       "bar.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(2 + group), "n"(32 * kGroupWarps<NT>)
+      : "r"(static_cast<uint32_t>(v)), "r"(2 + group), "n"(32 * kGroupWarps<F32, NT>)
       : "memory");
   return r != 0;
 }
@@ -260,18 +270,20 @@ __device__ __forceinline__ void fence_proxy_async_all() {
 // computes the same places, and a slot may be written once the oldest slot still in use
 // starts less than a ring's length before its end.  A producer waits for the slots' releases
 // in order and keeps fewer than kInFlight of them unreleased when it fills one.
-//   It must not fall behind by two uses of a slot, whose barrier parity would be ambiguous:
-// while it waits, with its own slot j not filled, for the release of `tail`, no slot from
-// tail + kSlots on may be released.  The others pass slot j only by being ahead, and fill
-// slots below j + kInFlight at most; its own slots are kProducerWarps apart, so
-// j - tail < kInFlight + kProducerWarps.  Hence 2 kInFlight + kProducerWarps <= kSlots + 1.
+//   Slot i belongs to team i mod kTeams; warp j of a team of TW copies the slot's rows j, j + TW,
+// ... and arrives at the slot's barrier for their bytes.
+//   A producer must not fall behind by two uses of a slot, whose barrier parity would be
+// ambiguous: while it waits, with its own slot j not filled, for the release of `tail`, no slot from
+// tail + kSlots on may be released.  The other teams pass slot j only by being ahead, and fill
+// slots below j + kInFlight at most; its own slots are kTeams apart, so
+// j - tail < kInFlight + kTeams.  Hence 2 kInFlight + kTeams <= kSlots + 1.
 // ---------------------------------------------------------------------------------
-constexpr uint32_t kInFlight = (kSlots + 1 - kProducerWarps) / 2;
-template <bool F32>
+constexpr uint32_t kInFlight = (kSlots + 1 - kTeams) / 2;
+template <int TW>
 struct Producer {
   Shared s;
   int32_t* status;
-  uint32_t* start;     // line positions of the last kSlots slots
+  uint32_t start[kSlots / 32] = {};  // line positions of the last slots, slot i's in lane i % 32
   uint32_t me;         // this producer's index
   uint32_t line = 0;   // line position of the next slot
   uint32_t head = 0;   // the same modulo the ring
@@ -279,10 +291,13 @@ struct Producer {
   uint32_t tail = 0;   // slots known to be released
 
   __device__ __forceinline__ Producer(const Shared& sh, int32_t* st)
-      : s(sh), status(st), me((threadIdx.x >> 5) - kConsumerWarps) {
-    start = s.start + me * kSlots;
+      : s(sh), status(st), me((threadIdx.x >> 5) - kConsumerWarps) {}
+  __device__ __forceinline__ uint32_t team() const { return me / TW; }
+  __device__ __forceinline__ bool mine() const { return it % kTeams == team(); }
+  // Whether this warp copies row r of its team's slots.
+  __device__ __forceinline__ bool copies(uint32_t r) const {
+    return r % TW == me % TW;
   }
-  __device__ __forceinline__ bool mine() const { return it % kProducerWarps == me; }
 
   // Take the place of the next slot; `pass` moves on to the one after it.
   __device__ __forceinline__ void reserve(uint32_t bytes) {
@@ -290,8 +305,16 @@ struct Producer {
       line += s.ring_bytes - head;
       head = 0;
     }
-    if ((threadIdx.x & 31) == 0) start[it % kSlots] = line;
-    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kSlots / 32; ++i)
+      if (it % kSlots == 32 * i + (threadIdx.x & 31)) start[i] = line;
+  }
+  __device__ __forceinline__ uint32_t start_of(uint32_t slot) const {
+    uint32_t v = start[0];
+#pragma unroll
+    for (int i = 1; i < kSlots / 32; ++i)
+      if (slot % kSlots >= 32 * i) v = start[i];
+    return __shfl_sync(0xffffffffu, v, slot % 32);
   }
   __device__ __forceinline__ void pass(uint32_t bytes) {
     line += bytes;
@@ -302,7 +325,7 @@ struct Producer {
   // `stop` or a later one, or -1 on abort.
   __device__ __forceinline__ int ready(uint32_t bytes, uint32_t stop) {
     while (tail != it &&  // warp-uniform: every lane sees the same state
-           (it - tail >= kInFlight || line + bytes - start[tail % kSlots] > s.ring_bytes)) {
+           (it - tail >= kInFlight || line + bytes - start_of(tail) > s.ring_bytes)) {
       if (tail >= stop) return 0;
       if (!__all_sync(0xffffffffu, wait(&s.empty[tail % kSlots], (tail / kSlots) & 1u,
                                         s.abort_flag, status)))
@@ -311,42 +334,52 @@ struct Producer {
     }
     return 1;
   }
-  // Publish the slot's descriptor and arm its barrier; then come its copies.
-  __device__ __forceinline__ void open(SlotDesc d, uint32_t bytes) {
+  // Publish the slot's descriptor (all warps of the team write the same) and arm its barrier for
+  // this warp's part of `rows` rows of `bytes` bytes; then come its copies.
+  __device__ __forceinline__ void open(SlotDesc d, uint32_t rows, uint32_t bytes) {
     d.off = head;
     if ((threadIdx.x & 31) == 0) {
       s.desc[it % kSlots] = d;
-      mbar_arrive_expect_tx(&s.full[it % kSlots], bytes);
+      mbar_arrive_expect_tx(&s.full[it % kSlots],
+                            (rows + TW - 1 - me % TW) / TW * bytes);
     }
     __syncwarp();
   }
-  // Copy `rows` (at most 32) rows of `bytes` bytes, `stride` bytes apart, to rows row.. of the
-  // slot at `off`.
+  // This warp's part of the weight rows of slot `it`: n0 (at most 32) from w0, then n1 from w1.
+  __device__ __forceinline__ void copy_weights(uint32_t pitch, const uint8_t* w0, int n0,
+                                               const uint8_t* w1, int n1, size_t stride,
+                                               uint32_t bytes) {
+    const int r = (threadIdx.x & 31) * TW + me % TW;  // a tile has at most 32 rows
+    if (r < n0 + n1)
+      bulk_load(s.ring + head + static_cast<uint32_t>(r) * pitch,
+                r < n0 ? w0 + r * stride : w1 + (r - n0) * stride, bytes, &s.full[it % kSlots]);
+    __syncwarp();
+  }
+  // This warp's part of `n` (at most 32) rows behind the `row` weight rows of the slot at `off`.
   __device__ __forceinline__ void copy_rows(uint32_t slot, uint32_t off, uint32_t pitch, int row,
-                                            const uint8_t* src, size_t stride, int rows,
+                                            const uint8_t* src, size_t stride, int n,
                                             uint32_t bytes) {
     const int r = threadIdx.x & 31;
-    if (r < rows)
+    if (r < n && copies(row + r))
       bulk_load(s.ring + off + static_cast<uint32_t>(row + r) * pitch, src + r * stride,
                 bytes, &s.full[slot % kSlots]);
     __syncwarp();
   }
   // The same for the rows of a token mask.
-  __device__ __forceinline__ void copy_tokens(uint32_t slot, uint32_t off, uint32_t pitch,
-                                              int row, const uint8_t* src, size_t stride, uint32_t mask,
-                                              uint32_t bytes) {
+  __device__ __forceinline__ void copy_tokens(uint32_t pitch, int row, const uint8_t* src,
+                                              size_t stride, uint32_t mask, uint32_t bytes) {
     const int t = threadIdx.x & 31;
-    if ((mask >> t) & 1u)
-      bulk_load(s.ring + off +
-                    static_cast<uint32_t>(row + __popc(mask & ((1u << t) - 1u))) * pitch,
-                src + t * stride, bytes, &s.full[slot % kSlots]);
+    const int r = row + __popc(mask & ((1u << t) - 1u));
+    if (((mask >> t) & 1u) && copies(r))
+      bulk_load(s.ring + head + static_cast<uint32_t>(r) * pitch, src + t * stride, bytes,
+                &s.full[it % kSlots]);
     __syncwarp();
   }
   // Before leaving early: every copy of this producer has landed, or has had the wait's
   // limit to.
   __device__ __forceinline__ void drain() {
     for (uint32_t i = it - min(it, static_cast<uint32_t>(kSlots)); i < it; ++i)
-      if (i % kProducerWarps == me &&
+      if (i % kTeams == team() &&
           !wait_slow(&s.full[i % kSlots], (i / kSlots) & 1u, nullptr, status))
         break;
   }
@@ -372,6 +405,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+// bf16 pair tiles of at most 8 rows of each matrix take one 16-row block: the first matrix's rows
+// are its rows 0-7, the second's its rows 8-15.
+__device__ __forceinline__ bool pair_fold(const SlotDesc& d) { return d.r1 > 0 && d.r0 <= 8; }
 
 // Accumulators of one tile: bf16 fragments [row block][token block][4], or fp32 [token].
 template <bool F32, int NT> struct Acc;
@@ -411,7 +448,9 @@ template <int NT> struct Acc<false, NT> {
     const int g = lane >> 2, q = lane & 3;
     const uint32_t at = (part * 4 + q) * 16;
     // 16-row blocks: rows past a block's last one are clamped to it
-    uint32_t a[4] = {base + min(g, d.r0 - 1) * P + at, base + min(g + 8, d.r0 - 1) * P + at,
+    // (a pair tile of up to 8 rows each: one block, see pair_fold)
+    uint32_t a[4] = {base + min(g, d.r0 - 1) * P + at,
+                           base + (pair_fold(d) ? d.r0 + min(g, d.r1 - 1) : min(g + 8, d.r0 - 1)) * P + at,
                            base + (d.r0 + min(g, d.r1 - 1)) * P + at,
                            base + (d.r0 + min(g + 8, d.r1 - 1)) * P + at};
     const int nb = __popc(d.mask);
@@ -425,7 +464,7 @@ template <int NT> struct Acc<false, NT> {
       step[n] = row >= 0 ? kChunkBytes : 0;
     }
     float part_c[2][NT][4] = {};
-    constexpr int kStep = kGroupWarps<NT> * 64;                // bytes between a warp's blocks
+    constexpr int kStep = kGroupWarps<false, NT> * 64;         // bytes between a warp's blocks
     constexpr int kBlocks = kChunkBytes / kStep;
     constexpr int HB = NB == 4 ? 2 : 4;  // blocks loaded together, so that latencies overlap
 #pragma unroll 1
@@ -479,7 +518,7 @@ template <int NT> struct Acc<false, NT> {
   template <int NB>
   __device__ __forceinline__ void chunk_n(const SlotDesc& d, const Shared& s, int part,
                                           int lane) {
-    if (d.r1 > 0) chunk_of<true, NB>(d, s, part, lane);
+    if (d.r1 > 0 && !pair_fold(d)) chunk_of<true, NB>(d, s, part, lane);
     else chunk_of<false, NB>(d, s, part, lane);
   }
   __device__ __forceinline__ void chunk(const SlotDesc& d, const Shared& s, int part, int lane) {
@@ -529,7 +568,7 @@ template <int NT> struct Acc<true, NT> {
     const uint32_t a = base + min(lane & (rows - 1), n_rows - 1) * P + k * 16;
     const uint32_t b = base + n_rows * P + k * 16;
 #pragma unroll 1
-    for (int v0 = part * V * ks; v0 < d.kvec; v0 += V * ks * kGroupWarps<NT>) {
+    for (int v0 = part * V * ks; v0 < d.kvec; v0 += V * ks * kGroupWarps<true, NT>) {
       const int left = d.kvec - v0 - k;  // this lane's vectors: 0, ks, 2 ks, ...
       float w[V][4];
 #pragma unroll
@@ -590,6 +629,14 @@ __device__ __forceinline__ float red_sum(const float* red, int warps, int m, int
   return v;
 }
 
+// The total of row i of a pair tile's second matrix.
+template <bool F32, int NT>
+__device__ __forceinline__ float red_sum_second(const SlotDesc& d, const float* red, int warps,
+                                                int i, int n) {
+  const bool fold = !F32 && pair_fold(d);
+  return red_sum<NT>(red, warps, fold ? 0 : 1, fold ? 8 + i : i, n);
+}
+
 // Who runs a tile's epilogue: `count` threads, this one the `index`-th of them, on the partial
 // sums of `warps` warps.
 struct Crew {
@@ -598,16 +645,18 @@ struct Crew {
 
 // A phase whose tiles have few slots gives a tile to one group, which sums up and finishes it by
 // itself while the others are at other tiles: shared by all groups, a tile of two slots costs the
-// latency of both barriers and of the epilogue each time (Granite-shaped T=16: XX us instead of
-// YY).  With more slots to a tile the ring would hold slots of one group's tile only.
+// latency of both barriers and of the epilogue each time (32 experts, d=512, F=4096 T=16: 144 us
+// shared, 121 us by one group; Granite-shaped T=16 42.9 and 41.9).  Not in fp32, whose FMAs take
+// longer than those barriers (12+1 experts T=4: 80 us shared, 98 us by one group).  With more slots to a tile the ring would hold slots of one group's tile only.
 //   No group waits for use n + 1 of a slot's barrier before use n has completed: when it
 // waits for slots of its next tile, at most kGroups tiles on, the slots up to kInFlight before
 // the tile it finished have been filled.
 constexpr int kSoloChunks = 4;
-static_assert(kGroups<1> * kSoloChunks + kInFlight <= kSlots, "no parity of a slot is ambiguous");
-template <int NT>
+static_assert(kGroups<false, 1> * kSoloChunks + kInFlight <= kSlots,
+              "no parity of a slot is ambiguous");
+template <bool F32, int NT>
 __device__ __forceinline__ bool solo_tiles(int tiles, int chunks) {
-  return chunks <= kSoloChunks && tiles >= kGroups<NT>;
+  return !F32 && chunks <= kSoloChunks && tiles >= kGroups<F32, NT>;
 }
 
 // Consume the tiles of two phases: tiles[0] of chunks[0] slots each, then `between`, then
@@ -626,8 +675,8 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
                                         const int (&chunks)[2], bool solo, int32_t* status,
                                         Epi&& epilogue, Between&& between) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t group = warp / kGroupWarps<NT>;
-  const int part = warp % kGroupWarps<NT>;
+  const uint32_t group = warp / kGroupWarps<F32, NT>;
+  const int part = warp % kGroupWarps<F32, NT>;
   const int total = tiles[0] + tiles[1];
   constexpr int kWarpFloats = 8 * NT * kRedStride;
   uint32_t it = 0;       // slots passed
@@ -654,9 +703,9 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
       if (tile == total) return;
       acc.zero();
       if (solo) it = tile * chunks[0];
-      const uint32_t end = it + chunks[crossed ? 1 : 0], step = solo ? 1 : kGroups<NT>;
+      const uint32_t end = it + chunks[crossed ? 1 : 0], step = solo ? 1 : kGroups<F32, NT>;
 #pragma unroll 1
-      for (it += solo ? 0 : (group - it) % kGroups<NT>; it < end; it += step) {
+      for (it += solo ? 0 : (group - it) % kGroups<F32, NT>; it < end; it += step) {
         const uint32_t slot = it % kSlots;
         ok = __all_sync(0xffffffffu,
                         wait(&s.full[slot], (it / kSlots) & 1u, s.abort_flag, status));
@@ -669,17 +718,17 @@ __device__ __forceinline__ void consume(const Shared& s, const int (&tiles)[2],
       }
       it = end;
       if (solo) {
-        ok = group_all<NT>(group, ok);  // and the tile before is finished
+        ok = group_all<F32, NT>(group, ok);  // and the tile before is finished
         acc.store(s.red, warp, lane);
-        ok = group_all<NT>(group, ok);
+        ok = group_all<F32, NT>(group, ok);
         if (!ok) {
           between(false);
           return;
         }
-        constexpr int kCrew = 32 * kGroupWarps<NT>;
-        epilogue(d, s.red + group * kGroupWarps<NT> * kWarpFloats,
-                 Crew{static_cast<int>(threadIdx.x) % kCrew, kCrew, kGroupWarps<NT>});
-        tile += kGroups<NT>;
+        constexpr int kCrew = 32 * kGroupWarps<F32, NT>;
+        epilogue(d, s.red + group * kGroupWarps<F32, NT> * kWarpFloats,
+                 Crew{static_cast<int>(threadIdx.x) % kCrew, kCrew, kGroupWarps<F32, NT>});
+        tile += kGroups<F32, NT>;
         continue;
       }
     }
