@@ -286,7 +286,7 @@ cudaError_t launch_pair(AdapterFewParams p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   p.smem_bytes = kSmemBytes;
   return launch_cooperative(adapter_few_kernel<Tin, NT, PAIR>, dim3(sm_count()), dim3(kThreads<sizeof(Tin) == 4, NT>),
-                            kSmemBytes, s, p);
+                            kSmemBytes, 0, s, p);
 }
 
 template <typename Tin>

@@ -28,6 +28,7 @@
 
 #include "adapter_gemm.cuh"
 #include "gemm_common.cuh"
+#include "grid_sync.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -49,7 +50,7 @@ struct ShrinkParams {
   const int32_t* n_tokens;
   uint4* u;         // [2, T, rank / 8]: 8 ranks as 8 high and 8 low bf16 halves (2 vectors)
   float* u_parts;   // else [parts, 2, T, rank]: fp32 sums of `parts` pieces of the contraction
-  int parts;        // 0: u
+  int turns, parts; // a token tile's work is dealt over turns x parts CTAs (see shrink_tile)
   int32_t* blocks;  // [token blocks][1 + kMaxBlockAdapters]: adapters of each GEMM token block
   int32_t* status;
   int T, d_in, n, rank, block_tokens;
@@ -129,27 +130,28 @@ __device__ __forceinline__ void shrink_partial(float (&c)[4][4], const __nv_bflo
   }
 }
 
-__global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(const ShrinkParams p) {
-  __shared__ float red[kShrinkWarps][kShrinkTokens][kShrinkRanks + 1];
-  pdl_trigger();  // the GEMM may start; it waits for this grid before it reads u
+// Barrier of the 256 threads that shrink.
+__device__ __forceinline__ void shrink_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kShrinkWarps) : "memory");
+}
+using ShrinkSums = float[kShrinkWarps][kShrinkTokens][kShrinkRanks + 1];
+
+// Projection m of the 16 tokens of `tile` by 256 threads: every turns-th adapter of theirs from
+// `turn` on, piece `part` of the contraction.  PARTS: fp32 pieces, else u.
+template <bool PARTS>
+__device__ __forceinline__ void shrink_tile(const ShrinkParams& p, ShrinkSums& red, int tile,
+                                            int turn, int m, int part, int live) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int parts = max(p.parts, 1), m = blockIdx.z / parts, part = blockIdx.z % parts;
-  const int t0 = blockIdx.x * kShrinkTokens;
+  const int parts = PARTS ? p.parts : 1;
+  const int t0 = tile * kShrinkTokens;
   const int dv = p.d_in / 8, blocks = (dv + 3) / 4;  // whole 32-wide blocks to a part
   const int v_lo = blocks * part / parts * 4, v_hi = min(dv, blocks * (part + 1) / parts * 4);
-  const int live = live_tokens(p.n_tokens, p.T);
-  const int tiles = (p.T + kShrinkTokens - 1) / kShrinkTokens;
-  if (blockIdx.x >= tiles) {  // the CTAs behind the token tiles list the blocks' adapters
-    const int tb = blockIdx.x - tiles;
-    if (blockIdx.y == 0 && blockIdx.z == 0 && tb * p.block_tokens < live) list_block_adapters(p, tb, live);
-    return;
-  }
-  if (t0 >= live) return;
   const int nt = min(kShrinkTokens, live - t0);
   int id = lane < nt ? __ldg(p.ids + t0 + lane) : -1;
   if (id < -1 || id >= p.n) {
-    if (blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) record_status(p.status, MOE_ERR_BAD_ADAPTER_ID);
+    if (turn == 0 && m == 0 && part == 0 && warp == 0)
+      record_status(p.status, MOE_ERR_BAD_ADAPTER_ID);
     id = -1;
   }
   const uint32_t same = __match_any_sync(0xffffffffu, id);
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
   const __nv_bfloat16* x1 = p.x + static_cast<size_t>(t0 + min(g + 8, nt - 1)) * p.d_in;
 
   for (int i = 0; leaders != 0; leaders &= leaders - 1, ++i) {
-    if (i % gridDim.y != blockIdx.y) continue;  // the same for every warp
+    if (i % p.turns != turn) continue;  // the same for every warp
     const int lead = __ffs(leaders) - 1;
     const int a_id = __shfl_sync(0xffffffffu, id, lead);
     const uint32_t tokens = __shfl_sync(0xffffffffu, same, lead);
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
         red[warp][g + 8][8 * n + 2 * q] = c[n][2];
         red[warp][g + 8][8 * n + 2 * q + 1] = c[n][3];
       }
-      __syncthreads();
+      shrink_sync();
       // a thread: two neighbouring ranks of a token
       const int t = threadIdx.x / (kShrinkRanks / 2), j = threadIdx.x % (kShrinkRanks / 2) * 2;
       if (((tokens >> t) & 1u) && j0 + j < p.rank) {
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
         }
         v[0] *= sc;
         v[1] *= sc;
-        if (p.parts > 0) {
+        if constexpr (PARTS) {
           *reinterpret_cast<float2*>(
               p.u_parts + ((static_cast<size_t>(part) * 2 + m) * p.T + t0 + t) * p.rank + j0 + j) =
               make_float2(v[0], v[1]);
@@ -209,9 +211,27 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
           u[4] = lo;
         }
       }
-      __syncthreads();
+      shrink_sync();
     }
   }
+}
+
+template <bool PARTS>
+__global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(const ShrinkParams p) {
+  __shared__ ShrinkSums red;
+  pdl_trigger();  // the GEMM may start; it waits for this grid before it reads u
+  const int live = live_tokens(p.n_tokens, p.T);
+  const int tiles = (p.T + kShrinkTokens - 1) / kShrinkTokens;
+  const int tile = blockIdx.x;
+  if (tile >= tiles) {  // the CTAs behind the token tiles list the blocks' adapters
+    const int tb = tile - tiles;
+    if (blockIdx.y == 0 && blockIdx.z == 0 && tb * p.block_tokens < live)
+      list_block_adapters(p, tb, live);
+    return;
+  }
+  const int parts = PARTS ? p.parts : 1;
+  if (tile * kShrinkTokens < live)
+    shrink_tile<PARTS>(p, red, tile, blockIdx.y, blockIdx.z / parts, blockIdx.z % parts, live);
 }
 
 // ------------------------------------------------------------------------------ GEMM
@@ -255,6 +275,9 @@ struct GemmParams {
   int32_t* status;
   int T, d_in, d_out, n, rank;
   int row_blocks, tok_blocks, boxes, stages, split;  // split: CTAs of a cluster per tile
+  int fused;            // with a cluster per tile: the shrink is in this kernel
+  ShrinkParams shrink;
+  GridSync sync;
 };
 
 // What of s B u the epilogue adds: nothing, all of it, or the products with the non-finite
@@ -622,6 +645,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
     }
+    if (SPLIT && p.fused) {
+      // the shrink, over all CTAs of the grid, while W streams
+      ShrinkSums& red = *reinterpret_cast<ShrinkSums*>(su_all);
+      const int turns = p.shrink.turns, parts = p.shrink.parts;
+      const int items = (live + kShrinkTokens - 1) / kShrinkTokens * (turns * M * parts);
+#pragma unroll 1
+      for (int i = blockIdx.x; i < items; i += gridDim.x) {
+        const int part = i % parts, m = i / parts % M, turn = i / (parts * M) % turns;
+        shrink_tile<true>(p.shrink, red, i / (parts * M * turns), turn, m, part, live);
+      }
+      shrink_sync();
+      if (threadIdx.x == 0) grid_arrive(p.sync);
+    }
     pdl_wait();  // u is complete; what read y before this call is done
     for (int tile = first_tile, iter = 0; tile < total; tile += tile_step, ++iter) {
       const int rb = tile / tok_blocks, tb = tile - rb * tok_blocks;
@@ -667,6 +703,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   }
   if constexpr (SPLIT) {  // one tile per cluster
+    if (p.fused && threadIdx.x == 0 && first_tile < total)  // u is complete
+      grid_wait(p.sync, gridDim.x, abort_flag, p.status);
     __syncwarp();
     cluster_sync_all();
     if (warp < kEpiWarps && first_tile < total && *abort_flag == 0) {
@@ -699,6 +737,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem_base, 2 * ACC_COLS);
+  if (SPLIT && p.fused && threadIdx.x == 0 && *abort_flag == 0) grid_leave(p.sync);
 }
 
 // Clusters of `size` CTAs of the GEMM that the current device holds at once: fewer than its SMs
@@ -741,7 +780,7 @@ cudaError_t set_up_gemm() {
 }
 
 template <bool PAIR>
-cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, cudaStream_t s) {
+cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, int ctas, cudaStream_t s) {
   constexpr int NT = kTileTokens<PAIR>;
   const int sms = sm_count();
   p.row_blocks = (p.d_out + BW - 1) / BW;
@@ -753,9 +792,13 @@ cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, cudaStream_t s) {
     return launch_pdl(adapter_gemm_kernel<PAIR, false>, dim3(static_cast<unsigned>(std::min<int64_t>(
                                                      tiles, sms))),
                       dim3(kGemmThreads), kGemmSmem, s, maps, p);
-  return launch_pdl_cluster(adapter_gemm_kernel<PAIR, true>,
-                            dim3(static_cast<unsigned>(tiles * p.split)), dim3(kGemmThreads),
-                            kGemmSmem, static_cast<unsigned>(p.split), s, maps, p);
+  if (!p.fused)
+    return launch_pdl_cluster(adapter_gemm_kernel<PAIR, true>,
+                              dim3(static_cast<unsigned>(tiles * p.split)), dim3(kGemmThreads),
+                              kGemmSmem, static_cast<unsigned>(p.split), s, maps, p);
+  return launch_cooperative(adapter_gemm_kernel<PAIR, true>, dim3(static_cast<unsigned>(ctas)),
+                            dim3(kGemmThreads), kGemmSmem, static_cast<unsigned>(p.split), s, maps,
+                            p);
 }
 
 }  // namespace
@@ -793,6 +836,7 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   uint4* u = reinterpret_cast<uint4*>(w + L.u);
   int32_t* blocks = reinterpret_cast<int32_t*>(w + L.blocks);
   int32_t* status = reinterpret_cast<int32_t*>(w);
+  unsigned int* sync = reinterpret_cast<unsigned int*>(w + kWsGridSyncOffset);
   GemmMaps maps;
   bool ok = encode_2d_box(&maps.x, a.x, c.d_in, c.T, kTokBox) &&
             encode_2d_box(&maps.w[0], a.w[0], c.d_in, c.d_out, BW);
@@ -806,39 +850,54 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   cudaError_t e = a.pair ? set_up_gemm<true, true>() : set_up_gemm<false, true>();
   if (e == cudaSuccess) e = a.pair ? set_up_gemm<true, false>() : set_up_gemm<false, false>();
   if (e != cudaSuccess) return e;
-  int split = gemm_split(c, a.pair, sms);
-  {
-    const int nt = a.pair ? kTileTokens<true> : kTileTokens<false>;
-    const int64_t gemm_tiles = static_cast<int64_t>((c.d_out + BW - 1) / BW) * ((c.T + nt - 1) / nt);
-    while (split > 1 && gemm_tiles > (a.pair ? resident_clusters<true>(split)
-                                             : resident_clusters<false>(split)))
-      split /= 2;
+  // (a cluster per tile: all clusters resident at once)
+  int split = gemm_split(c, a.pair, sms), clusters = 0;
+  const int nt = a.pair ? kTileTokens<true> : kTileTokens<false>;
+  const int64_t gemm_tiles = static_cast<int64_t>((c.d_out + BW - 1) / BW) * ((c.T + nt - 1) / nt);
+  for (; split > 1; split /= 2) {
+    clusters = a.pair ? resident_clusters<true>(split) : resident_clusters<false>(split);
+    if (gemm_tiles <= clusters) break;
   }
-  // Deal a tile's adapters over grid.y until the grid covers the SMs twice, and at least over
-  // two: the tile where two requests meet would take twice as long as the others.  In the split
-  // form, whose epilogue adds the pieces up, also cut the contraction (blocks of 32 for every warp).
-  const int deal = std::max(2, std::min(kShrinkTokens, 2 * sms / (tiles * m)));
+  // The split form's GEMM can shrink by itself, its epilogue warps being idle while W streams: worth
+  // it while a CTA has one adapter of a tile to itself at most.  us in one launch / two:
+  // 14336x4096 T=24 32.5 / 39.6, gate/up 4096x8192 T=16 35.8 / 42.6, T=64 46 / 54, but gate/up
+  // 4096x4096 T=96 45.9 / 43.8 and 1024x512 T=200 28.7 / 25.2.
+  const bool fused = split > 1 && tiles * m * kShrinkTokens <= clusters * split;
+  // Deal a tile's adapters over `turns` CTAs until the grid covers the SMs (twice, in a launch of
+  // its own), and at least over two: the tile where two requests meet would take twice as long as
+  // the others.  In the split form, whose epilogue adds the pieces up, also cut the contraction
+  // (blocks of 32 for every warp).
+  const int ctas = fused ? clusters * split : 2 * sms;
+  const int turns = std::max(2, std::min(kShrinkTokens, ctas / (tiles * m)));
   const int parts = split == 1 ? 0
-                               : std::max(1, std::min({kMaxParts, 2 * sms / (tiles * m * deal),
+                               : std::max(1, std::min({kMaxParts, ctas / (tiles * m * turns),
                                                        c.d_in / (32 * kShrinkWarps)}));
   const ShrinkParams sp{static_cast<const bf16*>(a.x),
                         {static_cast<const bf16*>(a.a[0]), static_cast<const bf16*>(a.a[1])},
-                        a.scale, a.ids, a.n_tokens, u, reinterpret_cast<float*>(w + L.u), parts,
-                        blocks, status, c.T, c.d_in, c.n_adapters, c.rank,
-                        pairs ? kPairBlockTokens : a.pair ? kTileTokens<true> : kTileTokens<false>};
-  static DeviceOnce once;
-  e = once.run([] { return prefer_max_shared(adapter_shrink_kernel); });
-  if (e != cudaSuccess) return e;
-  const int blocks_n = (c.T + sp.block_tokens - 1) / sp.block_tokens;
-  adapter_shrink_kernel<<<dim3(tiles + blocks_n, deal, m * std::max(parts, 1)), 32 * kShrinkWarps, 0, s>>>(sp);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+                        a.scale, a.ids, a.n_tokens, u, reinterpret_cast<float*>(w + L.u), turns,
+                        parts, blocks, status, c.T, c.d_in, c.n_adapters, c.rank,
+                        pairs ? kPairBlockTokens : nt};
+  if (!fused) {
+    static DeviceOnce once;
+    e = once.run([] {
+      const cudaError_t r = prefer_max_shared(adapter_shrink_kernel<false>);
+      return r != cudaSuccess ? r : prefer_max_shared(adapter_shrink_kernel<true>);
+    });
+    if (e != cudaSuccess) return e;
+    const dim3 grid(tiles + (c.T + sp.block_tokens - 1) / sp.block_tokens, turns,
+                    m * std::max(parts, 1));
+    if (parts > 0) adapter_shrink_kernel<true><<<grid, 32 * kShrinkWarps, 0, s>>>(sp);
+    else adapter_shrink_kernel<false><<<grid, 32 * kShrinkWarps, 0, s>>>(sp);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
 
   if (pairs) return launch_adapter_pair(c, a, u, blocks, status, s);
   GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u,
                reinterpret_cast<const float*>(w + L.u), parts, blocks, a.ids,
                static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y), a.n_tokens, status,
-               c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, split};
-  return a.pair ? launch_gemm<true>(maps, p, s) : launch_gemm<false>(maps, p, s);
+               c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, split, fused, sp,
+               GridSync{sync, sync + 1}};
+  return a.pair ? launch_gemm<true>(maps, p, ctas, s) : launch_gemm<false>(maps, p, ctas, s);
 }
 
 }  // namespace moe

@@ -187,20 +187,25 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
 }
 
 // A cooperative launch: all CTAs are resident at the same time, so they may wait for each
-// other.
+// other.  `cluster`: CTAs of a cluster, 0 for none.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block,
-                                      size_t smem, cudaStream_t s, Args... args) {
+                                      size_t smem, unsigned cluster, cudaStream_t s,
+                                      Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster != 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -541,7 +541,7 @@ cudaError_t launch_nt(FewParams p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   p.smem_bytes = kSmemBytes;
   return launch_cooperative(few_layer_kernel<Tin, NT>, dim3(sm_count()), dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes,
-                            s, p);
+                            0, s, p);
 }
 
 template <typename Tin>

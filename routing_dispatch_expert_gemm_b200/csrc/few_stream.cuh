@@ -35,6 +35,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "grid_sync.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -210,37 +211,6 @@ __device__ __forceinline__ bool group_all(uint32_t group, bool v) {
 // Where CTA i's share of n rows begins.
 static __device__ __noinline__ int64_t share_begin(int64_t n, uint32_t i) { return n * i / gridDim.x; }
 
-// ---------------------------------------------------------------------------------
-// Grid barrier: counts arrivals in the workspace header (all CTAs are resident).  Both
-// words are zero between launches: the last CTA to leave clears them.
-// ---------------------------------------------------------------------------------
-struct GridSync {
-  unsigned int* count;  // arrivals so far in this launch
-  unsigned int* left;   // CTAs that have left
-};
-
-__device__ __forceinline__ void grid_arrive(const GridSync& g) {  // one thread, after a barrier
-  __threadfence();
-  atomicAdd(g.count, 1u);
-}
-// One thread.  Bounded: returns false (and records MOE_ERR_TIMEOUT) when the arrivals do not come.
-static __device__ __noinline__ bool grid_wait(const GridSync& g, unsigned int target,
-                                          volatile int* abort_flag, int32_t* status) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1;; ++it) {
-    unsigned int v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(g.count) : "memory");
-    if (v >= target) return true;
-    if ((it & 63u) == 0) {
-      if (*abort_flag != 0) return false;
-      if (static_cast<int64_t>(global_timer_ns() - t0) > kWaitLimitNs) {
-        *abort_flag = 1;
-        record_status(status, MOE_ERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
 // The same by several whole warps of a CTA, once per launch: one lane of the `poller` warp polls,
 // the others wait in shared memory (polls of all warps would crowd the arrivals).
 __device__ __forceinline__ bool grid_wait_warps(const GridSync& g, unsigned int target,
@@ -249,13 +219,6 @@ __device__ __forceinline__ bool grid_wait_warps(const GridSync& g, unsigned int 
   if (poller && (threadIdx.x & 31) == 0 && grid_wait(g, target, abort_flag, status))
     mbar_arrive(passed);
   return __all_sync(0xffffffffu, wait(passed, 0, abort_flag, status));
-}
-__device__ __forceinline__ void grid_leave(const GridSync& g) {  // one thread, waits all passed
-  __threadfence();
-  if (atomicAdd(g.left, 1u) == gridDim.x - 1) {
-    *g.count = 0;
-    *g.left = 0;
-  }
 }
 // Make this thread's global writes visible to bulk copies issued by other threads after a
 // barrier (generic proxy -> async proxy), and the reader's counterpart.
