@@ -309,6 +309,8 @@ size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg);
  *               (MOE_ERR_INVALID)
  *   n_tokens    device int32 or NULL: rows 0 .. *n_tokens - 1 hold tokens (clamped to 0..T;
  *               NULL: all T); y's rows behind them are left as they were.
+ * Up to 32 tokens, and some more beside a small W, the kernel waits for all its CTAs, as
+ * moe_forward_few does: the same holds for MOE_ERR_TIMEOUT.
  * A_a x is summed and kept in fp32 or better than 16 bits of it, sums are fp32, y is rounded
  * once.  x, w, a and b must be 16-byte aligned (else MOE_ERR_INVALID).                     */
 moe_status moe_adapter_linear(const moe_adapter_config* cfg, const void* x, const void* w,

@@ -103,14 +103,16 @@ __device__ __forceinline__ float expand(const Tin* b, const float* u, int rank) 
 }
 
 template <typename Tin, int NT, bool PAIR>
-__global__ void __launch_bounds__(kThreads<sizeof(Tin) == 4, NT>, 1) adapter_few_kernel(const AdapterFewParams p) {
+__global__ void __launch_bounds__(kThreads<sizeof(Tin) == 4, NT>, 1)
+    adapter_few_kernel(const AdapterFewParams p) {
   constexpr bool F32 = sizeof(Tin) == 4;
   constexpr int VEC = Vec<Tin>::N;
   constexpr int M = PAIR ? 2 : 1;           // projections
   constexpr int TILE = kTileRows / M;       // output rows of a tile
   extern __shared__ __align__(128) uint8_t smem[];
   const Shared s = carve<NT>(smem, kAdapterTableBytes, p.smem_bytes);
-  AdapterTables& tb = *reinterpret_cast<AdapterTables*>(smem + kCtlBytes + kRedBufs<NT> * kRedFloats<NT> * 4);
+  AdapterTables& tb = *reinterpret_cast<AdapterTables*>(smem + kCtlBytes +
+                                                        kRedBufs<NT> * kRedFloats<NT> * 4);
   const int tid = threadIdx.x, warp = tid >> 5;
 
   init_shared<F32, NT>(s);
@@ -285,8 +287,8 @@ cudaError_t launch_pair(AdapterFewParams p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   p.smem_bytes = kSmemBytes;
-  return launch_cooperative(adapter_few_kernel<Tin, NT, PAIR>, dim3(sm_count()), dim3(kThreads<sizeof(Tin) == 4, NT>),
-                            kSmemBytes, 0, s, p);
+  return launch_cooperative(adapter_few_kernel<Tin, NT, PAIR>, dim3(sm_count()),
+                            dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes, 0, s, p);
 }
 
 template <typename Tin>

@@ -3,10 +3,12 @@
 //   p[t] = W x_t + s_a B_a (A_a x_t),  a = adapter of token t (-1: none)
 //   linear   y[t] = p[t] (+ addend[t])         gate_up  h[t] = SiLU(p_gate[t]) * p_up[t]
 //
-// Two launches, the second starting under the first (programmatic dependent launch):
-//   adapter_shrink_kernel  u[t] = s_a A_a x_t, summed in fp32, kept as two bf16 halves.  A CTA takes 16 consecutive tokens and
-//       runs warp-level MMAs (tokens on M, ranks on N) once per adapter in use among them
-//       (dealt over grid.y when there are few CTAs), its 8 warps splitting the contraction.
+// Two launches, the second starting under the first (programmatic dependent launch); few tokens
+// beside few tiles take one, in which the GEMM's epilogue warps shrink while W streams:
+//   adapter_shrink_kernel  u[t] = s_a A_a x_t, summed in fp32, kept as two bf16 halves.  A CTA takes
+//       16 consecutive tokens and runs warp-level MMAs (tokens on M, ranks on N) once per adapter
+//       in use among them (dealt over CTAs when there are few), its 8 warps splitting the
+//       contraction.
 //       A and x are read straight into MMA fragments (16-byte loads; the k permutation inside
 //       a 32-wide block is the same on both sides).  2 T rank d_in FLOP and the bytes of x and
 //       the A matrices: small beside W's product, and overlapped with its start.
@@ -22,7 +24,7 @@
 // With enough tiles the GEMM is persistent, the epilogue of a tile overlapping the next tile's
 // MMAs (two accumulator sets).  With few tiles (a decode batch on a small projection) a cluster
 // of 2..8 CTAs splits the contraction of one tile; the partial tiles meet in distributed
-// shared memory, where each CTA finishes its share of the tokens in rank order (no atomics,
+// shared memory, where each CTA finishes its share of the tokens in rank order (no float atomics,
 // the same bits every run).
 #include <algorithm>
 
@@ -285,7 +287,8 @@ struct GemmParams {
 // stand for the other adapters' tokens).
 enum Expand { kExpandNone, kExpandAll, kExpandNonFinite };
 
-// Finishes and stores `cnt` tokens from t0 on (row c of each projection).  v[m][i]: row c of projection m for token t0 + i.  One warp; su: its shared memory.
+// Finishes and stores `cnt` tokens from t0 on (row c of each projection).  v[m][i]: row c of
+// projection m for token t0 + i.  One warp; su: its shared memory.
 template <bool PAIR>
 __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PAIR ? 2 : 1][kChunk],
                                               int t0, int cnt, int c, Expand expand, float* su) {
@@ -455,7 +458,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int k_all = (p.d_in + BK - 1) / BK;
   const int k_lo = k_all * rank / split, k_hi = k_all * (rank + 1) / split;
   // K blocks that the adapters of a token block add per projection; 0: the epilogue adds them,
-  // or there are none (then it has nothing to add).  Written by the shrink kernel: after pdl_wait only.
+  // or there are none (then it has nothing to add).  Written by the shrink kernel: after pdl_wait
+  // only.
   const int units_per = p.rank / 8 * 2;  // 8-rank units of an adapter, high and low
   auto ext_blocks = [&](int tb) {
     if (SPLIT) return 0;
@@ -763,7 +767,8 @@ int resident_clusters(int size) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, adapter_gemm_kernel<PAIR, SPLIT>, &cfg) != cudaSuccess) n = -1;
+    if (cudaOccupancyMaxActiveClusters(&n, adapter_gemm_kernel<PAIR, SPLIT>, &cfg) != cudaSuccess)
+      n = -1;
     slot.store(n > 0 ? n : -1, std::memory_order_relaxed);
   }
   return n;
@@ -814,6 +819,10 @@ static int gemm_split(const moe_adapter_config& c, bool pair, int sms) {
   int split = 1;
   while (split < 8 && tiles * split * 2 <= sms && split * 2 <= k_blocks) split *= 2;
   return split;
+}
+
+bool adapter_splits(const moe_adapter_config& c, bool pair) {
+  return gemm_split(c, pair, sm_count()) > 1;
 }
 
 size_t adapter_u_bytes(const moe_adapter_config& c) {

@@ -170,16 +170,20 @@ moe_status validate_adapter(const moe_adapter_config* c) {
 }
 
 // Whether the streaming kernel runs a call of at most 32 tokens.  It reads the token rows once per
-// CTA, so many tokens beside a large W are better off on tcgen05, whose fixed costs (a second
-// launch, the cluster) are 5 to 20 us.  Measured, rank 16, us streaming / tcgen05:
-//   linear  2048x2048 T=32 17 / 28;   4096x4096 T=16 20 / 20, T=24 25 / 21;
-//   linear  4096x8192 T=12 26 / 25;   14336x4096 T=8 36 / 37, T=24 61 / 39;
-//   gate/up 4096x4096 T=16 31 / 33, T=24 41 / 33;   4096x8192 T=8 40 / 43, T=16 53 / 45.
+// CTA, so more than 8 tokens beside a large W are better off on tcgen05, and up to 8 a large pair whose
+// GEMM splits the contraction and shrinks in the same launch.  Measured, rank 16, us
+// streaming / tcgen05:
+//   linear  2048x2048 T=16 13 / 15, T=32 18 / 16;  1024x8192 T=16 16 / 16, T=24 20 / 17;
+//   linear  4096x4096 T=8 15 / 18, T=16 21 / 18;  14336x4096 T=8 31 / 31, T=12 43 / 31;
+//   linear  8192x28672 T=8 91 / 108, T=12 112 / 99;
+//   gate/up 4096x4096 T=8 23 / 25, T=12 28 / 25;  4096x8192 T=4 35 / 34, T=8 40 / 35;
+//   gate/up 4096x14336 (not split) T=8 61 / 69, T=12 70 / 53.
 bool adapter_streams(const moe_adapter_config& c, bool pair) {
   if (c.T > 32) return false;
-  if (c.T <= 8 || c.dtype == MOE_F32) return true;
+  if (c.T <= 4 || c.dtype == MOE_F32) return true;
   const int64_t weights = static_cast<int64_t>(c.d_in) * c.d_out * (pair ? 2 : 1);
-  return weights <= (int64_t{12} << 20) || (c.T <= 16 && weights <= (int64_t{32} << 20));
+  if (c.T <= 8) return weights <= (int64_t{60} << 20) || !adapter_splits(c, pair);
+  return weights <= (int64_t{c.T <= 16 ? 12 : 6} << 20);
 }
 
 AdapterLayout adapter_layout(const moe_adapter_config& c) {

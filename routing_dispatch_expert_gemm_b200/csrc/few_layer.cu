@@ -321,7 +321,8 @@ struct DownPos {
 };
 
 template <typename Tin, int NT>
-__global__ void __launch_bounds__(kThreads<sizeof(Tin) == 4, NT>, 1) few_layer_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kThreads<sizeof(Tin) == 4, NT>, 1)
+    few_layer_kernel(const FewParams p) {
   constexpr bool F32 = sizeof(Tin) == 4;
   constexpr int VEC = Vec<Tin>::N;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -540,8 +541,8 @@ cudaError_t launch_nt(FewParams p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   p.smem_bytes = kSmemBytes;
-  return launch_cooperative(few_layer_kernel<Tin, NT>, dim3(sm_count()), dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes,
-                            0, s, p);
+  return launch_cooperative(few_layer_kernel<Tin, NT>, dim3(sm_count()),
+                            dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes, 0, s, p);
 }
 
 template <typename Tin>
@@ -565,7 +566,8 @@ FewLayout few_layer_layout(const moe_config& c) {
 
 bool few_layer_supported(const moe_config& c) {
   return c.T <= kMaxTokens && c.d <= (1 << 24) && c.d_ff <= (1 << 24) &&
-         (c.E + 1) * static_cast<int64_t>(c.d_ff) <= INT_MAX && !c.stats && c.layout == MOE_LAYOUT_RAGGED &&
+         (c.E + 1) * static_cast<int64_t>(c.d_ff) <= INT_MAX && !c.stats &&
+         c.layout == MOE_LAYOUT_RAGGED &&
          c.overflow == MOE_OVERFLOW_DROP && c.fuse == MOE_FUSE_NONE;
 }
 

@@ -167,8 +167,8 @@ __device__ __forceinline__ void init_shared(const Shared& s) {
 // The engine's waits: one inlined try, the bounded loop out of line.  These kernels run once per
 // layer from a cold instruction cache, where code size is latency: inlined everywhere the
 // kernels were 175 KB.
-static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                       int32_t* status) {
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity,
+                                              volatile int* abort_flag, int32_t* status) {
   return mbar_wait_bounded(bar, parity, abort_flag, kWaitLimitNs, status);
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
@@ -209,7 +209,9 @@ __device__ __forceinline__ bool group_all(uint32_t group, bool v) {
 }
 
 // Where CTA i's share of n rows begins.
-static __device__ __noinline__ int64_t share_begin(int64_t n, uint32_t i) { return n * i / gridDim.x; }
+static __device__ __noinline__ int64_t share_begin(int64_t n, uint32_t i) {
+  return n * i / gridDim.x;
+}
 
 // The same by several whole warps of a CTA, once per launch: one lane of the `poller` warp polls,
 // the others wait in shared memory (polls of all warps would crowd the arrivals).
@@ -412,10 +414,10 @@ template <int NT> struct Acc<false, NT> {
     const uint32_t at = (part * 4 + q) * 16;
     // 16-row blocks: rows past a block's last one are clamped to it
     // (a pair tile of up to 8 rows each: one block, see pair_fold)
+    const int up = d.r0 + min(g, d.r1 - 1);
     uint32_t a[4] = {base + min(g, d.r0 - 1) * P + at,
-                           base + (pair_fold(d) ? d.r0 + min(g, d.r1 - 1) : min(g + 8, d.r0 - 1)) * P + at,
-                           base + (d.r0 + min(g, d.r1 - 1)) * P + at,
-                           base + (d.r0 + min(g + 8, d.r1 - 1)) * P + at};
+                     base + (pair_fold(d) ? up : min(g + 8, d.r0 - 1)) * P + at, base + up * P + at,
+                     base + (d.r0 + min(g + 8, d.r1 - 1)) * P + at};
     const int nb = __popc(d.mask);
     uint32_t b[NB], step[NB];
 #pragma unroll
@@ -610,7 +612,8 @@ struct Crew {
 // itself while the others are at other tiles: shared by all groups, a tile of two slots costs the
 // latency of both barriers and of the epilogue each time (32 experts, d=512, F=4096 T=16: 144 us
 // shared, 121 us by one group; Granite-shaped T=16 42.9 and 41.9).  Not in fp32, whose FMAs take
-// longer than those barriers (12+1 experts T=4: 80 us shared, 98 us by one group).  With more slots to a tile the ring would hold slots of one group's tile only.
+// longer than those barriers (12+1 experts T=4: 80 us shared, 98 us by one group).  With more
+// slots to a tile the ring would hold slots of one group's tile only.
 //   No group waits for use n + 1 of a slot's barrier before use n has completed: when it
 // waits for slots of its next tile, at most kGroups tiles on, the slots up to kInFlight before
 // the tile it finished have been filled.

@@ -211,12 +211,14 @@ struct AdapterLayout {
   size_t blocks;  // of the adapters per GEMM token block (adapter_sm100.cu)
   size_t total;   // bytes in all
 };
-// bf16, any T: shrink launch + tcgen05 GEMM.
+// bf16, any T: tcgen05 GEMM, the shrink in a launch before it or in the same.
 // Bytes of its u, and of its table of adapters per token block.
 size_t adapter_u_bytes(const moe_adapter_config& c);
 size_t adapter_block_table_bytes(int T);
 cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs& a,
                                  const AdapterLayout& L, void* ws, cudaStream_t s);
+// Whether its GEMM splits the contraction of a tile over CTAs.
+bool adapter_splits(const moe_adapter_config& c, bool pair);
 // fp32, any T: shrink launch + CUDA-core GEMM.
 cudaError_t launch_adapter_simt(const moe_adapter_config& c, const AdapterArgs& a,
                                 const AdapterLayout& L, void* ws, cudaStream_t s);

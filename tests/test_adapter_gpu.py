@@ -359,3 +359,68 @@ def test_broken_rows_of_rare_adapters(N):
     want, bound = reference(q, False)
     assert bool(((y[:, 256:].double() - want).abs() <= bound).all())
     assert bool(torch.isfinite(y[100:]).all())
+
+
+@pytest.mark.parametrize("pair", [False, True], ids=["linear", "gate_up"])
+def test_calls_on_two_streams_at_once(N, pair):
+    """Calls whose kernels wait for all of their CTAs, on two streams, each with its own
+    workspace: the same bits as one after the other."""
+    shapes = [(3, 512, 1024), (24, 2048, 4096), (40, 4096, 512), (100, 512, 512)]
+    ps = [make(T, d_in, d_out, 6, 16, seed=T) for T, d_in, d_out in shapes]
+    want = [call(N, p, pair) for p in ps]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for rep in range(6):
+        for i, p in enumerate(ps):
+            for s in streams:
+                with torch.cuda.stream(s):
+                    T, d_in, d_out = shapes[i]
+                    cfg = N.make_adapter_config(T, d_in, d_out, 6, 16)
+                    ws = N.adapter_workspace(cfg)
+                    y = torch.zeros((T, d_out), dtype=torch.bfloat16, device="cuda")
+                    if pair:
+                        N.moe_adapter_gate_up(cfg, p["x"], p["w"][0], p["w"][1], p["a"][0],
+                                              p["b"][0], p["a"][1], p["b"][1], p["scale"],
+                                              p["ids"], y, None, ws)
+                    else:
+                        N.moe_adapter_linear(cfg, p["x"], p["w"][0], p["a"][0], p["b"][0],
+                                             p["scale"], p["ids"], None, y, None, ws)
+                    got.append((i, y, ws))
+    torch.cuda.synchronize()
+    for i, y, ws in got:
+        assert torch.equal(y, want[i]) and N.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,d_in,d_out,n,mix", [
+    (16, 4096, 8192, 16, "tokens"), (24, 14336, 264, 64, "tokens"), (33, 1032, 520, 40, "tokens"),
+    (64, 1024, 1024, 64, "tokens"), (64, 4104, 136, 3, "requests"), (128, 520, 264, 9, "one"),
+    (12, 16384, 4096, 5, "none"), (129, 2048, 256, 129, "tokens")])
+def test_shrink_inside_the_gemm(N, T, d_in, d_out, n, mix):
+    """Shapes whose GEMM splits the contraction, around the sizes where it shrinks by itself;
+    the same workspace again and again, with other counts of tokens, eagerly and from a graph."""
+    p = make(T, d_in, d_out, n, 16, mix=mix, seed=5)
+    cfg = N.make_adapter_config(T, d_in, d_out, n, 16)
+    ws = N.adapter_workspace(cfg)
+    for pair in (False, True):
+        ref = reference(p, pair)
+        check(call(N, p, pair, ws=ws), ref, T)
+        for live in (0, 1, T // 2 + 1):
+            check(call(N, p, pair, n_tokens=live, ws=ws), ref, live)
+        y = torch.full((T, d_out), 7.0, dtype=torch.bfloat16, device="cuda")
+        count = torch.tensor([T], dtype=torch.int32, device="cuda")
+        args = ((p["w"][0], p["w"][1], p["a"][0], p["b"][0], p["a"][1], p["b"][1]) if pair else
+                (p["w"][0], p["a"][0], p["b"][0]))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if pair:
+                N.moe_adapter_gate_up(cfg, p["x"], *args, p["scale"], p["ids"], y, count, ws)
+            else:
+                N.moe_adapter_linear(cfg, p["x"], *args, p["scale"], p["ids"], None, y, count, ws)
+        for live in (T, 2, T - 1):
+            y.fill_(7.0)
+            count.fill_(live)
+            g.replay()
+            check(y, ref, live)
+        assert N.moe_get_device_status(ws) == 0
