@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = !PAIR || m == static_cast<int>(rank);
         const int row0 = PAIR ? cb * OUT : cb * BN + static_cast<int>(rank) * (BN / 2);
         const __nv_bfloat16* b =
-            p.b[m] + static_cast<size_t>(max(id, 0)) * p.d_out * p.rank + g8 * 8;
+            (m == 0 ? p.b[0] : p.b[M - 1]) +
+            static_cast<size_t>(max(id, 0)) * p.d_out * p.rank + g8 * 8;
 #pragma unroll 4
         for (int r = et >> 3; r < BN / 2; r += 8)
           cp_async_16_zfill(extB + r * 128 + ((j ^ (r & 7)) << 4),

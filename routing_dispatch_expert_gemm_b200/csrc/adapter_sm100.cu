@@ -167,7 +167,8 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, ShrinkSums& r
     const int lead = __ffs(leaders) - 1;
     const int a_id = __shfl_sync(0xffffffffu, id, lead);
     const uint32_t tokens = __shfl_sync(0xffffffffu, same, lead);
-    const __nv_bfloat16* A = p.a[m] + static_cast<size_t>(a_id) * p.rank * p.d_in;
+    const __nv_bfloat16* A =  // (an index into p.a would put p on the stack)
+        (m == 0 ? p.a[0] : p.a[1]) + static_cast<size_t>(a_id) * p.rank * p.d_in;
     const float sc = p.scale != nullptr ? __ldg(p.scale + a_id) : 1.f;
     for (int j0 = 0; j0 < p.rank; j0 += kShrinkRanks) {
       const int nb = min(4, (p.rank - j0) / 8);  // rank is a multiple of 8
@@ -277,8 +278,7 @@ struct GemmParams {
   int32_t* status;
   int T, d_in, d_out, n, rank;
   int row_blocks, tok_blocks, boxes, stages, split;  // split: CTAs of a cluster per tile
-  int fused;            // with a cluster per tile: the shrink is in this kernel
-  ShrinkParams shrink;
+  ShrinkParams shrink;  // with the shrink in this kernel
   GridSync sync;
 };
 
@@ -393,8 +393,9 @@ __device__ __forceinline__ void gather_partials(const float* part, int cnt, floa
   }
 }
 
-// SPLIT (a cluster per tile) is a template argument for the code's size: see kChunk.
-template <bool PAIR, bool SPLIT>
+// SPLIT: a cluster per tile.  FUSED: the shrink is in this kernel.  Template arguments for the
+// code's size: see kChunk.
+template <bool PAIR, bool SPLIT, bool FUSED>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     adapter_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams p) {
   constexpr int M = PAIR ? 2 : 1;
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
     }
-    if (SPLIT && p.fused) {
+    if constexpr (FUSED) {
       // the shrink, over all CTAs of the grid, while W streams
       ShrinkSums& red = *reinterpret_cast<ShrinkSums*>(su_all);
       const int turns = p.shrink.turns, parts = p.shrink.parts;
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   }
   if constexpr (SPLIT) {  // one tile per cluster
-    if (p.fused && threadIdx.x == 0 && first_tile < total)  // u is complete
+    if (FUSED && threadIdx.x == 0 && first_tile < total)  // u is complete
       grid_wait(p.sync, gridDim.x, abort_flag, p.status);
     __syncwarp();
     cluster_sync_all();
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem_base, 2 * ACC_COLS);
-  if (SPLIT && p.fused && threadIdx.x == 0 && *abort_flag == 0) grid_leave(p.sync);
+  if (FUSED && threadIdx.x == 0 && *abort_flag == 0) grid_leave(p.sync);
 }
 
 // Clusters of `size` CTAs of the GEMM that the current device holds at once: fewer than its SMs
@@ -749,7 +750,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // of clusters doubled a 2048x2048 call.
 template <bool PAIR>
 int resident_clusters(int size) {
-  constexpr bool SPLIT = true;
   static std::atomic<int> known[64][4];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -767,25 +767,33 @@ int resident_clusters(int size) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, adapter_gemm_kernel<PAIR, SPLIT>, &cfg) != cudaSuccess)
+    if (cudaOccupancyMaxActiveClusters(&n, adapter_gemm_kernel<PAIR, true, true>, &cfg) != cudaSuccess)
       n = -1;
     slot.store(n > 0 ? n : -1, std::memory_order_relaxed);
   }
   return n;
 }
 
-template <bool PAIR, bool SPLIT>
+template <bool PAIR, bool SPLIT, bool FUSED>
 cudaError_t set_up_gemm() {
   static DeviceOnce once;
   return once.run([] {
-    cudaError_t r = cudaFuncSetAttribute(adapter_gemm_kernel<PAIR, SPLIT>,
+    cudaError_t r = cudaFuncSetAttribute(adapter_gemm_kernel<PAIR, SPLIT, FUSED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-    return r != cudaSuccess ? r : prefer_max_shared(adapter_gemm_kernel<PAIR, SPLIT>);
+    return r != cudaSuccess ? r : prefer_max_shared(adapter_gemm_kernel<PAIR, SPLIT, FUSED>);
   });
 }
 
 template <bool PAIR>
-cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, int ctas, cudaStream_t s) {
+cudaError_t set_up_gemms() {
+  cudaError_t e = set_up_gemm<PAIR, true, true>();
+  if (e == cudaSuccess) e = set_up_gemm<PAIR, true, false>();
+  return e == cudaSuccess ? set_up_gemm<PAIR, false, false>() : e;
+}
+
+template <bool PAIR>
+cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, bool fused, int ctas,
+                        cudaStream_t s) {
   constexpr int NT = kTileTokens<PAIR>;
   const int sms = sm_count();
   p.row_blocks = (p.d_out + BW - 1) / BW;
@@ -793,17 +801,18 @@ cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, int ctas, cudaStream
   p.boxes = std::min(NT / kTokBox, (p.T + kTokBox - 1) / kTokBox);
   p.stages = std::min(kMaxStages, kRingBytes / ((PAIR ? 2 : 1) * W_BYTES + p.boxes * kBoxBytes));
   const int64_t tiles = static_cast<int64_t>(p.row_blocks) * p.tok_blocks;
-  if (p.split == 1)
-    return launch_pdl(adapter_gemm_kernel<PAIR, false>, dim3(static_cast<unsigned>(std::min<int64_t>(
-                                                     tiles, sms))),
-                      dim3(kGemmThreads), kGemmSmem, s, maps, p);
-  if (!p.fused)
-    return launch_pdl_cluster(adapter_gemm_kernel<PAIR, true>,
-                              dim3(static_cast<unsigned>(tiles * p.split)), dim3(kGemmThreads),
-                              kGemmSmem, static_cast<unsigned>(p.split), s, maps, p);
-  return launch_cooperative(adapter_gemm_kernel<PAIR, true>, dim3(static_cast<unsigned>(ctas)),
-                            dim3(kGemmThreads), kGemmSmem, static_cast<unsigned>(p.split), s, maps,
-                            p);
+  const dim3 block(kGemmThreads);
+  const unsigned split = static_cast<unsigned>(p.split);
+  if (split == 1)
+    return launch_pdl(adapter_gemm_kernel<PAIR, false, false>,
+                      dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sms))), block, kGemmSmem,
+                      s, maps, p);
+  if (!fused)
+    return launch_pdl_cluster(adapter_gemm_kernel<PAIR, true, false>,
+                              dim3(static_cast<unsigned>(tiles) * split), block, kGemmSmem, split, s,
+                              maps, p);
+  return launch_cooperative(adapter_gemm_kernel<PAIR, true, true>, dim3(ctas), block, kGemmSmem,
+                            split, s, maps, p);
 }
 
 }  // namespace
@@ -856,8 +865,7 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   const bool pairs = adapter_pair_fits(c, a.pair);
   const int sms = sm_count();
   const int tiles = (c.T + kShrinkTokens - 1) / kShrinkTokens, m = a.pair ? 2 : 1;
-  cudaError_t e = a.pair ? set_up_gemm<true, true>() : set_up_gemm<false, true>();
-  if (e == cudaSuccess) e = a.pair ? set_up_gemm<true, false>() : set_up_gemm<false, false>();
+  cudaError_t e = a.pair ? set_up_gemms<true>() : set_up_gemms<false>();
   if (e != cudaSuccess) return e;
   // (a cluster per tile: all clusters resident at once)
   int split = gemm_split(c, a.pair, sms), clusters = 0;
@@ -904,9 +912,10 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u,
                reinterpret_cast<const float*>(w + L.u), parts, blocks, a.ids,
                static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y), a.n_tokens, status,
-               c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, split, fused, sp,
+               c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, split, sp,
                GridSync{sync, sync + 1}};
-  return a.pair ? launch_gemm<true>(maps, p, ctas, s) : launch_gemm<false>(maps, p, ctas, s);
+  return a.pair ? launch_gemm<true>(maps, p, fused, ctas, s)
+                : launch_gemm<false>(maps, p, fused, ctas, s);
 }
 
 }  // namespace moe
