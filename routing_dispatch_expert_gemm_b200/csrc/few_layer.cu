@@ -77,7 +77,10 @@ struct Tables {
 // Cost of a gate/up row pair with nb tokens: two weight rows and, per 16 pairs, nb token rows
 // through the same copies and shared memory, and their MMAs.  Measured on skewed experts (T=32,
 // 1 to 30 tokens each): at 32 + nb the CTAs of the fullest expert took 497 us, the others 305.
-__device__ __forceinline__ int pair_cost(int nb) { return 32 + 2 * nb; }
+// In fp32 a token costs twice that (12+1 experts, d=776, F=4812, T=16: 290 us at 2, 258 at 4, 269
+// at 8).
+template <bool F32>
+__device__ __forceinline__ int pair_cost(int nb) { return 32 + (F32 ? 4 : 2) * nb; }
 
 constexpr uint32_t kTableBytes = (sizeof(Tables) + 15) & ~15u;
 // Only while the tables are built: in the ring, which is still empty.
@@ -217,6 +220,7 @@ __device__ __forceinline__ void select_tokens(const FewParams& p, Tables& tb, Ch
 }
 
 // The tables, by the consumer threads.
+template <bool F32>
 __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Choice& ch, int live) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e <= p.E; e += kConsumers) tb.mask[e] = 0;
@@ -233,7 +237,7 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
       if (blockIdx.x == 0 && e < p.E && p.demand_out != nullptr) p.demand_out[e] = __popc(m);
       if (p.capacity >= 0)  // arrival order is token order: the lowest C tokens stay
         while (__popc(m) > p.capacity) m &= ~(0x80000000u >> __clz(m));
-      const int n = __popc(m), w = n > 0 ? pair_cost(n) : 0;
+      const int n = __popc(m), w = n > 0 ? pair_cost<F32>(n) : 0;
       int incl = n, cincl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -267,7 +271,7 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
         tb.seg_mask[nseg] = live == 32 ? 0xffffffffu : (1u << live) - 1u;
         tb.seg_hrow[nseg] = static_cast<int16_t>(rows);
         tb.cost[nseg] = cost;
-        cost += pair_cost(live);
+        cost += pair_cost<F32>(live);
         most = live;
         ++nseg;
       }
@@ -293,7 +297,7 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
     for (int s = tid >> 1; s < tb.nseg; s += kConsumers / 2) {
       const int64_t a = static_cast<int64_t>(tb.cost[s]) * p.F;
       const int w = tb.cost[s + 1] - tb.cost[s];
-      if (at >= a && at < a + static_cast<int64_t>(w) * p.F)  // F <= 2^24, w < 2^7
+      if (at >= a && at < a + static_cast<int64_t>(w) * p.F)  // F <= 2^24, w < 2^8
         (end ? tb.hi : tb.lo) = s * p.F + static_cast<int>(static_cast<uint32_t>(at - a) / w);
     }
   }
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads<sizeof(Tin) == 4, NT>, 1)
     }
     consumer_sync();
     ok = *s.abort_flag == 0;  // written before the barrier: the same for all
-    if (ok) build_tables(p, tb, *reinterpret_cast<Choice*>(s.ring), live);
+    if (ok) build_tables<F32>(p, tb, *reinterpret_cast<Choice*>(s.ring), live);
     else if (tid == 0) tb.nseg = tb.c0 = tb.c1 = 0;
     fence_proxy_async_smem();  // Choice lies where bulk copies now write
   }
