@@ -272,8 +272,8 @@ moe_status moe_forward(const moe_config* cfg, const void* x, const void* w_route
  * The kernel occupies every SM (a cooperative launch) and can be captured into a graph.  If
  * it ever reports MOE_ERR_TIMEOUT, clear the status (moe_get_device_status) or call
  * moe_workspace_init before the workspace's next use.  Up to 8 tokens it is faster than
- * moe_forward, up to 16 as fast or faster, beyond that slower on large experts: it reads the
- * token rows once per CTA.
+ * moe_forward, up to 16 mostly, beyond that slower on large experts: it reads the token rows
+ * once per CTA.
  * Source: "271,104 Routes...", section 5 (with small batches the cost is moving weights). */
 moe_status moe_forward_few(const moe_config* cfg, const void* x, const void* w_router,
                            const float* logit_bias, const void* w_gate, const void* w_up,
@@ -309,8 +309,8 @@ size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg);
  *               (MOE_ERR_INVALID)
  *   n_tokens    device int32 or NULL: rows 0 .. *n_tokens - 1 hold tokens (clamped to 0..T;
  *               NULL: all T); y's rows behind them are left as they were.
- * Up to 32 tokens, and some more beside a small W, the kernel waits for all its CTAs, as
- * moe_forward_few does: the same holds for MOE_ERR_TIMEOUT.
+ * With few tokens the kernel's CTAs wait for each other, as moe_forward_few's do: the same holds
+ * for MOE_ERR_TIMEOUT.
  * A_a x is summed and kept in fp32 or better than 16 bits of it, sums are fp32, y is rounded
  * once.  x, w, a and b must be 16-byte aligned (else MOE_ERR_INVALID).                     */
 moe_status moe_adapter_linear(const moe_adapter_config* cfg, const void* x, const void* w,

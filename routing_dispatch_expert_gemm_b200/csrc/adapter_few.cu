@@ -288,7 +288,7 @@ cudaError_t launch_pair(AdapterFewParams p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   p.smem_bytes = kSmemBytes;
   return launch_cooperative(adapter_few_kernel<Tin, NT, PAIR>, dim3(sm_count()),
-                            dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes, 0, s, p);
+                            dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes, s, p);
 }
 
 template <typename Tin>
@@ -308,7 +308,7 @@ cudaError_t launch_adapter_few(const moe_adapter_config& c, const AdapterArgs& a
   const AdapterFewParams p{a.x, {a.w[0], a.w[1]}, {a.a[0], a.a[1]}, {a.b[0], a.b[1]}, a.scale,
                            a.ids, a.addend, a.y, a.n_tokens,
                            reinterpret_cast<float*>(w + L.u), reinterpret_cast<int32_t*>(w),
-                           GridSync{sync, sync + 1}, c.T, c.d_in, c.d_out, c.n_adapters, c.rank,
+                           GridSync{sync, sync + 1, sync + 2}, c.T, c.d_in, c.d_out, c.n_adapters, c.rank,
                            0};
   return c.dtype == MOE_BF16 ? launch_typed<__nv_bfloat16>(p, a.pair, s)
                              : launch_typed<float>(p, a.pair, s);

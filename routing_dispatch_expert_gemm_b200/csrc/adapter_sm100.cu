@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // per tile of this CTA, modulo kFlags: its K blocks of adapters met a non-finite element of B
   // (the ext warps run at most kMaxStages tiles ahead of the epilogue's two)
   volatile int* nonfinite = abort_flag + 1;
+  volatile int* ticket = nonfinite + kFlags;  // [2] FUSED: this CTA's pieces of the shrink
   int* s_ids = reinterpret_cast<int*>(ctl + 512);  // the ext warps': adapters of their tile's tokens
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -437,6 +438,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if constexpr (FUSED) ticket[0] = static_cast<int>(atomicAdd(p.sync.ticket, 1u));
   }
   if (warp == kProducerWarp && lane == 0) {
     tma_prefetch_desc(&maps.x);
@@ -458,6 +460,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int total = p.row_blocks * tok_blocks;
   const int k_all = (p.d_in + BK - 1) / BK;
   const int k_lo = k_all * rank / split, k_hi = k_all * (rank + 1) / split;
+  const int shrink_items = FUSED ? (live + kShrinkTokens - 1) / kShrinkTokens *
+                                       (p.shrink.turns * M * p.shrink.parts) : 0;
   // K blocks that the adapters of a token block add per projection; 0: the epilogue adds them,
   // or there are none (then it has nothing to add).  Written by the shrink kernel: after pdl_wait
   // only.
@@ -651,17 +655,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     }
     if constexpr (FUSED) {
-      // the shrink, over all CTAs of the grid, while W streams
+      // the shrink, over all CTAs that run, while W streams
       ShrinkSums& red = *reinterpret_cast<ShrinkSums*>(su_all);
       const int turns = p.shrink.turns, parts = p.shrink.parts;
-      const int items = (live + kShrinkTokens - 1) / kShrinkTokens * (turns * M * parts);
+      int done = 0;
 #pragma unroll 1
-      for (int i = blockIdx.x; i < items; i += gridDim.x) {
+      for (int i = ticket[0]; i < shrink_items; i = ticket[done & 1]) {
+        int next = 0;  // its latency passes under the piece's work
+        if (threadIdx.x == 0) next = static_cast<int>(atomicAdd(p.sync.ticket, 1u));
         const int part = i % parts, m = i / parts % M, turn = i / (parts * M) % turns;
         shrink_tile<true>(p.shrink, red, i / (parts * M * turns), turn, m, part, live);
+        ++done;
+        if (threadIdx.x == 0) ticket[done & 1] = next;
+        shrink_sync();
       }
-      shrink_sync();
-      if (threadIdx.x == 0) grid_arrive(p.sync);
+      if (threadIdx.x == 0 && done > 0) grid_arrive(p.sync, done);
     }
     pdl_wait();  // u is complete; what read y before this call is done
     for (int tile = first_tile, iter = 0; tile < total; tile += tile_step, ++iter) {
@@ -709,7 +717,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   if constexpr (SPLIT) {  // one tile per cluster
     if (FUSED && threadIdx.x == 0 && first_tile < total)  // u is complete
-      grid_wait(p.sync, gridDim.x, abort_flag, p.status);
+      grid_wait(p.sync, shrink_items, abort_flag, p.status);
     __syncwarp();
     cluster_sync_all();
     if (warp < kEpiWarps && first_tile < total && *abort_flag == 0) {
@@ -811,8 +819,8 @@ cudaError_t launch_gemm(const GemmMaps& maps, GemmParams p, bool fused, int ctas
     return launch_pdl_cluster(adapter_gemm_kernel<PAIR, true, false>,
                               dim3(static_cast<unsigned>(tiles) * split), block, kGemmSmem, split, s,
                               maps, p);
-  return launch_cooperative(adapter_gemm_kernel<PAIR, true, true>, dim3(ctas), block, kGemmSmem,
-                            split, s, maps, p);
+  return launch_cluster(adapter_gemm_kernel<PAIR, true, true>, dim3(ctas), block, kGemmSmem,
+                        split, s, maps, p);
 }
 
 }  // namespace
@@ -913,7 +921,7 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
                reinterpret_cast<const float*>(w + L.u), parts, blocks, a.ids,
                static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y), a.n_tokens, status,
                c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, split, sp,
-               GridSync{sync, sync + 1}};
+               GridSync{sync, sync + 1, sync + 2}};
   return a.pair ? launch_gemm<true>(maps, p, fused, ctas, s)
                 : launch_gemm<false>(maps, p, fused, ctas, s);
 }

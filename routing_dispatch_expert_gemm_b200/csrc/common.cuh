@@ -22,7 +22,8 @@ constexpr size_t kWsStatsCounterOffset = 64;
 // Byte offset, in the header, of the ticket counter of the dispatch prep (the CTA that
 // writes the last tile of the expert histogram turns it into prefixes and offsets).
 constexpr size_t kWsPrepCounterOffset = 128;
-// Byte offset, in the header, of the two words of the few-token kernels' grid barrier.
+// Byte offset, in the header, of the three words of the kernels whose CTAs wait for each other
+// (grid_sync.cuh).
 constexpr size_t kWsGridSyncOffset = 192;
 
 // A route (t, j) is valid if its expert id is in range and not repeated earlier in the
@@ -187,25 +188,39 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
 }
 
 // A cooperative launch: all CTAs are resident at the same time, so they may wait for each
-// other.  `cluster`: CTAs of a cluster, 0 for none.
+// other.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block,
-                                      size_t smem, unsigned cluster, cudaStream_t s,
-                                      Args... args) {
+                                      size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster != 0 ? 2 : 1;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Clusters of `cluster_x` CTAs along x, after everything before in the stream.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                  unsigned cluster_x, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster_x;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

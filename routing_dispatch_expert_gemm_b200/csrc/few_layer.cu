@@ -546,7 +546,7 @@ cudaError_t launch_nt(FewParams p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   p.smem_bytes = kSmemBytes;
   return launch_cooperative(few_layer_kernel<Tin, NT>, dim3(sm_count()),
-                            dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes, 0, s, p);
+                            dim3(kThreads<sizeof(Tin) == 4, NT>), kSmemBytes, s, p);
 }
 
 template <typename Tin>
@@ -582,7 +582,7 @@ cudaError_t launch_few_layer(const moe_config& c, const FewArgs& a, void* ws, cu
   FewParams p{a.x, a.w_router, a.bias, a.w_gate, a.w_up, a.w_down, a.s_gate, a.s_up, a.s_down,
               a.y, a.ids, a.gates, a.demand, a.offsets, a.n_tokens,
               reinterpret_cast<float*>(w + L.logits), w + L.h,
-              reinterpret_cast<int32_t*>(w), GridSync{sync, sync + 1},
+              reinterpret_cast<int32_t*>(w), GridSync{sync, sync + 1, sync + 2},
               c.T, c.d, c.E, c.k, c.d_ff, c.gate_mode, c.capacity, c.has_shared,
               c.add_residual, 0};
   return c.dtype == MOE_BF16 ? launch_typed<__nv_bfloat16>(p, s) : launch_typed<float>(p, s);

@@ -1,4 +1,6 @@
-// Grid barrier of the kernels whose CTAs are all resident (cooperative launches).
+// What the CTAs of a grid wait for each other with.  Either all CTAs are resident (a cooperative
+// launch) and arrive once each, or the work waited for is handed out by tickets: a CTA waits only
+// once all tickets are taken, so by CTAs that run and, before they wait themselves, finish it.
 #pragma once
 
 #include "common.cuh"
@@ -6,16 +8,17 @@
 
 namespace moe {
 
-// Grid barrier: counts arrivals in the workspace header (all CTAs are resident).  Both
-// words are zero between launches: the last CTA to leave clears them.
+// Words in the workspace header, zero between launches: the last CTA to leave clears them.
 struct GridSync {
-  unsigned int* count;  // arrivals so far in this launch
-  unsigned int* left;   // CTAs that have left
+  unsigned int* count;   // arrivals, or finished tickets, so far in this launch
+  unsigned int* left;    // CTAs that have left
+  unsigned int* ticket;  // next ticket
 };
 
-__device__ __forceinline__ void grid_arrive(const GridSync& g) {  // one thread, after a barrier
+// One thread, after a barrier.
+__device__ __forceinline__ void grid_arrive(const GridSync& g, unsigned int n = 1u) {
   __threadfence();
-  atomicAdd(g.count, 1u);
+  atomicAdd(g.count, n);
 }
 // One thread.  Bounded: returns false (and records MOE_ERR_TIMEOUT) when the arrivals do not come.
 static __device__ __noinline__ bool grid_wait(const GridSync& g, unsigned int target,
@@ -40,6 +43,7 @@ __device__ __forceinline__ void grid_leave(const GridSync& g) {  // one thread, 
   if (atomicAdd(g.left, 1u) == gridDim.x - 1) {
     *g.count = 0;
     *g.left = 0;
+    *g.ticket = 0;
   }
 }
 
