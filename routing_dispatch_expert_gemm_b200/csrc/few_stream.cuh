@@ -7,9 +7,9 @@
 //   * Warps 8.. produce: the CTA's rows are cut into tiles of up to 32 weight rows and the
 //     contraction into chunks of 1 KB per row (2 or 4 KB in thin tiles, chunk_vecs); a slot of
 //     the ring holds one chunk of a tile's weight rows and of its token rows, copied with one
-//     bulk copy per row.  Slots
-//     are sized by the rows they hold, so thin tiles (a phase that leaves a CTA 7 rows)
-//     still keep the whole ring in flight; the stream does not stop between tiles or phases.
+//     bulk copy per row.  Slots are sized by the rows they hold, so thin tiles (a phase that
+//     leaves a CTA 7 rows) still keep the whole ring in flight; the stream does not stop between
+//     tiles or phases.
 //     One warp issues a bulk copy about every 28 to 45 ns, which would cap the stream at half
 //     of HBM's rate (Mixtral-shaped T=16: 890 us with one producer), so slot i belongs to
 //     producer team i mod kTeams, one lane per row; every producer follows the same
@@ -28,7 +28,8 @@
 //     fp32: FMA, a weight row per lane.
 //   * The 8 partial sums per output meet in shared memory in warp order (which slots a warp
 //     takes depends on the shape alone, so runs give the same bits); the caller's epilogue
-//     consumes a tile's total while the next tile's slots are already being consumed.
+//     consumes a tile's total while the next tile's slots are already being consumed.  Where a
+//     tile has few slots, one group takes it whole, epilogue and all (solo_tiles).
 //
 // The MMA reads whole 16-row and 8-token fragments; rows past a tile's last one are clamped
 // to it.  A garbage row or token column only reaches its own outputs, which are not stored.
