@@ -875,8 +875,10 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   const int tiles = (c.T + kShrinkTokens - 1) / kShrinkTokens, m = a.pair ? 2 : 1;
   cudaError_t e = a.pair ? set_up_gemms<true>() : set_up_gemms<false>();
   if (e != cudaSuccess) return e;
-  // (a cluster per tile: all clusters resident at once)
-  int split = gemm_split(c, a.pair, sms), clusters = 0;
+  // (a cluster per tile: all clusters resident at once).  The kernel over SM pairs reads u as bf16
+  // halves, which only the shrink of the form that is not split writes: enough pair tiles for it and
+  // few enough tiles to split can meet (one row block of W, T near 128 times the SMs).
+  int split = pairs ? 1 : gemm_split(c, a.pair, sms), clusters = 0;
   const int nt = a.pair ? kTileTokens<true> : kTileTokens<false>;
   const int64_t gemm_tiles = static_cast<int64_t>((c.d_out + BW - 1) / BW) * ((c.T + nt - 1) / nt);
   for (; split > 1; split /= 2) {

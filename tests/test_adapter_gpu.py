@@ -424,3 +424,14 @@ def test_shrink_inside_the_gemm(N, T, d_in, d_out, n, mix):
             g.replay()
             check(y, ref, live)
         assert N.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [
+    (18688, 128, 64), (18689, 128, 64), (18816, 72, 128), (18944, 256, 128), (18945, 128, 128)])
+def test_prompts_beside_a_narrow_projection(N, T, d_in, d_out):
+    """A row block or two of W and so many tokens that SM pairs run the GEMM: around the token
+    counts where as many CTAs could also split the contraction."""
+    p = make(T, d_in, d_out, 6, 16, mix="requests", seed=9)
+    for pair in (False, True):
+        check(call(N, p, pair), reference(p, pair), T)
+
