@@ -350,12 +350,14 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
         for (int i = 0; i < kChunk; ++i) {
           float bf[8];
           Vec<__nv_bfloat16>::to_f32(b[i], bf);
-          if (expand == kExpandNonFinite) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) bf[q] = isfinite(bf[q]) ? 0.f : bf[q];
-          }
           const float4* uv = reinterpret_cast<const float4*>(su + i * kMaxRank + j0);
-          const float4 w0 = uv[0], w1 = uv[1];
+          float4 w0 = uv[0], w1 = uv[1];
+          if (expand == kExpandNonFinite) {  // of the others neither factor: 0 * inf is NaN
+            float* w[8] = {&w0.x, &w0.y, &w0.z, &w0.w, &w1.x, &w1.y, &w1.z, &w1.w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (isfinite(bf[q])) bf[q] = *w[q] = 0.f;
+          }
           float s = fmaf(bf[0], w0.x, fmaf(bf[1], w0.y, fmaf(bf[2], w0.z, bf[3] * w0.w)));
           s = fmaf(bf[4], w1.x, fmaf(bf[5], w1.y, fmaf(bf[6], w1.z, fmaf(bf[7], w1.w, s))));
           if ((with >> i) & 1u) v[m][i] += s;

@@ -435,3 +435,32 @@ def test_prompts_beside_a_narrow_projection(N, T, d_in, d_out):
     for pair in (False, True):
         check(call(N, p, pair), reference(p, pair), T)
 
+
+# T, d_in, d_out: streaming, split, one CTA per tile (twice), SM pairs
+BROKEN_SHAPES = [(6, 128, 64), (90, 128, 64), (90, 64, 64), (700, 128, 5000), (1000, 128, 5000)]
+
+
+@pytest.mark.parametrize("T,d_in,d_out", BROKEN_SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_shrink_beside_a_broken_adapter(N, T, d_in, d_out, dtype):
+    """One request's A x is +inf in one rank (its outputs are +inf), another's B holds a NaN and
+    an infinity: neither knows of the other, whatever tile they share."""
+    p = make(T, d_in, d_out, 4, 16, dtype, "requests", seed=3)
+    p["ids"][T // 2], p["ids"][T // 2 + 1] = 2, 1
+    p["a"][0][2, 5, 9] = float("inf")
+    p["x"][:, 9] = 1.0
+    p["b"][0][2, :, 5] = 0.5
+    p["b"][0][1, 7, 3], p["b"][0][1, d_out - 1, 4] = float("nan"), float("inf")
+    y = call(N, p, False)
+    assert bool((y[p["ids"] == 2] == float("inf")).all())
+    broken = p["ids"] == 1
+    assert bool(torch.isnan(y[broken][:, 7]).all())
+    assert not bool(torch.isfinite(y[broken][:, d_out - 1]).any())
+    q = dict(p, a=[p["a"][0].clone()], b=[p["b"][0].clone()])
+    q["a"][0][2, 5, 9] = q["b"][0][1, 7, 3] = q["b"][0][1, d_out - 1, 4] = 0.0
+    want, bound = reference(q, False)
+    good = (y.double() - want).abs() <= bound
+    assert bool(good[(p["ids"] != 2) & ~broken].all())
+    rest = [c for c in range(d_out) if c not in (7, d_out - 1)]
+    assert bool(good[broken][:, rest].all())
+
