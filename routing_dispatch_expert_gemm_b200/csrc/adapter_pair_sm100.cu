@@ -16,8 +16,9 @@
 //              gate/up a block serves one projection; the other one's columns get zeros.
 //   warps 0-7  epilogue of one accumulator set while the next tile's MMAs fill the other: SwiGLU
 //              or addend, bf16 through a padded shared-memory slice, 64-byte row segments.
-// Token blocks that leave their adapters to the epilogue (too many of them), and the non-finite
-// elements of B, which the K blocks leave out, are added there in fp32, a token per thread.
+// Token blocks that leave their adapters to the epilogue (too many of them), and the products with
+// a non-finite element of B or u, which the K blocks leave out (times the zeros there they would be
+// NaN: in other tokens, or in the other projection), are added there in fp32, a token per thread.
 // No TMA multicast is used.
 #include <algorithm>
 
@@ -69,8 +70,8 @@ __device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Adds u_t B[c0 .. c0 + 31] of the lane's token to v; with `only_nonfinite` the products with
-// non-finite elements of B alone.
+// Adds u_t B[c0 .. c0 + 31] of the lane's token to v; with `only_nonfinite` the products with a
+// non-finite factor alone.
 __device__ __forceinline__ void expand_row(const PairParams& p, int m, int t, int id, int c0,
                                            bool only_nonfinite, float (&v)[32]) {
   if (id < 0) return;
@@ -91,7 +92,7 @@ __device__ __forceinline__ void expand_row(const PairParams& p, int m, int t, in
       Vec<__nv_bfloat16>::to_f32(ld_vec(b + static_cast<size_t>(c) * p.rank), f);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (!only_nonfinite || !isfinite(f[i])) v[c] = fmaf(f[i], h[i], v[c]);
+        if (!only_nonfinite || !isfinite(f[i]) || !isfinite(h[i])) v[c] = fmaf(f[i], h[i], v[c]);
     }
   }
 }
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // per tile of this pair that has K blocks of adapters, modulo kFlags: they met a non-finite
-  // element of B, [SM].  Only such tiles count: the ext warps may pass any number of others, but
+  // element, [SM].  Only such tiles count: the ext warps may pass any number of others, but
   // fill a block only after the last one's MMAs, which wait for the epilogue two tiles before.
   volatile int* nonfinite = abort_flag + 1;
   int* s_ids = reinterpret_cast<int*>(ctl + 512);     // the ext warps': adapters of their tokens
@@ -304,6 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
         for (int r = et >> 3; r < BN / 2; r += 8)  // this thread's own copies
           found |= zero_nonfinite(extB + r * 128 + ((j ^ (r & 7)) << 4));
+        if (id >= 0 && (q & 1) == 0)  // low halves are finite
+          for (int r = et >> 3; r < BM; r += 8)
+            if (s_ids[r] == id) found |= zero_nonfinite(extA + r * 128 + ((j ^ (r & 7)) << 4));
         fence_proxy_async_smem();  // for the tensor core
         found = !ext_all(!found);
         if (et == 0) {

@@ -282,9 +282,9 @@ struct GemmParams {
   GridSync sync;
 };
 
-// What of s B u the epilogue adds: nothing, all of it, or the products with the non-finite
-// elements of B, which the adapters' K blocks leave out (there they would reach the zeros that
-// stand for the other adapters' tokens).
+// What of s B u the epilogue adds: nothing, all of it, or the products with a non-finite factor,
+// which the adapters' K blocks leave out.  There a non-finite element of B would reach the zeros that
+// stand for the other adapters' tokens, and one of u the zero that stands for such an element.
 enum Expand { kExpandNone, kExpandAll, kExpandNonFinite };
 
 // Finishes and stores `cnt` tokens from t0 on (row c of each projection).  v[m][i]: row c of
@@ -356,7 +356,7 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
             float* w[8] = {&w0.x, &w0.y, &w0.z, &w0.w, &w1.x, &w1.y, &w1.z, &w1.w};
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              if (isfinite(bf[q])) bf[q] = *w[q] = 0.f;
+              if (isfinite(bf[q]) && isfinite(*w[q])) bf[q] = *w[q] = 0.f;
           }
           float s = fmaf(bf[0], w0.x, fmaf(bf[1], w0.y, fmaf(bf[2], w0.z, bf[3] * w0.w)));
           s = fmaf(bf[4], w1.x, fmaf(bf[5], w1.y, fmaf(bf[6], w1.z, fmaf(bf[7], w1.w, s))));
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* drain = ext_go + kMaxStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // per tile of this CTA, modulo kFlags: its K blocks of adapters met a non-finite element of B
+  // per tile of this CTA, modulo kFlags: its K blocks of adapters met a non-finite element
   // (the ext warps run at most kMaxStages tiles ahead of the epilogue's two)
   volatile int* nonfinite = abort_flag + 1;
   volatile int* ticket = nonfinite + kFlags;  // [2] FUSED: this CTA's pieces of the shrink
@@ -626,6 +626,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll 4
         for (int r = et >> 3; r < BW; r += 8)  // this thread's own copies
           found |= zero_nonfinite(dst + r * 128 + ((j ^ (r & 7)) << 4));
+        if (id >= 0 && (q & 1) == 0)  // low halves are finite
+          for (int r = et >> 3; r < rows; r += 8)
+            if (s_ids[r] == id) found |= zero_nonfinite(xdst + r * 128 + ((j ^ (r & 7)) << 4));
         fence_proxy_async_smem();  // for the tensor core
         found = !ext_all(!found);
         if (et == 0) {

@@ -464,3 +464,41 @@ def test_infinite_shrink_beside_a_broken_adapter(N, T, d_in, d_out, dtype):
     rest = [c for c in range(d_out) if c not in (7, d_out - 1)]
     assert bool(good[broken][:, rest].all())
 
+
+@pytest.mark.parametrize("side", [0, 1], ids=["gate", "up"])
+@pytest.mark.parametrize("T,d_in,d_out", BROKEN_SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_shrink_of_one_projection(N, T, d_in, d_out, dtype, side):
+    """A x of one request is +inf for the gate or for the up projection alone: h is the infinity
+    that SiLU(gate) up gives, since the other projection stays finite."""
+    p = make(T, d_in, d_out, 4, 16, dtype, "requests", seed=6)
+    p["ids"][T // 2] = 2
+    p["a"][side][2, 5, 9] = float("inf")
+    p["x"][:, 9] = 1.0
+    p["b"][side][2, :, 5] = 0.5
+    own = p["ids"] == 2
+    h = call(N, p, True)
+    other, slack = projection(p, 1 - side)  # SiLU has the sign of its argument
+    clear = other.abs() > slack
+    want = torch.where(other > 0, float("inf"), float("-inf"))
+    assert float(clear[own].double().mean()) > 0.9
+    assert bool((h.double() == want)[own[:, None] & clear].all())
+    q = dict(p, a=[a.clone() for a in p["a"]])
+    q["a"][side][2, 5, 9] = 0.0
+    want, bound = reference(q, True)
+    assert bool(((h.double() - want).abs() <= bound)[~own].all())
+
+
+@pytest.mark.parametrize("T,d_in,d_out", BROKEN_SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_shrink_meets_an_infinite_row(N, T, d_in, d_out, dtype):
+    """inf * inf and inf * -inf in the same rank are infinities, not NaNs."""
+    p = make(T, d_in, d_out, 4, 16, dtype, "requests", seed=8)
+    p["ids"][T // 2] = 2
+    p["a"][0][2, 5, 9] = float("inf")
+    p["x"][:, 9] = 1.0
+    p["b"][0][2, :, 5] = 0.5
+    p["b"][0][2, 3, 5], p["b"][0][2, 6, 5] = float("inf"), float("-inf")
+    y = call(N, p, False)[p["ids"] == 2].float()
+    assert bool((y[:, 6] == float("-inf")).all())
+    assert bool((y[:, [c for c in range(d_out) if c != 6]] == float("inf")).all())
