@@ -13,12 +13,12 @@
 //              on the token side (zeros for other adapters' tokens), B_a on the weight side.  They
 //              have a buffer of their own and are spread over the tile's K steps, so that filling
 //              one (about 1.5 us: L2 latency) hides behind the W blocks between them.  For
-//              gate/up a block serves one projection; the other one's columns get zeros.
+//              gate/up a block serves one projection: N = 128, into its columns.
 //   warps 0-7  epilogue of one accumulator set while the next tile's MMAs fill the other: SwiGLU
 //              or addend, bf16 through a padded shared-memory slice, 64-byte row segments.
 // Token blocks that leave their adapters to the epilogue (too many of them), and the products with
 // a non-finite element of B or u, which the K blocks leave out (times the zeros there they would be
-// NaN: in other tokens, or in the other projection), are added there in fp32, a token per thread.
+// NaN), are added there in fp32, a token per thread.
 // No TMA multicast is used.
 #include <algorithm>
 
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp && lane == 0 && leader) {
     // ------------------------------------------------------------ MMA issuer (leader)
-    constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, BN);
+    constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, BN), idesc_ext = idesc_bf16_f32(2 * BM, OUT);
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0, ext_phase = 0;
     bool ok = true;
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The adapters' blocks follow evenly spread ones of W.  Only a compare per K block: this
       // thread issues one every 512 cycles, and 64-bit products here cost 10 us at T=4099.
       int e = 0;
-      const int ext_step = ext > 0 ? max(1, k_blocks / (ext + 1)) : k_blocks;
+      const int ext_step = ext > 0 ? max(1, k_blocks / ext) : k_blocks;
       int ext_at = ext > 0 ? min(ext_step, k_blocks) : k_blocks;
       for (int kb = 0; kb < k_blocks && ok; ++kb) {
         if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs, p.status)) {
@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t ea = smem_desc_k_sw128(extA), eb = smem_desc_k_sw128(extB);
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma_bf16_pair(d_tmem, ea + 2 * kk, eb + 2 * kk, idesc, 1u);
+            tc_mma_bf16_pair(d_tmem + (e * M >= ext ? (M - 1) * OUT : 0), ea + 2 * kk,
+                             eb + 2 * kk, idesc_ext, 1u);
           tc_commit_pair_mc(ext_empty, 0x3);
         }
       }
@@ -284,17 +285,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = et & 7, q = (m == 0 ? e : e - n) * 8 + j;
         const int id = q < units ? __ldcg(list + 1 + q / units_per) : -1;
         const int g8 = q % units_per / 2;
-        // the weight rows of this SM: of projection m, or (gate/up) none of it
-        const bool mine = !PAIR || m == static_cast<int>(rank);
-        const int row0 = PAIR ? cb * OUT : cb * BN + static_cast<int>(rank) * (BN / 2);
+        // the weight rows of this SM: half of the tile's of projection m
+        const int row0 = cb * OUT + static_cast<int>(rank) * (OUT / 2);
         const __nv_bfloat16* b =
             (m == 0 ? p.b[0] : p.b[M - 1]) +
             static_cast<size_t>(max(id, 0)) * p.d_out * p.rank + g8 * 8;
 #pragma unroll 4
-        for (int r = et >> 3; r < BN / 2; r += 8)
+        for (int r = et >> 3; r < OUT / 2; r += 8)
           cp_async_16_zfill(extB + r * 128 + ((j ^ (r & 7)) << 4),
                             b + static_cast<size_t>(min(row0 + r, p.d_out - 1)) * p.rank,
-                            mine && id >= 0 && row0 + r < p.d_out);
+                            id >= 0 && row0 + r < p.d_out);
         const uint4* u = p.u + (static_cast<size_t>(m) * p.T * (p.rank / 8) + g8) * 2 + (q & 1);
 #pragma unroll 4
         for (int r = et >> 3; r < BM; r += 8)
@@ -303,11 +303,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             id >= 0 && s_ids[r] == id);
         cp_async_wait_all();
 #pragma unroll 4
-        for (int r = et >> 3; r < BN / 2; r += 8)  // this thread's own copies
+        for (int r = et >> 3; r < OUT / 2; r += 8)  // this thread's own copies
           found |= zero_nonfinite(extB + r * 128 + ((j ^ (r & 7)) << 4));
         if (id >= 0 && (q & 1) == 0)  // low halves are finite
+#pragma unroll 8
           for (int r = et >> 3; r < BM; r += 8)
-            if (s_ids[r] == id) found |= zero_nonfinite(extA + r * 128 + ((j ^ (r & 7)) << 4));
+            found |= zero_nonfinite(extA + r * 128 + ((j ^ (r & 7)) << 4));
         fence_proxy_async_smem();  // for the tensor core
         found = !ext_all(!found);
         if (et == 0) {

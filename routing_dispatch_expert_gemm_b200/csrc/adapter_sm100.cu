@@ -627,8 +627,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int r = et >> 3; r < BW; r += 8)  // this thread's own copies
           found |= zero_nonfinite(dst + r * 128 + ((j ^ (r & 7)) << 4));
         if (id >= 0 && (q & 1) == 0)  // low halves are finite
+#pragma unroll 4
           for (int r = et >> 3; r < rows; r += 8)
-            if (s_ids[r] == id) found |= zero_nonfinite(xdst + r * 128 + ((j ^ (r & 7)) << 4));
+            found |= zero_nonfinite(xdst + r * 128 + ((j ^ (r & 7)) << 4));
         fence_proxy_async_smem();  // for the tensor core
         found = !ext_all(!found);
         if (et == 0) {
