@@ -262,9 +262,11 @@ moe_status moe_forward(const moe_config* cfg, const void* x, const void* w_route
  *               and gates_out.
  *   capacity    as in moe_dispatch: a route past its expert's first C tokens is dropped.
  *   Masks       a logit_bias of -inf keeps an expert from being chosen while k others are
- *               left; a route chosen at a logit of -inf (or NaN, which ranks as -inf) has
- *               gate 0, and a token with no other logit has only zero gates, so its routed
- *               part is zero.
+ *               left; a route chosen at a logit of -inf has gate 0 and does not run (it still
+ *               counts in ids, demand, capacity and offsets), so the masked expert's weights
+ *               reach nobody, and a token with no other logit has only zero gates and a routed
+ *               part of zero.  A NaN logit ranks as -inf and has gate 0 too, but its route
+ *               runs: a NaN in x shows in y.
  *   y           may be x itself; must not overlap it otherwise (MOE_ERR_INVALID).
  * cfg->tiles is ignored.  MOE_ERR_UNSUPPORTED: T > 32, d or d_ff above 2^24, (E + 1) * d_ff of
  * 2^31 or more, stats, the padded layout, the reroute policy, fused steps.  MOE_ERR_INVALID

@@ -62,7 +62,7 @@ struct FewParams {
 // What every CTA knows after the top-k: touched experts in ascending order, the shared
 // expert last (index E).  H row of (expert, its s-th token): hrow + s.
 struct Tables {
-  uint32_t mask[kMaxExperts + 1];  // kept tokens of each expert
+  uint32_t mask[kMaxExperts + 1];  // tokens that each expert runs for
   uint32_t seg_mask[kMaxExperts + 1];
   int16_t seg_e[kMaxExperts + 2];
   int16_t seg_hrow[kMaxExperts + 2];
@@ -87,6 +87,10 @@ constexpr uint32_t kTableBytes = (sizeof(Tables) + 15) & ~15u;
 struct Choice {
   int32_t ids[kMaxTokens * 32];  // [T, k]
   float gates[kMaxTokens * 32];  // [T, k]
+  // Tokens that chose the expert at a logit of -inf, because fewer than k others are open.  Their
+  // gate is 0 and the route does not run (a closed expert's weights may hold anything: 0 * NaN),
+  // but demand, capacity and offsets count it.  A NaN logit ranks as -inf and runs: NaN stays NaN.
+  uint32_t closed[kMaxExperts];
 };
 static_assert(kCtlBytes + kRedFloats<4> * 4 + kTableBytes + 2 * kMaxSlotBytes <= kSmemBytes,
               "the ring holds two of the largest slots");
@@ -195,6 +199,7 @@ __device__ __forceinline__ void select_token(const FewParams& p, Tables& tb, Cho
       ch.ids[t * p.k + rank[i]] = e;
       ch.gates[t * p.k + rank[i]] = open ? ej[i] / denom : 0.f;
       atomicOr(&tb.mask[e], 1u << t);
+      if (z[i] == -INFINITY) atomicOr(&ch.closed[e], 1u << t);
     }
   }
 }
@@ -223,7 +228,10 @@ __device__ __forceinline__ void select_tokens(const FewParams& p, Tables& tb, Ch
 template <bool F32>
 __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Choice& ch, int live) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int e = tid; e <= p.E; e += kConsumers) tb.mask[e] = 0;
+  for (int e = tid; e <= p.E; e += kConsumers) {
+    tb.mask[e] = 0;
+    if (e < p.E) ch.closed[e] = 0;
+  }
   consumer_sync();
   if (p.E <= 32) select_tokens<1>(p, tb, ch, live);
   else if (p.E <= 64) select_tokens<2>(p, tb, ch, live);
@@ -237,8 +245,10 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
       if (blockIdx.x == 0 && e < p.E && p.demand_out != nullptr) p.demand_out[e] = __popc(m);
       if (p.capacity >= 0)  // arrival order is token order: the lowest C tokens stay
         while (__popc(m) > p.capacity) m &= ~(0x80000000u >> __clz(m));
+      const int kept = __popc(m);
+      if (e < p.E) m &= ~ch.closed[e];
       const int n = __popc(m), w = n > 0 ? pair_cost<F32>(n) : 0;
-      int incl = n, cincl = w;
+      int incl = kept, cincl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -246,7 +256,7 @@ __device__ __forceinline__ void build_tables(const FewParams& p, Tables& tb, Cho
         if (lane >= o) { incl += v; cincl += q; }
       }
       const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
-      const int row = rows + incl - n;
+      const int row = rows + incl - kept;  // H rows are numbered by the kept routes
       if (e < p.E) {
         tb.mask[e] = m;
         tb.row[e] = static_cast<int16_t>(row);
@@ -526,7 +536,7 @@ __global__ void __launch_bounds__(kThreads<sizeof(Tin) == 4, NT>, 1)
     };
     consume<F32, NT>(s, tiles, chunks, solo_tiles<F32, NT>(tiles[0], chunks[0]), p.status, epilogue,
                      between);
-    if (nseg == 0 && ok) {  // capacity 0 and no shared expert: only the residual is left
+    if (nseg == 0 && ok) {  // no route runs and no shared expert: only the residual is left
 #pragma unroll 1
       for (int i = tid; i < rows * live; i += kConsumers) put(i / rows, c0 + i % rows, 0.f);
     }

@@ -313,3 +313,29 @@ def test_unaligned_output_and_wide_shapes(N):
         out = call(N, cfg, p, n_tokens=T - 1, y=y)
         check(out, reference(p, out, 3, "topk_softmax", -1, True, T - 1), T - 1)
         assert bool((flat[:3] == 7.0).all()) and bool((flat[3 + T * d:] == 7.0).all())
+
+
+@pytest.mark.parametrize("T", [5, 14, 29])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shared", [False, True])
+def test_masked_experts_with_broken_weights(N, T, dtype, shared):
+    """A route at a logit of -inf is counted, but does not run: NaNs and infinities in the weights
+    of a masked expert reach nobody, also where fewer than k experts are open, or none is."""
+    inf = float("inf")
+    for bias, cap in (([-inf, -inf, 0.3, -inf, -inf, -inf], -1), ([-inf] * 6, -1),
+                      ([-inf, 0.0, -inf, 0.5, -inf, -inf], 2)):
+        p = make(T, 256, 6, 3, 128, dtype, shared, bias=bias, seed=T)
+        cfg = N.make_config(T, 256, 6, 3, 128, dtype=dtype, has_shared=shared, capacity=cap)
+        clean = call(N, cfg, p)
+        ref = reference(p, clean, 3, "topk_softmax", cap)
+        q = dict(p)
+        for name, value in (("w_gate", float("nan")), ("w_up", inf), ("w_down", float("nan"))):
+            q[name] = p[name].clone()
+            q[name][torch.tensor(bias) == -inf] = value
+        out = call(N, cfg, q)
+        check(out, ref, T)
+        for name in ("ids", "gates", "demand", "offsets", "y"):
+            assert torch.equal(out[name], clean[name]), name
+        assert out["demand"].tolist() == ref["demand"]
+        kept = [c if cap < 0 else min(c, cap) for c in ref["demand"]]
+        assert out["offsets"].tolist()[:-1] == [sum(kept[:e]) for e in range(7)]
