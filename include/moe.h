@@ -347,7 +347,8 @@ moe_status moe_forward_profiled(const moe_config* cfg, const void* x, const void
 
 /* Synchronise `stream`, copy the device status word of `ws` to *status_out (a moe_status)
  * and, if clear != 0, reset it to MOE_OK (after any error the whole header, as
- * moe_workspace_init does).  Returns MOE_ERR_CUDA if the copy fails.                    */
+ * moe_workspace_init does; on `stream`, complete on return).  Returns MOE_ERR_CUDA if the
+ * copy or the reset fails.                                                              */
 moe_status moe_get_device_status(void* ws, moe_stream_t stream, int32_t clear,
                                  int32_t* status_out);
 

@@ -497,8 +497,12 @@ moe_status moe_get_device_status(void* ws, moe_stream_t stream, int32_t clear,
   if (cudaMemcpy(&v, ws, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
   // After a timeout the header's tickets and barrier counts may stand anywhere: all start again.
   // Whatever the word says: it keeps the first error, and a timeout may have followed another.
-  const size_t bytes = v != MOE_OK ? kWsHeaderBytes : sizeof(int32_t);
-  if (clear && cudaMemset(ws, 0, bytes) != cudaSuccess) return MOE_ERR_CUDA;
+  // On `stream`, and complete on return: cleared on another stream, the counts could be zeroed under
+  // the next launch, which would wait for arrivals that were erased.
+  if (clear && v != MOE_OK) {
+    if (cudaMemsetAsync(ws, 0, kWsHeaderBytes, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return MOE_ERR_CUDA;
+  }
   *status_out = v;
   return MOE_OK;
 }

@@ -502,3 +502,37 @@ def test_infinite_shrink_meets_an_infinite_row(N, T, d_in, d_out, dtype):
     y = call(N, p, False)[p["ids"] == 2].float()
     assert bool((y[:, 6] == float("-inf")).all())
     assert bool((y[:, [c for c in range(d_out) if c != 6]] == float("inf")).all())
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [(3, 512, 256), (24, 2048, 1024), (700, 128, 5000)])
+def test_clear_then_call_on_a_side_stream(N, T, d_in, d_out):
+    """A recorded error clears the whole header, on the stream that is named and before the call
+    returns: the next launch on it finds all counts zero."""
+    p = make(T, d_in, d_out, 4, 16, seed=2)
+    want = call(N, p, False)
+    bad = dict(p, ids=p["ids"].clone())
+    bad["ids"][0] = 99
+    cfg = N.make_adapter_config(T, d_in, d_out, 4, 16)
+    ws = N.adapter_workspace(cfg)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = torch.zeros_like(want)
+
+    def run(q):
+        N.moe_adapter_linear(cfg, q["x"], q["w"][0], q["a"][0], q["b"][0], q["scale"], q["ids"],
+                             None, y, None, ws, stream=side)
+
+    for _ in range(20):
+        run(bad)
+        assert N.moe_get_device_status(ws, stream=side) == 7  # kept until it is cleared
+        assert N.moe_get_device_status(ws, stream=side, clear=True) == 7
+        run(p)
+        assert N.moe_get_device_status(ws, stream=side, clear=True) == 0
+        assert torch.equal(y, want)
+    header = ws[:256].view(torch.int32)
+    header.copy_(torch.arange(1, 65))  # as a launch that timed out may leave it
+    torch.cuda.synchronize()
+    assert N.moe_get_device_status(ws, stream=side, clear=True) == 1
+    assert not bool(header.any())
+    run(p)
+    assert N.moe_get_device_status(ws, stream=side) == 0 and torch.equal(y, want)
