@@ -297,7 +297,9 @@ typedef struct {
  * or 4 (fp32); rank <= 128; T, d_in <= 2^24; d_out <= 2^20; T * d_in, T * d_out and
  * d_in * d_out below 2^40.                                                              */
 
-/* Bytes of workspace of the two calls below; 0 for an invalid config.                     */
+/* Bytes of workspace of the two calls below; 0 for an invalid config.  They depend on T and
+ * rank alone and fall with neither: a workspace sized for the largest T and rank serves every
+ * smaller call, whatever its other sizes.                                                */
 size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg);
 
 /* y[t] = W x[t] + scale[a] B_a (A_a x[t]) (+ addend[t]),  a = adapter_ids[t].

@@ -43,6 +43,9 @@ constexpr int kShrinkWarps = 8;
 constexpr int kShrinkTokens = 16;  // MMA rows
 constexpr int kShrinkRanks = 32;   // ranks per pass: 4 MMA column blocks
 constexpr int kMaxParts = 8;         // pieces of the contraction, in the split form
+// Tokens times pieces beyond one.  A launch of its own has two CTAs per SM and at least two per 16
+// tokens, so on 148 SMs its pieces end at 148 * 16 / T anyway.
+constexpr int64_t kPartTokens = 2560;
 
 struct ShrinkParams {
   const __nv_bfloat16* x;
@@ -849,11 +852,10 @@ bool adapter_splits(const moe_adapter_config& c, bool pair) {
 }
 
 size_t adapter_u_bytes(const moe_adapter_config& c) {
-  // the split form keeps up to kMaxParts pieces; either projection count
-  const size_t one = 2 * static_cast<size_t>(c.T) * c.rank * 4;
-  const bool split = c.dtype == MOE_BF16 && (gemm_split(c, false, sm_count()) > 1 ||
-                                             gemm_split(c, true, sm_count()) > 1);
-  return split ? kMaxParts * one : one;
+  // T tokens once, or in the pieces of the split form, for either projection count.  From T and the
+  // rank alone, and never falling: one workspace serves all smaller calls, on any device.
+  const int64_t rows = std::max<int64_t>(c.T, std::min(int64_t{kMaxParts} * c.T, kPartTokens));
+  return 2 * static_cast<size_t>(rows) * c.rank * 4;
 }
 
 size_t adapter_block_table_bytes(int T) {
@@ -904,7 +906,8 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   const int turns = std::max(2, std::min(kShrinkTokens, ctas / (tiles * m)));
   const int parts = split == 1 ? 0
                                : std::max(1, std::min({kMaxParts, ctas / (tiles * m * turns),
-                                                       c.d_in / (32 * kShrinkWarps)}));
+                                                       c.d_in / (32 * kShrinkWarps),
+                                                       static_cast<int>(kPartTokens / c.T)}));
   const ShrinkParams sp{static_cast<const bf16*>(a.x),
                         {static_cast<const bf16*>(a.a[0]), static_cast<const bf16*>(a.a[1])},
                         a.scale, a.ids, a.n_tokens, u, reinterpret_cast<float*>(w + L.u), turns,

@@ -536,3 +536,20 @@ def test_clear_then_call_on_a_side_stream(N, T, d_in, d_out):
     assert not bool(header.any())
     run(p)
     assert N.moe_get_device_status(ws, stream=side) == 0 and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_workspace_of_the_largest_batch(N, dtype):
+    """A workspace sized for the largest batch and rank serves the smaller calls of a server, of
+    either projection, and nothing behind it is written."""
+    most = N.moe_adapter_workspace_bytes(N.make_adapter_config(513, 64, 64, 1, 32, dtype))
+    buf = torch.full((most + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    ws = buf[:most]
+    N.moe_workspace_init(ws)
+    for T, d_in, d_out, rank in ((513, 2048, 512, 16), (512, 2048, 512, 32), (257, 4096, 1024, 16),
+                                 (256, 4096, 1024, 32), (64, 2048, 2048, 32), (17, 16384, 256, 16),
+                                 (3, 128, 4096, 32), (1, 64, 64, 8), (480, 4096, 128, 32)):
+        p = make(T, d_in, d_out, 5, rank, dtype, seed=T)
+        for pair in (False, True):
+            check(call(N, p, pair, ws=ws), reference(p, pair), T)
+    assert bool((buf[most:] == 0x5a).all())

@@ -106,3 +106,22 @@ def test_types_of_ids_and_counts(native):
     with pytest.raises(ValueError):
         native.moe_forward_few(layer, FAKE, FAKE, None, FAKE, FAKE, FAKE, None, None, None, FAKE,
                                None, None, None, None, count, WS, 0)
+
+
+def test_a_workspace_serves_smaller_calls(native):
+    """Bytes never fall as T or the rank grows, and nothing else changes them: one workspace of
+    the largest sizes serves all calls."""
+    def size(T, rank, d_in=64, d_out=32, dtype="bf16", n=2):
+        return native.moe_adapter_workspace_bytes(
+            native.make_adapter_config(T, d_in, d_out, n, rank, dtype))
+
+    Ts = sorted({*range(1, 5200), *(1 << i for i in range(13, 25)), 18944, 18945, (1 << 24) - 1})
+    for rank in (8, 16, 128):
+        sizes = [size(T, rank) for T in Ts]
+        assert sizes == sorted(sizes) and sizes[0] > 256
+    for T in (1, 40, 256, 257, 512, 513, 2304, 2305, 20000):
+        ranks = [size(T, r) for r in range(8, 129, 8)]
+        assert ranks == sorted(ranks)
+        for d_in, d_out in ((4096, 4096), (4096, 8192), (4096, 1024), (64, 128), (16384, 8)):
+            for dtype in ("bf16", "f32"):
+                assert size(T, 16, d_in, d_out, dtype, 99) == size(T, 16)
