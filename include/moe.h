@@ -158,7 +158,7 @@ int32_t moe_capacity(int32_t T, int32_t k, int32_t E, int32_t phi_num, int32_t p
 int64_t moe_max_rows(const moe_config* cfg);
 
 /* Bytes of workspace that moe_forward needs (it keeps every intermediate there); the
- * staged calls and moe_forward_few are covered too.
+ * staged calls and moe_forward_few are covered too, and the same config with fewer tokens.
  * Returns 0 for an invalid config.                                                      */
 size_t moe_workspace_bytes(const moe_config* cfg);
 

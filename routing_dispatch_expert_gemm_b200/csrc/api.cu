@@ -330,7 +330,11 @@ int64_t moe_max_rows(const moe_config* cfg) {
 size_t moe_workspace_bytes(const moe_config* cfg) {
   if (validate(cfg) != MOE_OK) return 0;
   const size_t total = layout_of(*cfg).total;
-  return few_layer_supported(*cfg) ? std::max(total, few_layer_layout(*cfg).total) : total;
+  // moe_forward_few's part also for more tokens than it takes: with a capacity it can be the larger
+  // one, and a workspace for the largest T serves the calls of fewer tokens
+  moe_config few = *cfg;
+  few.T = std::min(few.T, kFewTokens);
+  return few_layer_supported(few) ? std::max(total, few_layer_layout(few).total) : total;
 }
 
 moe_status moe_workspace_init(void* ws, moe_stream_t stream) {

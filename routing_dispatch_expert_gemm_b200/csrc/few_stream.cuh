@@ -42,7 +42,7 @@
 namespace moe {
 namespace few {
 
-constexpr int kMaxTokens = 32;       // one token-mask word
+constexpr int kMaxTokens = kFewTokens;  // one token-mask word
 constexpr int kConsumerWarps = 8;
 constexpr int kConsumers = 32 * kConsumerWarps;
 // Warps that share a slot: more of them where token rows leave the ring few slots, which are then

@@ -189,6 +189,7 @@ struct FewArgs {
 struct FewLayout {
   size_t logits, h, total;  // byte offsets in the workspace, bytes in all
 };
+constexpr int kFewTokens = 32;
 FewLayout few_layer_layout(const moe_config& c);
 bool few_layer_supported(const moe_config& c);
 cudaError_t launch_few_layer(const moe_config& c, const FewArgs& a, void* ws, cudaStream_t s);

@@ -60,3 +60,14 @@ def test_workspace_covers_both_forwards(native):
             cfg = native.make_config(T, 256, 200, 8, 1024, **kw)
             rows = T * (8 + cfg.has_shared)
             assert native.moe_workspace_bytes(cfg) >= 256 + T * 200 * 4 + rows * 1024 * 2
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(capacity=0), dict(capacity=1, has_shared=True), dict(capacity=40),
+    dict(dtype="f32", capacity=2), dict(stats=True, capacity=3), dict(fuse="gather+combine"),
+    dict(layout="padded", capacity=8), dict(layout="padded", capacity=8, overflow="reroute")])
+def test_workspace_serves_fewer_tokens(native, kw):
+    """Bytes never fall as T grows, also from 32 tokens, the most of the few-token layer, to 33."""
+    sizes = [native.moe_workspace_bytes(native.make_config(T, 256, 200, 8, 1024, **kw))
+             for T in (*range(1, 300), 500, 1000, 4096, 4097)]
+    assert sizes == sorted(sizes) and sizes[0] > 256
