@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import sys
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
 
@@ -154,10 +155,29 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _ptr_32(t, dtype):
+    """Address of 32-bit ids, counts or factors ("int32", "float32").  They are what a caller has
+    in another type or on the host; read as if they were not, they are out of range."""
+    if isinstance(t, int):
+        if 0 <= t < 4096:  # no address: a number of tokens, say
+            raise ValueError("counts are passed to libmoe as device tensors, not as numbers")
+        return t
+    if t.dtype is not getattr(sys.modules["torch"], dtype):
+        raise ValueError(f"ids and counts passed to libmoe must be int32, factors float32: "
+                         f"{t.dtype} for {dtype}")
+    if not (t.is_cuda or t.is_pinned()):
+        raise ValueError("ids, counts and factors passed to libmoe must be in device memory")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libmoe must be contiguous")
+    return t.data_ptr()
+
+
 def _ptr_i32(t):
-    if t is not None and not isinstance(t, int) and t.element_size() != 4:
-        raise ValueError("ids and token counts passed to libmoe must be int32")
-    return _ptr(t)
+    return None if t is None else _ptr_32(t, "int32")
+
+
+def _ptr_f32(t):
+    return None if t is None else _ptr_32(t, "float32")
 
 
 def _stream(s):
@@ -271,10 +291,11 @@ def moe_forward_few(cfg, x, w_router, logit_bias, w_gate, w_up, w_down, shared_g
     with the number of leading rows of ``x`` that hold tokens, or None for all of them."""
     with _on_device(x):
         _check(lib().moe_forward_few(ctypes.byref(cfg), _ptr(x), _ptr(w_router),
-                                     _ptr(logit_bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                     _ptr_f32(logit_bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                                      _ptr(shared_gate), _ptr(shared_up), _ptr(shared_down),
-                                     _ptr(y), _ptr(ids_out), _ptr(gates_out), _ptr(demand_out),
-                                     _ptr(offsets_out), _ptr_i32(n_tokens), _ptr(ws),
+                                     _ptr(y), _ptr_i32(ids_out), _ptr_f32(gates_out),
+                                     _ptr_i32(demand_out), _ptr_i32(offsets_out),
+                                     _ptr_i32(n_tokens), _ptr(ws),
                                      _stream(stream)), "moe_forward_few")
 
 
@@ -287,8 +308,8 @@ def moe_adapter_linear(cfg, x, w, a, b, scale, adapter_ids, addend, y, n_tokens,
     see moe_adapter_linear in include/moe.h.  ``scale``, ``addend``, ``n_tokens`` may be None."""
     with _on_device(x):
         _check(lib().moe_adapter_linear(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(a), _ptr(b),
-                                        _ptr(scale), _ptr_i32(adapter_ids), _ptr(addend), _ptr(y),
-                                        _ptr_i32(n_tokens), _ptr(ws), _stream(stream)),
+                                        _ptr_f32(scale), _ptr_i32(adapter_ids), _ptr(addend),
+                                        _ptr(y), _ptr_i32(n_tokens), _ptr(ws), _stream(stream)),
                "moe_adapter_linear")
 
 
@@ -298,7 +319,7 @@ def moe_adapter_gate_up(cfg, x, w_gate, w_up, a_gate, b_gate, a_up, b_up, scale,
     with _on_device(x):
         _check(lib().moe_adapter_gate_up(ctypes.byref(cfg), _ptr(x), _ptr(w_gate), _ptr(w_up),
                                          _ptr(a_gate), _ptr(b_gate), _ptr(a_up), _ptr(b_up),
-                                         _ptr(scale), _ptr_i32(adapter_ids), _ptr(h),
+                                         _ptr_f32(scale), _ptr_i32(adapter_ids), _ptr(h),
                                          _ptr_i32(n_tokens), _ptr(ws), _stream(stream)),
                "moe_adapter_gate_up")
 

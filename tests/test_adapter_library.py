@@ -125,3 +125,45 @@ def test_a_workspace_serves_smaller_calls(native):
         for d_in, d_out in ((4096, 4096), (4096, 8192), (4096, 1024), (64, 128), (16384, 8)):
             for dtype in ("bf16", "f32"):
                 assert size(T, 16, d_in, d_out, dtype, 99) == size(T, 16)
+
+
+def test_types_and_places_of_factors_and_counts(native):
+    """32-bit values of another type, values on the host and plain numbers for a count would be
+    read as what they are not, partly behind their end."""
+    torch = pytest.importorskip("torch")
+    cfg = native.make_adapter_config(**SHAPE)
+    layer = native.make_config(8, 128, 4, 2, 128)
+
+    def lin(scale=None, ids=FAKE, n_tokens=None):
+        native.moe_adapter_linear(cfg, FAKE, FAKE, FAKE, FAKE, scale, ids, None, OUT, n_tokens,
+                                  WS + 1, 0)
+
+    def pair(scale=None, ids=FAKE, n_tokens=None):
+        native.moe_adapter_gate_up(cfg, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, scale, ids, OUT,
+                                   n_tokens, WS + 1, 0)
+
+    def few(logit_bias=None, ids_out=None, gates_out=None, demand_out=None, offsets_out=None,
+            n_tokens=None):
+        native.moe_forward_few(layer, FAKE, FAKE, logit_bias, FAKE, FAKE, FAKE, None, None, None,
+                               FAKE, ids_out, gates_out, demand_out, offsets_out, n_tokens, WS + 1,
+                               0)
+
+    i32, f32 = torch.zeros(64, dtype=torch.int32), torch.zeros(64)
+    for call in (lin, pair, few):
+        with pytest.raises(native.MoeError):  # of the workspace: the rest is well
+            call()
+        for bad in (f32, i32.long(), i32, 0, 5, True):  # i32: in pageable host memory
+            with pytest.raises(ValueError):
+                call(n_tokens=bad)
+    for call in (lin, pair):
+        for bad in (f32, i32):
+            with pytest.raises(ValueError):
+                call(ids=bad)
+        for bad in (f32.bfloat16(), f32.double(), i32, f32):
+            with pytest.raises(ValueError):
+                call(scale=bad)
+    for name, bad in (("logit_bias", f32.bfloat16()), ("gates_out", f32.bfloat16()),
+                      ("ids_out", i32.long()), ("demand_out", i32.long()),
+                      ("offsets_out", f32), ("ids_out", i32)):
+        with pytest.raises(ValueError):
+            few(**{name: bad})
