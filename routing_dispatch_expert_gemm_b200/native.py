@@ -135,6 +135,9 @@ def lib() -> ctypes.CDLL:
             "moe_status_string": (ctypes.c_char_p, [_I32]),
             "moe_abi_version": (_I32, []),
         }
+        missing = [name for name in sig if not hasattr(L, name)]
+        if missing:  # entry points are added within an ABI version
+            raise ImportError(f"{LIB_PATH} lacks {', '.join(missing)}: rebuild the library")
         for name, (res, args) in sig.items():
             f = getattr(L, name)
             f.restype, f.argtypes = res, args

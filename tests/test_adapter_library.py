@@ -167,3 +167,19 @@ def test_types_and_places_of_factors_and_counts(native):
                       ("offsets_out", f32), ("ids_out", i32)):
         with pytest.raises(ValueError):
             few(**{name: bad})
+
+
+def test_an_older_library_asks_for_a_rebuild(native, tmp_path, monkeypatch):
+    """A library of the same ABI version from before an entry point was added, and one of another
+    version: the message says what to do."""
+    import subprocess
+    older = [n for n in native.EXPORTS if n not in ("moe_forward_few", "moe_adapter_linear")]
+    for version, names, text in ((native.ABI_VERSION, older, "lacks moe_forward_few, moe_adapter"),
+                                 (native.ABI_VERSION - 1, native.EXPORTS, "ABI version")):
+        src, so = tmp_path / f"v{version}.c", tmp_path / f"v{version}.so"
+        src.write_text("".join(f"int {n}(void) {{ return {version}; }}\n" for n in names))
+        subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
+        monkeypatch.setattr(native, "_lib", None)
+        monkeypatch.setattr(native, "LIB_PATH", str(so))
+        with pytest.raises(ImportError, match=f"{text}.*rebuild"):
+            native.lib()
