@@ -7,8 +7,16 @@
 
 namespace moe {
 
-// Adapters of a token block that go through extra K blocks; with more the epilogue expands them.
-constexpr int kMaxBlockAdapters = 64;
+constexpr int kPairBlockTokens = 256;  // tokens of a token block over SM pairs, the largest
+// A token block's adapters go through extra K blocks if they have this many tokens each on average,
+// or fit into this many K blocks of 8 units (8 ranks, high or low half); else the epilogue expands
+// them.  A K block costs up to 1.5 us to fill; the last tokens of a prompt, expanded, cost T=4099
+// 28 us.
+constexpr int kAdapterTokens = 16, kSmallBlocks = 4;
+constexpr int kMaxBlockAdapters = 16;  // that the rule admits
+static_assert(kPairBlockTokens / kAdapterTokens <= kMaxBlockAdapters &&
+                  kSmallBlocks * 8 / 2 <= kMaxBlockAdapters,
+              "an adapter has two units at least");
 constexpr int kExtThreads = 64;  // threads that fill those K blocks
 
 __device__ __forceinline__ int live_tokens(const int32_t* n_tokens, int T) {
@@ -42,9 +50,8 @@ __device__ __forceinline__ bool zero_nonfinite(uint8_t* p) {
   return any;
 }
 
-// The GEMM over SM pairs: 256 tokens per token block.  u and blocks come from the shrink kernel.
+// The GEMM over SM pairs: kPairBlockTokens tokens per token block.  u and blocks come from the shrink kernel.
 bool adapter_pair_fits(const moe_adapter_config& c, bool pair);
-constexpr int kPairBlockTokens = 256;
 cudaError_t launch_adapter_pair(const moe_adapter_config& c, const AdapterArgs& a, const uint4* u,
                                 const int32_t* blocks, int32_t* status, cudaStream_t s);
 

@@ -19,8 +19,9 @@
 //       low halves of the tokens of adapter a and zeros for the others.  A block costs what 64
 //       columns of W cost; prompts of a few requests need one or two (fp32 FMA in the epilogue
 //       instead: T=4099, rank 16: 165 us; rank 32 gate/up T=1531: 560 us).
-//       Token blocks with more than kMaxBlockAdapters adapters, and the split form below, add
-//       B_a u in the epilogue, in fp32 FMA: a thread holds one row of W for 8 tokens.
+//       Token blocks with more adapters than pay this (kAdapterTokens: 16 at most), and the split
+//       form below, add B_a u in the epilogue, in fp32 FMA: a thread holds one row of W for 8
+//       tokens.
 // With enough tiles the GEMM is persistent, the epilogue of a tile overlapping the next tile's
 // MMAs (two accumulator sets).  With few tiles (a decode batch on a small projection) a cluster
 // of 2..8 CTAs splits the contraction of one tile; the partial tiles meet in distributed
@@ -62,9 +63,8 @@ struct ShrinkParams {
 };
 
 // Adapters of token block `tb`, by the whole CTA: their number, then the adapters in the order
-// of their first token; or kMaxBlockAdapters + 1 when the epilogue is to expand them: more than
-// the table holds, or fewer than 16 tokens each, unless four K blocks hold them (a K block costs
-// up to 1.5 us to fill; the last tokens of a prompt, expanded, cost T=4099 28 us).
+// of their first token; or kMaxBlockAdapters + 1 when the epilogue is to expand them (the rule
+// beside kAdapterTokens).
 __device__ __forceinline__ void list_block_adapters(const ShrinkParams& p, int tb, int live) {
   __shared__ int s_ids[32 * kShrinkWarps], s_count[kShrinkWarps];
   const int tid = threadIdx.x, t = tb * p.block_tokens + tid;
@@ -84,9 +84,9 @@ __device__ __forceinline__ void list_block_adapters(const ShrinkParams& p, int t
     all += s_count[w];
   }
   int32_t* out = p.blocks + static_cast<size_t>(tb) * (1 + kMaxBlockAdapters);
-  const bool few = all <= kMaxBlockAdapters &&
-                   (all * 16 <= min(p.block_tokens, live - tb * p.block_tokens) ||
-                    all * (p.rank / 8) * 2 <= 4 * 8);
+  const bool few =
+      all * kAdapterTokens <= min(p.block_tokens, live - tb * p.block_tokens) ||
+      all * (p.rank / 8) * 2 <= kSmallBlocks * 8;
   if (tid == 0) out[0] = few || all == 0 ? all : kMaxBlockAdapters + 1;
   if (first && before < kMaxBlockAdapters) out[1 + before] = id;
 }

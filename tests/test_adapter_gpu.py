@@ -553,3 +553,18 @@ def test_one_workspace_of_the_largest_batch(N, dtype):
         for pair in (False, True):
             check(call(N, p, pair, ws=ws), reference(p, pair), T)
     assert bool((buf[most:] == 0x5a).all())
+
+
+@pytest.mark.parametrize("used", [4, 5, 8, 15, 16, 17, 40])
+@pytest.mark.parametrize("T,d_in,d_out,rank", [
+    (300, 64, 264, 8), (300, 64, 264, 32), (1024, 72, 5000, 8), (1279, 128, 5000, 16)])
+def test_adapters_of_a_token_block(N, T, d_in, d_out, rank, used):
+    """Around the number of adapters that a token block passes through K blocks, evenly mixed and
+    with the first one on nearly all tokens; the last block is a short one."""
+    p = make(T, d_in, d_out, 64, rank, seed=used)
+    even = torch.arange(T, device="cuda") % used
+    skewed = torch.where(torch.arange(T, device="cuda") % 256 < used, even, 0)
+    for ids in (even, skewed):
+        p["ids"] = (63 - ids).to(torch.int32)
+        for pair in (False, True):
+            check(call(N, p, pair), reference(p, pair), T)
