@@ -57,7 +57,8 @@ struct ShrinkParams {
   uint4* u;         // [2, T, rank / 8]: 8 ranks as 8 high and 8 low bf16 halves (2 vectors)
   float* u_parts;   // else [parts, 2, T, rank]: fp32 sums of `parts` pieces of the contraction
   int turns, parts; // a token tile's work is dealt over turns x parts CTAs (see shrink_tile)
-  int32_t* blocks;  // [token blocks][1 + kMaxBlockAdapters]: adapters of each GEMM token block
+  int32_t* blocks;  // [token blocks][1 + kMaxBlockAdapters]: adapters of each GEMM token block,
+                    // without u_parts
   int32_t* status;
   int T, d_in, n, rank, block_tokens;
 };
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 2) adapter_shrink_kernel(co
   const int live = live_tokens(p.n_tokens, p.T);
   const int tiles = (p.T + kShrinkTokens - 1) / kShrinkTokens;
   const int tile = blockIdx.x;
-  if (tile >= tiles) {  // the CTAs behind the token tiles list the blocks' adapters
+  if (!PARTS && tile >= tiles) {  // the CTAs behind the token tiles list the blocks' adapters
     const int tb = tile - tiles;
     if (blockIdx.y == 0 && blockIdx.z == 0 && tb * p.block_tokens < live)
       list_block_adapters(p, tb, live);
@@ -920,8 +921,9 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
       return r != cudaSuccess ? r : prefer_max_shared(adapter_shrink_kernel<true>);
     });
     if (e != cudaSuccess) return e;
-    const dim3 grid(tiles + (c.T + sp.block_tokens - 1) / sp.block_tokens, turns,
-                    m * std::max(parts, 1));
+    // token tiles, then (the split form does without) the token blocks whose adapters are listed
+    const int lists = parts > 0 ? 0 : (c.T + sp.block_tokens - 1) / sp.block_tokens;
+    const dim3 grid(tiles + lists, turns, m * std::max(parts, 1));
     if (parts > 0) adapter_shrink_kernel<true><<<grid, 32 * kShrinkWarps, 0, s>>>(sp);
     else adapter_shrink_kernel<false><<<grid, 32 * kShrinkWarps, 0, s>>>(sp);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
