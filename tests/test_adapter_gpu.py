@@ -568,3 +568,21 @@ def test_adapters_of_a_token_block(N, T, d_in, d_out, rank, used):
         p["ids"] = (63 - ids).to(torch.int32)
         for pair in (False, True):
             check(call(N, p, pair), reference(p, pair), T)
+
+
+@pytest.mark.parametrize("pair", [False, True], ids=["linear", "gate_up"])
+def test_a_wait_that_runs_out(N, pair):
+    """A ticket word past the work: no CTA shrinks, and the wait for the pieces ends at its time
+    limit with MOE_ERR_TIMEOUT, y as it was.  Cleared, the workspace serves again."""
+    T, d_in, d_out = 33, 1032, 520  # the split form that shrinks by itself
+    p = make(T, d_in, d_out, 6, 16, seed=1)
+    want = call(N, p, pair)
+    cfg = N.make_adapter_config(T, d_in, d_out, 6, 16)
+    ws = N.adapter_workspace(cfg)
+    assert torch.equal(call(N, p, pair, ws=ws), want)
+    ws[200:204].view(torch.int32).fill_(1 << 20)  # zero between launches
+    y = call(N, p, pair, ws=ws, status=6)
+    assert bool((y == 7.0).all())
+    assert not bool(ws[:256].any())
+    for _ in range(3):
+        assert torch.equal(call(N, p, pair, ws=ws), want)
