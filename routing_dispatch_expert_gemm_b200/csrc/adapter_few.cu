@@ -1,5 +1,5 @@
 // A projection shared by all tokens plus each token's own low-rank adapter, for at most 32
-// tokens (moe_adapter_linear, moe_adapter_gate_up):
+// tokens, 16 in fp32 (moe_adapter_linear, moe_adapter_gate_up; adapter_streams in api.cu chooses):
 //   p[t] = W x_t + s_a B_a (A_a x_t),  a = adapter of token t (-1: none)
 //   linear   y[t] = p[t] (+ addend[t])         gate_up  h[t] = SiLU(p_gate[t]) * p_up[t]
 // Source: "Mixture-of-Experts: routing and capacity", Top-k and mixture (the shared expert,
@@ -295,7 +295,9 @@ template <typename Tin>
 cudaError_t launch_typed(const AdapterFewParams& p, bool pair, cudaStream_t s) {
   if (p.T <= 8) return pair ? launch_pair<Tin, 1, true>(p, s) : launch_pair<Tin, 1, false>(p, s);
   if (p.T <= 16) return pair ? launch_pair<Tin, 2, true>(p, s) : launch_pair<Tin, 2, false>(p, s);
-  return pair ? launch_pair<Tin, 4, true>(p, s) : launch_pair<Tin, 4, false>(p, s);
+  // (fp32 beyond 16 tokens is the CUDA-core GEMM's)
+  if constexpr (sizeof(Tin) == 4) return cudaErrorInvalidValue;
+  else return pair ? launch_pair<Tin, 4, true>(p, s) : launch_pair<Tin, 4, false>(p, s);
 }
 
 }  // namespace

@@ -1,4 +1,4 @@
-// Projections with per-token low-rank adapters in fp32, beyond the few-token kernel's range
+// Projections with per-token low-rank adapters in fp32, where the few-token kernel does not run
 // (moe_adapter_linear, moe_adapter_gate_up):
 //   p[t] = W x_t + s_a B_a (A_a x_t);  y[t] = p[t] (+ addend[t])  or  SiLU(p_gate) * p_up
 // CUDA cores, as the fp32 expert FFN: tf32 cannot meet its tolerance.  Two launches:

@@ -1,5 +1,5 @@
 // Projections with per-token low-rank adapters for larger batches (bf16, moe_adapter_linear and
-// moe_adapter_gate_up beyond the few-token kernel's range):
+// moe_adapter_gate_up where the few-token kernel does not run):
 //   p[t] = W x_t + s_a B_a (A_a x_t),  a = adapter of token t (-1: none)
 //   linear   y[t] = p[t] (+ addend[t])         gate_up  h[t] = SiLU(p_gate[t]) * p_up[t]
 //

@@ -169,21 +169,42 @@ moe_status validate_adapter(const moe_adapter_config* c) {
   return MOE_OK;
 }
 
-// Whether the streaming kernel runs a call of at most 32 tokens.  It reads the token rows once per
-// CTA, so more than 8 tokens beside a large W are better off on tcgen05, and up to 8 a large pair whose
-// GEMM splits the contraction and shrinks in the same launch.  Measured, rank 16, us
-// streaming / tcgen05:
-//   linear  2048x2048 T=16 13 / 15, T=32 18 / 16;  1024x8192 T=16 16 / 16, T=24 20 / 17;
-//   linear  4096x4096 T=8 15 / 18, T=16 21 / 18;  14336x4096 T=8 31 / 31, T=12 43 / 31;
-//   linear  8192x28672 T=8 91 / 108, T=12 112 / 99;
-//   gate/up 4096x4096 T=8 23 / 25, T=12 28 / 25;  4096x8192 T=4 35 / 34, T=8 40 / 35;
-//   gate/up 4096x14336 (not split) T=8 61 / 69, T=12 70 / 53.
+// Whether the streaming kernel runs a call of at most 32 tokens.  Measured, us streaming / other
+// kernel (W from HBM, 16 adapters in use).
+//   bf16: it reads the token rows once per CTA, so more than 8 tokens beside a large W are better off
+// on tcgen05, and up to 8 a large pair whose GEMM splits the contraction and shrinks in the same
+// launch; but tcgen05's shrink and expansion grow with the rank, which costs streaming little.
+//   rank 16   linear 2048x2048 T=16 12 / 15, T=24 15 / 15, T=32 16 / 15; 4096x2048 T=12 14 / 16, T=16
+//             17 / 16; 4096x4096 T=8 15 / 18, T=16 21 / 18; 14336x4096 T=8 31 / 31, T=12 43 / 31;
+//             8192x28672 T=8 91 / 108, T=12 112 / 99; gate/up 2048x2816 T=16 18 / 19, 4096x4096
+//             T=8 23 / 25, T=12 28 / 25, 4096x8192 T=4 35 / 34, T=8 40 / 35, 4096x14336 (not split)
+//             T=8 61 / 69, T=12 70 / 53
+//   rank 32   linear 4096x4096 T=16 19 / 19, T=24 25 / 20, 4096x8192 T=12 27 / 24; gate/up 4096x8192
+//             T=8 40 / 40, T=12 46 / 40
+//   rank 64   linear 4096x4096 T=16 22 / 30, T=32 32 / 34, 4096x8192 T=16 34 / 37, T=24 45 / 42,
+//             14336x4096 T=12 51 / 47; gate/up 4096x8192 T=8 46 / 58
+//   rank 128  linear 4096x4096 T=16 25 / 46, T=32 37 / 54, 14336x4096 T=16 57 / 74, T=32 91 / 91,
+//             8192x28672 T=8 128 / 178; gate/up 4096x8192 T=24 105 / 127
+//   fp32: the streaming loop loads a token's vector again for each row of W, the other kernel holds 4
+// tokens by 4 rows, but its warp goes through all of d_in alone, in as many rounds as its tiles take,
+// and beyond 4096 rows of W it is the one with 64-token tiles.
+//   linear    512x512 T=1 10 / 4; 1024x1024 T=8 11 / 10, T=16 23 / 10; 2048x1024 T=8 13 / 16, T=9
+//             21 / 14; 2048x2048 T=4 14 / 16, T=8 16 / 17, T=16 32 / 18; 2048x4096 T=8 24 / 18;
+//             4096x1024 T=8 18 / 30, T=16 52 / 29; 4096x4096 T=4 29 / 32, T=8 40 / 33, T=12
+//             57 / 60, T=16 73 / 61; 8192x8192 T=16 222 / 360, T=32 554 / 363
+//   gate/up   1024x1024 T=1 11 / 12, T=8 13 / 13, T=16 23 / 13; 2048x2048 T=4 20 / 21, T=8 25 / 22,
+//             T=9 33 / 38, T=16 44 / 40; 4096x4096 T=8 67 / 77, T=16 123 / 142, T=32 290 / 250
 bool adapter_streams(const moe_adapter_config& c, bool pair) {
   if (c.T > 32) return false;
-  if (c.T <= 4 || c.dtype == MOE_F32) return true;
-  const int64_t weights = static_cast<int64_t>(c.d_in) * c.d_out * (pair ? 2 : 1);
-  if (c.T <= 8) return weights <= (int64_t{60} << 20) || !adapter_splits(c, pair);
-  return weights <= (int64_t{c.T <= 16 ? 12 : 6} << 20);
+  const int64_t rows = static_cast<int64_t>(c.d_out) * (pair ? 2 : 1), weights = rows * c.d_in;
+  if (c.dtype == MOE_F32) {
+    if (rows > 4096) return c.T <= 16;
+    return c.T <= 8 && c.d_in > 1024 && (c.T <= 4 || c.d_in > c.d_out);
+  }
+  if (c.T <= 4) return true;
+  if (c.T <= 8 && (c.rank > 16 || !adapter_splits(c, pair))) return true;
+  const int mi = c.T <= 8 ? 60 : c.T <= 16 ? 12 : 6;  // Mi weights, at rank 16
+  return weights <= (int64_t{mi} << 20) * std::max(c.rank, 16) / 16 * (c.rank > 64 ? 2 : 1);
 }
 
 AdapterLayout adapter_layout(const moe_adapter_config& c) {

@@ -223,7 +223,7 @@ bool adapter_splits(const moe_adapter_config& c, bool pair);
 // fp32, any T: shrink launch + CUDA-core GEMM.
 cudaError_t launch_adapter_simt(const moe_adapter_config& c, const AdapterArgs& a,
                                 const AdapterLayout& L, void* ws, cudaStream_t s);
-// At most 32 tokens, either type, one launch.
+// At most 32 tokens in bf16, 16 in fp32, one launch.
 cudaError_t launch_adapter_few(const moe_adapter_config& c, const AdapterArgs& a,
                                const AdapterLayout& L, void* ws, cudaStream_t s);
 

@@ -586,3 +586,25 @@ def test_a_wait_that_runs_out(N, pair):
     assert not bool(ws[:256].any())
     for _ in range(3):
         assert torch.equal(call(N, p, pair, ws=ws), want)
+
+
+@pytest.mark.parametrize("pair", [False, True], ids=["linear", "gate_up"])
+@pytest.mark.parametrize("case", [
+    (1, 1028, 132, 3, 12, "f32", None), (3, 2052, 516, 40, 20, "f32", None),
+    (4, 1024, 2048, 4, 128, "f32", 3), (5, 1540, 260, 3, 8, "f32", None),
+    (8, 2052, 1028, 9, 64, "f32", 7), (8, 1028, 1032, 9, 16, "f32", None),
+    (9, 1540, 260, 5, 8, "f32", None), (2, 132, 4100, 2, 4, "f32", None),
+    (16, 516, 4360, 16, 36, "f32", None), (11, 72, 5000, 40, 128, "f32", 10),
+    (17, 516, 4360, 5, 8, "f32", 16), (32, 8, 4100, 5, 8, "f32", None),
+    (8, 4096, 8200, 16, 16, "bf16", None), (8, 4096, 8200, 16, 32, "bf16", None),
+    (16, 4096, 4104, 16, 128, "bf16", None), (32, 4096, 2056, 16, 128, "bf16", 31),
+    (32, 4096, 2056, 16, 64, "bf16", None), (16, 8, 4096, 4, 32, "bf16", None),
+    (40, 8, 136, 4, 8, "bf16", None), (70, 56, 5000, 9, 48, "bf16", 65),
+    (300, 16, 5000, 9, 48, "bf16", None), (1024, 8, 5000, 3, 16, "bf16", None)],
+    ids=lambda c: "-".join(str(v) for v in c[:6]))
+def test_where_the_kernels_change(N, case, pair):
+    """On both sides of the sizes, types and ranks that decide between the kernels, and
+    contractions shorter than a K block."""
+    T, d_in, d_out, n, rank, dtype, live = case
+    p = make(T, d_in, d_out, n, rank, dtype, seed=T + rank)
+    check(call(N, p, pair, n_tokens=live), reference(p, pair), T if live is None else live)
