@@ -23,6 +23,13 @@ __device__ __forceinline__ int live_tokens(const int32_t* n_tokens, int T) {
   return n_tokens != nullptr ? min(max(__ldg(n_tokens), 0), T) : T;
 }
 
+// Whether u of token t, whose adapter is `id`, is not finite for one of M projections.
+template <int M>
+__device__ __forceinline__ bool broken_token(const uint8_t* broken, int T, int t, int id) {
+  uint32_t b = __ldcg(broken + t);
+  if (M == 2) b |= __ldcg(broken + T + t);
+  return id >= 0 && b != 0;
+}
 // Barrier of the ext warps; whether `v` held on all of their threads.
 __device__ __forceinline__ bool ext_all(bool v) {
   uint32_t r;
@@ -53,6 +60,7 @@ __device__ __forceinline__ bool zero_nonfinite(uint8_t* p) {
 // The GEMM over SM pairs: kPairBlockTokens tokens per token block.  u and blocks come from the shrink kernel.
 bool adapter_pair_fits(const moe_adapter_config& c, bool pair);
 cudaError_t launch_adapter_pair(const moe_adapter_config& c, const AdapterArgs& a, const uint4* u,
-                                const int32_t* blocks, int32_t* status, cudaStream_t s);
+                                const int32_t* blocks, const uint8_t* broken, int32_t* status,
+                                cudaStream_t s);
 
 }  // namespace moe

@@ -55,6 +55,7 @@ struct PairParams {
   const __nv_bfloat16* b[2];
   const uint4* u;
   const int32_t* blocks;
+  const uint8_t* broken;
   const int32_t* ids;
   const __nv_bfloat16* addend;
   __nv_bfloat16* y;
@@ -274,8 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int units = __ldcg(list) * units_per;
       const int t0 = tb * 2 * BM + static_cast<int>(rank) * BM;
       bool found = false;
-      for (int i = et; i < BM; i += kExtThreads)  // the last block's barrier has passed
-        s_ids[i] = t0 + i < live ? __ldg(p.ids + t0 + i) : -1;
+      bool broken = false;
+      for (int i = et; i < BM; i += kExtThreads) {  // the last block's barrier has passed
+        const int id = t0 + i < live ? __ldg(p.ids + t0 + i) : -1;
+        s_ids[i] = id;
+        if (t0 + i < live) broken |= broken_token<M>(p.broken, p.T, t0 + i, id);
+      }
+      broken = !ext_all(!broken);
       for (int e = 0; e < M * n; ++e, ++uses) {
         const int m = e >= n ? 1 : 0;
         ok = ext_all(uses == 0 || mbar_wait_bounded(ext_empty, (uses - 1) & 1u, abort_flag,
@@ -305,8 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
         for (int r = et >> 3; r < OUT / 2; r += 8)  // this thread's own copies
           found |= zero_nonfinite(extB + r * 128 + ((j ^ (r & 7)) << 4));
-        if (id >= 0 && (q & 1) == 0)  // low halves are finite
-#pragma unroll 8
+        if (broken && id >= 0)
           for (int r = et >> 3; r < BM; r += 8)
             found |= zero_nonfinite(extA + r * 128 + ((j ^ (r & 7)) << 4));
         fence_proxy_async_smem();  // for the tensor core
@@ -458,7 +463,8 @@ bool adapter_pair_fits(const moe_adapter_config& c, bool pair) {
 }
 
 cudaError_t launch_adapter_pair(const moe_adapter_config& c, const AdapterArgs& a, const uint4* u,
-                                const int32_t* blocks, int32_t* status, cudaStream_t s) {
+                                const int32_t* blocks, const uint8_t* broken, int32_t* status,
+                                cudaStream_t s) {
   using bf16 = __nv_bfloat16;
   PairMaps maps;
   bool ok = encode_2d_box(&maps.x, a.x, c.d_in, c.T, BM) &&
@@ -467,7 +473,8 @@ cudaError_t launch_adapter_pair(const moe_adapter_config& c, const AdapterArgs& 
   else maps.w[1] = maps.w[0];
   if (!ok) return cudaErrorInvalidValue;
   const PairParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u,
-                     blocks, a.ids, static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y),
+                     blocks, broken, a.ids, static_cast<const bf16*>(a.addend),
+                     static_cast<bf16*>(a.y),
                      a.n_tokens, status, c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0,
                      (reinterpret_cast<uintptr_t>(a.y) & 15) == 0,
                      (reinterpret_cast<uintptr_t>(a.addend) & 15) == 0};

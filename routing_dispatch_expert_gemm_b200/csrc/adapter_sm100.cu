@@ -59,6 +59,7 @@ struct ShrinkParams {
   int turns, parts; // a token tile's work is dealt over turns x parts CTAs (see shrink_tile)
   int32_t* blocks;  // [token blocks][1 + kMaxBlockAdapters]: adapters of each GEMM token block,
                     // without u_parts
+  uint8_t* broken;  // [2, T], with u: of tokens that have an adapter, whether a half is not finite
   int32_t* status;
   int T, d_in, n, rank, block_tokens;
 };
@@ -174,6 +175,8 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, ShrinkSums& r
     const __nv_bfloat16* A =  // (an index into p.a would put p on the stack)
         (m == 0 ? p.a[0] : p.a[1]) + static_cast<size_t>(a_id) * p.rank * p.d_in;
     const float sc = p.scale != nullptr ? __ldg(p.scale + a_id) : 1.f;
+    const int t = threadIdx.x / (kShrinkRanks / 2);  // this thread's token of the sums
+    bool broken = false;
     for (int j0 = 0; j0 < p.rank; j0 += kShrinkRanks) {
       const int nb = min(4, (p.rank - j0) / 8);  // rank is a multiple of 8
       const __nv_bfloat16* ar = A + static_cast<size_t>(j0 + g) * p.d_in;
@@ -191,7 +194,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, ShrinkSums& r
       }
       shrink_sync();
       // a thread: two neighbouring ranks of a token
-      const int t = threadIdx.x / (kShrinkRanks / 2), j = threadIdx.x % (kShrinkRanks / 2) * 2;
+      const int j = threadIdx.x % (kShrinkRanks / 2) * 2;
       if (((tokens >> t) & 1u) && j0 + j < p.rank) {
         float v[2] = {0.f, 0.f};
 #pragma unroll
@@ -211,6 +214,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, ShrinkSums& r
           const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
           const uint32_t lo = gemm::pack_bf16(isfinite(h0) ? v[0] - h0 : 0.f,
                                               isfinite(h1) ? v[1] - h1 : 0.f);
+          broken |= !isfinite(h0) || !isfinite(h1);
           uint32_t* u = reinterpret_cast<uint32_t*>(
               p.u + ((static_cast<size_t>(m) * p.T + t0 + t) * p.rank + j0) / 4) + (j / 8) * 8 +
               (j % 8) / 2;
@@ -219,6 +223,11 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, ShrinkSums& r
         }
       }
       shrink_sync();
+    }
+    if constexpr (!PARTS) {  // a half warp holds a token
+      const uint32_t any = __ballot_sync(0xffffffffu, broken) >> (lane & 16);
+      if ((lane & 15) == 0 && ((tokens >> t) & 1u))
+        p.broken[static_cast<size_t>(m) * p.T + t0 + t] = (any & 0xffffu) != 0;
     }
   }
 }
@@ -275,6 +284,7 @@ struct GemmParams {
   const float* u_parts;  // with `parts` > 0 instead of u
   int parts;
   const int32_t* blocks;
+  const uint8_t* broken;
   const int32_t* ids;
   const __nv_bfloat16* addend;
   __nv_bfloat16* y;
@@ -339,6 +349,24 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
         for (int i = 0; i < 8; ++i) o[i] = h[i] + l[i];
       }
       __syncwarp();
+      if (expand == kExpandNonFinite) {  // rare, and rolled: see kChunk
+#pragma unroll 1
+        for (int i = 0; i < cnt; ++i) {
+          if (!((with >> i) & 1u)) continue;
+          const int e = __shfl_sync(0xffffffffu, id, i);
+          const __nv_bfloat16* b = p.b[m] + (static_cast<size_t>(e) * p.d_out + row) * p.rank;
+          float s = 0.f;
+#pragma unroll 1
+          for (int j = 0; j < p.rank; ++j) {
+            const float f = __bfloat162float(b[j]), w = su[i * kMaxRank + j];
+            if (!isfinite(f) || !isfinite(w)) s = fmaf(f, w, s);
+          }
+#pragma unroll
+          for (int q = 0; q < kChunk; ++q)
+            if (q == i) v[m][q] += s;
+        }
+        continue;
+      }
       const __nv_bfloat16* brow[kChunk];
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) {
@@ -355,13 +383,7 @@ __device__ __forceinline__ void finish_tokens(const GemmParams& p, float (&v)[PA
           float bf[8];
           Vec<__nv_bfloat16>::to_f32(b[i], bf);
           const float4* uv = reinterpret_cast<const float4*>(su + i * kMaxRank + j0);
-          float4 w0 = uv[0], w1 = uv[1];
-          if (expand == kExpandNonFinite) {  // of the others neither factor: 0 * inf is NaN
-            float* w[8] = {&w0.x, &w0.y, &w0.z, &w0.w, &w1.x, &w1.y, &w1.z, &w1.w};
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (isfinite(bf[q]) && isfinite(*w[q])) bf[q] = *w[q] = 0.f;
-          }
+          const float4 w0 = uv[0], w1 = uv[1];
           float s = fmaf(bf[0], w0.x, fmaf(bf[1], w0.y, fmaf(bf[2], w0.z, bf[3] * w0.w)));
           s = fmaf(bf[4], w1.x, fmaf(bf[5], w1.y, fmaf(bf[6], w1.z, fmaf(bf[7], w1.w, s))));
           if ((with >> i) & 1u) v[m][i] += s;
@@ -595,8 +617,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int units = __ldcg(list) * units_per;
       const int ntok = min(NT, live - tb * NT), rows = (ntok + 15) / 16 * 16;
       // the barrier at the end of the last block has passed: the table is free
-      for (int i = et; i < rows; i += kExtThreads)
-        s_ids[i] = i < ntok ? __ldg(p.ids + tb * NT + i) : -1;
+      bool broken = false;
+      for (int i = et; i < rows; i += kExtThreads) {
+        const int id = i < ntok ? __ldg(p.ids + tb * NT + i) : -1;
+        s_ids[i] = id;
+        if (i < ntok) broken |= broken_token<M>(p.broken, p.T, tb * NT + i, id);
+      }
+      broken = !ext_all(!broken);
       for (int e = 0; e < M * n; ++e) {
         const int m = e >= n ? 1 : 0;
         ok = ext_all(mbar_wait_bounded(&ext_go[stage], (go_phase >> stage) & 1u, abort_flag,
@@ -630,8 +657,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll 4
         for (int r = et >> 3; r < BW; r += 8)  // this thread's own copies
           found |= zero_nonfinite(dst + r * 128 + ((j ^ (r & 7)) << 4));
-        if (id >= 0 && (q & 1) == 0)  // low halves are finite
-#pragma unroll 4
+        if (broken && id >= 0)
           for (int r = et >> 3; r < rows; r += 8)
             found |= zero_nonfinite(xdst + r * 128 + ((j ^ (r & 7)) << 4));
         fence_proxy_async_smem();  // for the tensor core
@@ -870,6 +896,7 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint4* u = reinterpret_cast<uint4*>(w + L.u);
   int32_t* blocks = reinterpret_cast<int32_t*>(w + L.blocks);
+  uint8_t* broken = w + L.broken;
   int32_t* status = reinterpret_cast<int32_t*>(w);
   unsigned int* sync = reinterpret_cast<unsigned int*>(w + kWsGridSyncOffset);
   GemmMaps maps;
@@ -912,7 +939,7 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
   const ShrinkParams sp{static_cast<const bf16*>(a.x),
                         {static_cast<const bf16*>(a.a[0]), static_cast<const bf16*>(a.a[1])},
                         a.scale, a.ids, a.n_tokens, u, reinterpret_cast<float*>(w + L.u), turns,
-                        parts, blocks, status, c.T, c.d_in, c.n_adapters, c.rank,
+                        parts, blocks, broken, status, c.T, c.d_in, c.n_adapters, c.rank,
                         pairs ? kPairBlockTokens : nt};
   if (!fused) {
     static DeviceOnce once;
@@ -929,9 +956,9 @@ cudaError_t launch_adapter_sm100(const moe_adapter_config& c, const AdapterArgs&
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
 
-  if (pairs) return launch_adapter_pair(c, a, u, blocks, status, s);
+  if (pairs) return launch_adapter_pair(c, a, u, blocks, broken, status, s);
   GemmParams p{{static_cast<const bf16*>(a.b[0]), static_cast<const bf16*>(a.b[1])}, u,
-               reinterpret_cast<const float*>(w + L.u), parts, blocks, a.ids,
+               reinterpret_cast<const float*>(w + L.u), parts, blocks, broken, a.ids,
                static_cast<const bf16*>(a.addend), static_cast<bf16*>(a.y), a.n_tokens, status,
                c.T, c.d_in, c.d_out, c.n_adapters, c.rank, 0, 0, 0, 0, split, sp,
                GridSync{sync, sync + 1, sync + 2}};

@@ -211,7 +211,8 @@ AdapterLayout adapter_layout(const moe_adapter_config& c) {
   AdapterLayout L{};
   L.u = kWsHeaderBytes;
   L.blocks = align256(L.u + adapter_u_bytes(c));
-  L.total = align256(L.blocks + adapter_block_table_bytes(c.T));
+  L.broken = align256(L.blocks + adapter_block_table_bytes(c.T));
+  L.total = align256(L.broken + 2 * static_cast<size_t>(c.T));
   return L;
 }
 

@@ -210,6 +210,7 @@ struct AdapterArgs {
 struct AdapterLayout {
   size_t u;       // byte offset of u: [2, T, rank], 4 bytes each (or several such pieces)
   size_t blocks;  // of the adapters per GEMM token block (adapter_sm100.cu)
+  size_t broken;  // of [2, T] bytes: u of the token is not finite (adapter_sm100.cu)
   size_t total;   // bytes in all
 };
 // bf16, any T: tcgen05 GEMM, the shrink in a launch before it or in the same.

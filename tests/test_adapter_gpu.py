@@ -608,3 +608,22 @@ def test_where_the_kernels_change(N, case, pair):
     T, d_in, d_out, n, rank, dtype, live = case
     p = make(T, d_in, d_out, n, rank, dtype, seed=T + rank)
     check(call(N, p, pair, n_tokens=live), reference(p, pair), T if live is None else live)
+
+
+@pytest.mark.parametrize("pair", [False, True], ids=["linear", "gate_up"])
+@pytest.mark.parametrize("T,d_in,d_out,n", [(90, 64, 64, 4), (700, 128, 5000, 16), (1000, 128, 5000, 16)])
+def test_nothing_of_a_broken_call_stays(N, T, d_in, d_out, n, pair):
+    """A call with a broken request, then clean ones on the same workspace: the bits of a fresh
+    one, also where requests without an adapter came between."""
+    p = make(T, d_in, d_out, n, 16, seed=4)
+    want = call(N, p, pair)
+    ws = N.adapter_workspace(N.make_adapter_config(T, d_in, d_out, n, 16))
+    q = dict(p, x=p["x"].clone(), b=[b.clone() for b in p["b"]])
+    q["x"][::3, 1] = float("inf")
+    q["b"][0][1, 3, 4] = float("nan")
+    gone = dict(p, ids=torch.full_like(p["ids"], -1))
+    for before in (q, gone, q):
+        call(N, before, pair, ws=ws)
+        assert torch.equal(call(N, p, pair, ws=ws), want)
+        live = T // 2
+        check(call(N, p, pair, n_tokens=live, ws=ws), reference(p, pair), live)
