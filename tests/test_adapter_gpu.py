@@ -627,3 +627,42 @@ def test_nothing_of_a_broken_call_stays(N, T, d_in, d_out, n, pair):
         assert torch.equal(call(N, p, pair, ws=ws), want)
         live = T // 2
         check(call(N, p, pair, n_tokens=live, ws=ws), reference(p, pair), live)
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 5), ("bf16", 64), ("bf16", 200), ("bf16", 1200),
+                                     ("f32", 4), ("f32", 16), ("f32", 200)])
+def test_adapters_past_32_bit_offsets(N, dtype, T):
+    """More than 2^31 elements in A and in B: the first and the last adapter in use."""
+    d, d_out, rank, n = 2056, 4104, 128, 8192
+    g = torch.Generator(device="cuda").manual_seed(T)
+    p = make(T, d, d_out, 2, rank, dtype, seed=T)
+    big = dict(p, scale=torch.ones(n, device="cuda"))
+    ids = torch.randint(-1, 2, (T,), generator=g, device="cuda").to(torch.int32)
+    ids[-1] = 1
+    a = torch.empty((n, rank, d), dtype=DT[dtype], device="cuda")
+    b = torch.empty((n, d_out, rank), dtype=DT[dtype], device="cuda")
+    assert a.numel() > 2 ** 31 and b.numel() > 2 ** 31
+    for big_m, small_m in ((a, p["a"]), (b, p["b"])):
+        big_m[0], big_m[n - 1] = small_m[0][0], small_m[0][1]
+    big["a"], big["b"] = [a, a], [b, b]
+    big["scale"][0], big["scale"][n - 1] = p["scale"][0], p["scale"][1]
+    big["ids"] = torch.where(ids == 1, n - 1, ids).to(torch.int32)
+    p["ids"], p["a"], p["b"] = ids, [p["a"][0]] * 2, [p["b"][0]] * 2
+    for pair in (False, True):
+        check(call(N, big, pair), reference(p, pair), T)
+
+
+@pytest.mark.parametrize("dtype,pair", [("bf16", False), ("bf16", True), ("f32", False),
+                                        ("f32", True)])
+def test_outputs_past_32_bit_offsets(N, dtype, pair):
+    """More than 2^31 outputs: the rows at the beginning, around 2^31 elements and at the end."""
+    T, d_in, d_out = 262400, 64, 8200
+    p = make(T, d_in, d_out, 3, 16, dtype, "requests", seed=1)
+    y = torch.full((T, d_out), 7.0, dtype=DT[dtype], device="cuda")
+    call(N, p, pair, not pair, T - 3, y=y)
+    middle = 2 ** 31 // d_out
+    rows = torch.cat([torch.arange(0, 300), torch.arange(middle - 150, middle + 150),
+                      torch.arange(T - 300, T - 3)]).cuda()
+    q = dict(p, x=p["x"][rows], ids=p["ids"][rows], addend=p["addend"][rows])
+    check(y[rows], reference(q, pair, not pair), len(rows))
+    assert bool((y[T - 3:] == 7.0).all())
