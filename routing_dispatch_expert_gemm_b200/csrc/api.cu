@@ -353,9 +353,14 @@ size_t moe_workspace_bytes(const moe_config* cfg) {
   if (validate(cfg) != MOE_OK) return 0;
   const size_t total = layout_of(*cfg).total;
   // moe_forward_few's part also for more tokens than it takes: with a capacity it can be the larger
-  // one, and a workspace for the largest T serves the calls of fewer tokens
+  // one, and a workspace for the largest T serves the calls of fewer tokens.  And whatever the
+  // options that it does not take: an option only adds bytes.
   moe_config few = *cfg;
   few.T = std::min(few.T, kFewTokens);
+  few.stats = 0;
+  few.layout = MOE_LAYOUT_RAGGED;
+  few.overflow = MOE_OVERFLOW_DROP;
+  few.fuse = MOE_FUSE_NONE;
   return few_layer_supported(few) ? std::max(total, few_layer_layout(few).total) : total;
 }
 

@@ -71,3 +71,15 @@ def test_workspace_serves_fewer_tokens(native, kw):
     sizes = [native.moe_workspace_bytes(native.make_config(T, 256, 200, 8, 1024, **kw))
              for T in (*range(1, 300), 500, 1000, 4096, 4097)]
     assert sizes == sorted(sizes) and sizes[0] > 256
+
+
+@pytest.mark.parametrize("T", [1, 7, 32, 33, 129])
+@pytest.mark.parametrize("capacity", [0, 1, 17])
+def test_an_option_only_adds_bytes(native, T, capacity):
+    """Also where the few-token layer, which does not take the option, has the larger part."""
+    shape = (T, 256, 200, 10, 1024)
+    base = native.moe_workspace_bytes(native.make_config(*shape, capacity=capacity))
+    for kw in (dict(stats=True), dict(layout="padded"), dict(layout="padded", overflow="reroute"),
+               dict(fuse="gather"), dict(fuse="combine"), dict(has_shared=True)):
+        cfg = native.make_config(*shape, capacity=capacity, **kw)
+        assert native.moe_workspace_bytes(cfg) >= base, kw
